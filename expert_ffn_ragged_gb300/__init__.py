@@ -19,6 +19,8 @@ Functions (same names as the C ABI, without the ``rd_`` prefix):
 * ``unsort_bwd_rows(g, y, w, limit=None)``                -> (grad [rows, hidden], dot [rows])
 * ``set_tuning(...)``, ``get_tuning()``, ``tuning(...)``  -> the process-wide launch overrides
 * ``status_bits(status)``, ``check_status(status)``       -> read a status word (names, or raise)
+* routing, sorting, dispatch / combine and the 4-bit products (``include/rd_moe.h``): the functions
+  of ``expert_ffn_ragged_gb300.moe``, importable from here
 
 Every tensor of a call must sit on one CUDA device; the call runs on that
 device's current stream (or ``stream``).  A ``status`` word (a one-element
@@ -38,6 +40,10 @@ __all__ = [
     "STATUS_NEG_SIZE", "STATUS_OVERFLOW", "STATUS_TIMEOUT", "MAX_GROUPS",
     "VARIANT_AUTO", "VARIANT_SINGLE", "VARIANT_PAIR", "set_tuning", "get_tuning", "tuning",
     "status_bits", "check_status",
+    "route", "route_bwd", "sort_rows", "dispatch_rows", "combine_rows", "combine_rows_bwd",
+    "mxfp4_scale_width", "mxfp4_quantize", "mxfp4_quantize_weights", "mxfp4_dequantize",
+    "ragged_dot_mxfp4", "Routing", "Mxfp4", "SCORE_SOFTMAX", "SCORE_SIGMOID", "MAX_TOPK",
+    "MAX_EXPERT_GROUPS", "EPI_SILU_GLU_MXFP4",
 ]
 
 EPI_NONE = 0
@@ -106,6 +112,7 @@ def load():
     lib.rd_get_tuning.restype = ctypes.c_int
     lib.rd_status_string.argtypes = [ctypes.c_int]
     lib.rd_status_string.restype = ctypes.c_char_p
+    moe.declare(lib)
     _lib = lib
     return lib
 
@@ -583,3 +590,10 @@ def unsort_bwd_rows(g, y, w, limit=None, grad=None, dot=None, stream=None):
                                       hidden, _ptr(limit), _stream(stream, dev))
     _check(code, "rd_unsort_bwd_rows")
     return grad, dot
+
+
+from . import moe  # noqa: E402  (its functions use the helpers above)
+from .moe import (  # noqa: E402
+    EPI_SILU_GLU_MXFP4, MAX_EXPERT_GROUPS, MAX_TOPK, SCORE_SIGMOID, SCORE_SOFTMAX, Mxfp4, Routing,
+    combine_rows, combine_rows_bwd, dispatch_rows, mxfp4_dequantize, mxfp4_quantize,
+    mxfp4_quantize_weights, mxfp4_scale_width, ragged_dot_mxfp4, route, route_bwd, sort_rows)

@@ -20,7 +20,8 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "librd.so")
 
-SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_dx.cu", "gemm_dw.cu", "glu.cu", "unsort.cu"]
+SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_dx.cu", "gemm_dw.cu", "glu.cu", "unsort.cu",
+           "api_moe.cu", "route.cu", "sort_rows.cu", "permute.cu", "mxfp4.cu", "gemm_mxfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",
                  "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
@@ -34,7 +35,7 @@ def _nvcc() -> str:
 
 
 def _headers():
-    out = [os.path.join(ROOT, "include", "rd.h")]
+    out = [os.path.join(ROOT, "include", h) for h in ("rd.h", "rd_moe.h")]
     for f in os.listdir(CSRC):
         if f.endswith((".h", ".cuh")):
             out.append(os.path.join(CSRC, f))

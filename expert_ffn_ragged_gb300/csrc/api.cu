@@ -12,6 +12,7 @@
 
 #include "../../include/rd.h"
 #include "gemm_args.h"
+#include "host.h"
 
 namespace rd {
 namespace {
@@ -23,12 +24,6 @@ constexpr int32_t kBandRows = 6144;              // default rows per band of the
 std::atomic<int32_t> g_variant{RD_VARIANT_AUTO};
 std::atomic<int32_t> g_band_rows{0};
 std::atomic<uint64_t> g_timeout_ns{0};
-
-uint64_t wait_timeout_ns() {
-  const uint64_t t = g_timeout_ns.load(std::memory_order_relaxed);
-  return t == 0 ? kTimeoutNs : t;
-}
-constexpr int64_t kMaxDim = 0x7FFFFFFF;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -49,7 +44,13 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// SM count of the current device, and whether it is an sm_103 part
+}  // namespace
+
+uint64_t wait_timeout_ns() {
+  const uint64_t t = g_timeout_ns.load(std::memory_order_relaxed);
+  return t == 0 ? kTimeoutNs : t;
+}
+
 rd_status current_device(int* sms) {
   static std::mutex mu;
   static int cached_sms[64];
@@ -71,18 +72,10 @@ rd_status current_device(int* sms) {
   return cached_state[dev] == 1 ? RD_OK : RD_ERR_UNSUPPORTED;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-// bf16 tensor map with 128-byte swizzle; dims/strides innermost first.
 // Encoding costs about a microsecond of host time, a large share of a small
 // call, so each thread keeps the last few maps it encoded (a map is a pure
 // function of these arguments).
+namespace {
 struct MapKey {
   const void* base;
   int rank;
@@ -90,6 +83,7 @@ struct MapKey {
   uint64_t strides[4];
   uint32_t box[5];
 };
+}  // namespace
 
 rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box) {
@@ -139,7 +133,6 @@ rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* d
   return RD_OK;
 }
 
-// checks shared by the three grouped calls
 rd_status check_groups(int64_t m, int64_t k, int64_t n, const int32_t* group_sizes,
                        int32_t g_total, int32_t group_offset, int32_t g_local,
                        const int32_t* limit, const int32_t* status) {
@@ -158,6 +151,7 @@ rd_status check_groups(int64_t m, int64_t k, int64_t n, const int32_t* group_siz
   return RD_OK;
 }
 
+namespace {
 // the output must not overlap any input (or the control words)
 bool out_aliases(const void* out, uint64_t out_bytes, const void* in0, uint64_t b0,
                  const void* in1, uint64_t b1, const void* gs, uint64_t bgs, const void* limit,
@@ -166,6 +160,8 @@ bool out_aliases(const void* out, uint64_t out_bytes, const void* in0, uint64_t 
          overlap(out, out_bytes, gs, bgs) || overlap(out, out_bytes, limit, 4) ||
          overlap(out, out_bytes, status, 4);
 }
+
+}  // namespace
 
 int grid_for(int sms, int64_t tiles_upper_bound) {
   int64_t g = tiles_upper_bound < 1 ? 1 : tiles_upper_bound;
@@ -201,7 +197,6 @@ int pair_grid(int sms, int64_t pair_tiles_upper_bound) {
   return 2 * grid_for(sms / 2, pair_tiles_upper_bound);
 }
 
-}  // namespace
 }  // namespace rd
 
 using namespace rd;

@@ -114,10 +114,10 @@ __device__ __forceinline__ long long warp_exclusive_scan(long long v, int lane) 
   return incl - v;
 }
 
-// Run by one warp: group boundaries, tile prefix, zero ranges, status bits.
-template <int OP, bool PAIR>
-__device__ __forceinline__ void build_schedule(GemmShared<PAIR>& sh, const GemmArgs& a, int lane) {
-  constexpr int TM = TileCfg<PAIR>::kTileM;
+// Run by one warp: group boundaries, tile prefix, zero ranges, status bits (TM: rows of a
+// tile; Shared and Args: the block's shared state and the launch arguments of a grouped kernel).
+template <int OP, int TM, class Shared, class Args>
+__device__ __forceinline__ void build_schedule(Shared& sh, const Args& a, int lane) {
   int32_t L = a.m;
   if (a.limit != nullptr) {
     const int32_t v = *a.limit;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_relinquish();
     }
   }
-  if (warp == 2) build_schedule<OP, PAIR>(sh, args, lane);
+  if (warp == 2) build_schedule<OP, TM>(sh, args, lane);
   ptx::tc_fence_before();
   __syncthreads();
   if (PAIR) ptx::cluster_sync();  // the peer's barriers are initialised before any remote use

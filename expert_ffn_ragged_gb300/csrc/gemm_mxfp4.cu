@@ -1,0 +1,71 @@
+// gemm_mxfp4.cu -- launches of the grouped product over 4-bit operands.
+#include "gemm_mxfp4.cuh"
+
+namespace rd {
+namespace {
+
+template <int EPI, bool PAIR>
+cudaError_t launch_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const Gemm4Args& args,
+                        int grid, cudaStream_t stream) {
+  constexpr size_t smem = gemm4_smem_bytes<PAIR>();
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  const auto kernel = grouped_gemm_mxfp4_kernel<EPI, PAIR>;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  if (!PAIR) {
+    kernel<<<grid, kThreads, smem, stream>>>(tmap_a, tmap_b, args);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // as for the bf16 products: no more CTA pairs than can be resident at once
+  static std::atomic<int> max_clusters[64];
+  int clusters = max_clusters[dev].load(std::memory_order_acquire);
+  if (clusters == 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    clusters = n > 0 ? n : 1;
+    max_clusters[dev].store(clusters, std::memory_order_release);
+  }
+  if (grid > 2 * clusters) grid = 2 * clusters;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, tmap_a, tmap_b, args);
+}
+
+template <bool PAIR>
+cudaError_t launch_epi(int epi, const CUtensorMap& a, const CUtensorMap& b, const Gemm4Args& args,
+                       int grid, cudaStream_t stream) {
+  switch (epi) {
+    case k4EpiNone: return launch_impl<k4EpiNone, PAIR>(a, b, args, grid, stream);
+    case k4EpiGlu: return launch_impl<k4EpiGlu, PAIR>(a, b, args, grid, stream);
+    default: return launch_impl<k4EpiGluQuant, PAIR>(a, b, args, grid, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mxfp4(int epi, bool pair, const CUtensorMap& a, const CUtensorMap& b,
+                              const Gemm4Args& args, int grid, cudaStream_t stream) {
+  return pair ? launch_epi<true>(epi, a, b, args, grid, stream)
+              : launch_epi<false>(epi, a, b, args, grid, stream);
+}
+
+}  // namespace rd

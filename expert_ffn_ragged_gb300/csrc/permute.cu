@@ -1,0 +1,171 @@
+// permute.cu -- token rows to packed rows (dispatch), back (combine), and combine's gradients.
+//
+// All three are streams of 16-byte vectors.  A warp owns a piece of a token's row (dispatch,
+// combine) or a whole row of a slot (the gradients, whose dot product it then reduces alone).
+// Packed rows are found through pos, so no inverse permutation is needed and x, d_out and out
+// cross HBM once.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "glu_math.cuh"
+#include "moe_args.h"
+
+namespace rd {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kRowBatch = 4;  // vectors per lane of one piece
+
+__device__ __forceinline__ int32_t rows_below(const int32_t* limit, int32_t rows) {
+  if (limit == nullptr) return rows;
+  const int32_t v = *limit;
+  return v < 0 ? 0 : (v > rows ? rows : v);
+}
+
+__device__ __forceinline__ uint4 ld_row(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__global__ void __launch_bounds__(kRowThreads) dispatch_rows_kernel(const RowsArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int32_t L = rows_below(a.limit, a.tokens);
+  const int pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
+  const int64_t units = static_cast<int64_t>(L) * pieces;
+  const uint4* x = static_cast<const uint4*>(a.x);
+  uint4* out = static_cast<uint4*>(a.out);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units;
+       u += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const int64_t t = u / pieces;
+    const int v0 = static_cast<int>(u - t * pieces) * 32 * kRowBatch + lane;
+    const int32_t p_lane = lane < a.topk ? a.pos[t * a.topk + lane] : -1;
+    uint4 v[kRowBatch];
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b)
+      if (v0 + 32 * b < a.vecs) v[b] = ld_row(x + t * a.vecs + v0 + 32 * b);
+    for (int k = 0; k < a.topk; ++k) {
+      const int32_t p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
+      if (p < 0 || p >= a.packed_rows) continue;
+      uint4* o = out + static_cast<int64_t>(p) * a.vecs;
+#pragma unroll
+      for (int b = 0; b < kRowBatch; ++b)
+        if (v0 + 32 * b < a.vecs) o[v0 + 32 * b] = v[b];
+    }
+  }
+}
+
+__device__ __forceinline__ void add_scaled(float (&acc)[8], uint4 y, float w) {
+  const uint32_t c[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(w, bf16_lo(c[i]), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, bf16_hi(c[i]), acc[2 * i + 1]);
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const RowsArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int32_t L = rows_below(a.limit, a.tokens);
+  const int pieces = (a.vecs + 31) / 32;
+  const int64_t units = static_cast<int64_t>(L) * pieces;
+  const uint4* y = static_cast<const uint4*>(a.x);
+  uint4* out = static_cast<uint4*>(a.out);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units;
+       u += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const int64_t t = u / pieces;
+    const int v = static_cast<int>(u - t * pieces) * 32 + lane;
+    int32_t p_lane = -1;
+    float w_lane = 0.0f;
+    if (lane < a.topk) {
+      p_lane = a.pos[t * a.topk + lane];
+      w_lane = a.w != nullptr ? a.w[t * a.topk + lane] : 1.0f;
+    }
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int k = 0; k < a.topk; ++k) {
+      const int32_t p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
+      const float w = __shfl_sync(0xFFFFFFFFu, w_lane, k);
+      if (p >= 0 && p < a.packed_rows && v < a.vecs)
+        add_scaled(acc, ld_row(y + static_cast<int64_t>(p) * a.vecs + v), w);
+    }
+    if (v < a.vecs)
+      out[t * a.vecs + v] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                       pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+  }
+}
+
+__device__ __forceinline__ uint32_t scale_dot(uint32_t d, uint32_t y, float w, float& dot) {
+  const float d0 = bf16_lo(d), d1 = bf16_hi(d);
+  dot = fmaf(d0, bf16_lo(y), dot);
+  dot = fmaf(d1, bf16_hi(y), dot);
+  return pack_bf16x2(__fmul_rn(d0, w), __fmul_rn(d1, w));
+}
+
+__global__ void __launch_bounds__(kRowThreads) combine_rows_bwd_kernel(const RowsArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int32_t L = rows_below(a.limit, a.tokens);
+  const int64_t slots = static_cast<int64_t>(L) * a.topk;
+  const uint4* d_out = static_cast<const uint4*>(a.x);
+  const uint4* y = static_cast<const uint4*>(a.y);
+  uint4* d_y = static_cast<uint4*>(a.out);
+  for (int64_t s = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); s < slots;
+       s += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const int64_t t = s / a.topk;
+    const int32_t p = a.pos[s];
+    float dot = 0.0f;
+    if (p >= 0 && p < a.packed_rows) {
+      const float w = a.w[s];
+      const uint4* dr = d_out + t * a.vecs;
+      const uint4* yr = y + static_cast<int64_t>(p) * a.vecs;
+      uint4* o = d_y + static_cast<int64_t>(p) * a.vecs;
+      for (int v0 = lane; v0 < a.vecs; v0 += 32 * kRowBatch) {
+        uint4 dv[kRowBatch], yv[kRowBatch];
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b) {
+          if (v0 + 32 * b < a.vecs) {
+            dv[b] = __ldg(dr + v0 + 32 * b);
+            yv[b] = ld_row(yr + v0 + 32 * b);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b)
+          if (v0 + 32 * b < a.vecs)
+            o[v0 + 32 * b] = make_uint4(scale_dot(dv[b].x, yv[b].x, w, dot), scale_dot(dv[b].y, yv[b].y, w, dot),
+                                        scale_dot(dv[b].z, yv[b].z, w, dot), scale_dot(dv[b].w, yv[b].w, w, dot));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    }
+    if (lane == 0) a.d_w[s] = dot;
+  }
+}
+
+int row_grid(int64_t units, int sms) {
+  const int64_t blocks = (units + kRowWarps - 1) / kRowWarps;
+  return static_cast<int>(blocks < 8 * static_cast<int64_t>(sms) ? blocks : 8 * static_cast<int64_t>(sms));
+}
+
+}  // namespace
+
+cudaError_t launch_dispatch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
+  const int64_t pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
+  dispatch_rows_kernel<<<row_grid(a.tokens * pieces, sms), kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
+  const int64_t pieces = (a.vecs + 31) / 32;
+  combine_rows_kernel<<<row_grid(a.tokens * pieces, sms), kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_rows_bwd(const RowsArgs& a, int sms, cudaStream_t stream) {
+  combine_rows_bwd_kernel<<<row_grid(static_cast<int64_t>(a.tokens) * a.topk, sms), kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace rd

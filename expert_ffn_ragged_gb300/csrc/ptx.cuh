@@ -285,6 +285,46 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_des
       : "memory");
 }
 
+// ---- block-scaled 4-bit MMA: E2M1 operands, one E8M0 scale per 32 elements of K, f32
+// accumulator; the scales sit in tensor memory (A: 32 lanes x 4 columns for 128 rows and 128
+// elements of K, repeated in every lane quarter; B: one column per 32 rows).
+__device__ __forceinline__ void tc_mma_mxfp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+          "r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_mxfp4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                  uint32_t idesc, uint32_t sfa_tmem,
+                                                  uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+          "r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory into 32 lanes x 4 columns, repeated in all four lane
+// quarters (in a pair: in both CTAs, each from its own shared memory).  Runs in order with the
+// MMAs that the same thread issues after it.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+               : "memory");
+}
+
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+               : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns: thread t of the warp receives
 // lane (taddr.lane + t), columns taddr.col .. taddr.col + 31.  The wait for
 // completion is part of the same statement so no use of the registers can
@@ -368,6 +408,26 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of a 512-byte block of scales (32 rows of 16 bytes, no swizzle): groups of 8 rows are
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// Instruction descriptor of tcgen05.mma.kind::mxf4: B scale byte bits 4-5, A format bits 7-9
+// (1 = E2M1), B format bits 10-12, both operands K-major, N >> 3 at bits 17-22, scale format bit 23
+// (1 = E8M0), M >> 4 at bits 24-28, A scale byte bits 29-30.  The scale byte (0 or 2) is the first
+// of the two bytes of the scale word that this K step of 64 uses.
+__host__ __device__ constexpr uint32_t idesc_mxfp4_f32(int M, int N, int scale_byte) {
+  return (static_cast<uint32_t>(scale_byte) << 4) | (1u << 7) | (1u << 10) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) |
+         (static_cast<uint32_t>(scale_byte) << 29);
 }
 
 }  // namespace ptx
