@@ -82,11 +82,12 @@ struct MapKey {
   uint64_t dims[5];
   uint64_t strides[4];
   uint32_t box[5];
+  CUtensorMapSwizzle swizzle;
 };
 }  // namespace
 
 rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                 const uint64_t* strides_bytes, const uint32_t* box) {
+                 const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   constexpr int kCache = 16;
   struct Entry {
     MapKey key;
@@ -99,6 +100,7 @@ rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* d
   std::memset(&key, 0, sizeof(key));
   key.base = base;
   key.rank = rank;
+  key.swizzle = swizzle;
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
     key.box[i] = box[i];
@@ -122,7 +124,7 @@ rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* d
   for (int i = 0; i < rank - 1; ++i) gstride[i] = strides_bytes[i];
   const CUresult r =
       fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), gdim, gstride,
-         gbox, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         gbox, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return RD_ERR_UNSUPPORTED;
   Entry& slot = cache[next_slot];

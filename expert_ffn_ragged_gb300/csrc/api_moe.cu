@@ -388,17 +388,27 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   if ((st = current_device(&sms)) != RD_OK) return st;
   if (m == 0 || n == 0) return RD_OK;
 
-  CUtensorMap ta = {}, tb = {};
+  Gemm4Maps maps = {};
   if (k > 0) {
-    // rows of k / 2 bytes as k / 4 two-byte elements: boxes of 128 bytes of a row
+    // rows of k / 2 bytes as k / 4 two-byte elements, boxes of 128 bytes of a row; scale rows as
+    // width / 2 such elements, boxes of 32 bytes
     const uint64_t da[2] = {static_cast<uint64_t>(k / 4), um};
     const uint64_t sa[1] = {static_cast<uint64_t>(k / 2)};
     const uint32_t ba[2] = {64, kBM};
-    if ((st = encode(&ta, a, 2, da, sa, ba)) != RD_OK) return st;
+    if ((st = encode(&maps.a, a, 2, da, sa, ba)) != RD_OK) return st;
     const uint64_t db[3] = {static_cast<uint64_t>(k / 4), static_cast<uint64_t>(n), ug};
     const uint64_t sb[2] = {static_cast<uint64_t>(k / 2), static_cast<uint64_t>(n) * (k / 2)};
     const uint32_t bb[3] = {64, k4Half, 1};
-    if ((st = encode(&tb, b, 3, db, sb, bb)) != RD_OK) return st;
+    if ((st = encode(&maps.b, b, 3, db, sb, bb)) != RD_OK) return st;
+    const uint64_t w = static_cast<uint64_t>(width);
+    const uint64_t das[2] = {w / 2, um}, sas[1] = {w};
+    const uint32_t bas[2] = {16, kBM};
+    if ((st = encode(&maps.a_scales, a_scales, 2, das, sas, bas, CU_TENSOR_MAP_SWIZZLE_32B)) != RD_OK)
+      return st;
+    const uint64_t dbs[3] = {w / 2, static_cast<uint64_t>(n), ug}, sbs[2] = {w, static_cast<uint64_t>(n) * w};
+    const uint32_t bbs[3] = {16, k4Half, 1};
+    if ((st = encode(&maps.b_scales, b_scales, 3, dbs, sbs, bbs, CU_TENSOR_MAP_SWIZZLE_32B)) != RD_OK)
+      return st;
   }
   const bool pair = use_pair(sms, m, g_total);
   const int tile_w = glu ? k4Half : k4BN;
@@ -406,15 +416,11 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   g.group_sizes = group_sizes;
   g.limit = limit;
   g.status = status;
-  g.a_scales = static_cast<const uint8_t*>(a_scales);
-  g.b_scales = static_cast<const uint8_t*>(b_scales);
   g.out = out;
   g.out_scales = static_cast<uint8_t*>(out_scales);
   g.m = static_cast<int32_t>(m);
   g.kc = static_cast<int32_t>(k);
-  g.n = static_cast<int32_t>(n);
   g.n_out = static_cast<int32_t>(n_out);
-  g.scale_width = static_cast<int32_t>(width);
   g.out_scale_width = static_cast<int32_t>(out_width);
   g.g_total = g_total;
   g.group_offset = group_offset;
@@ -427,5 +433,5 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
   const int grid = pair ? pair_grid(sms, tiles) : grid_for(sms, tiles);
   const int which = quant ? k4EpiGluQuant : (glu ? k4EpiGlu : k4EpiNone);
-  return done(launch_gemm_mxfp4(which, pair, ta, tb, g, grid, cu(stream)));
+  return done(launch_gemm_mxfp4(which, pair, maps, g, grid, cu(stream)));
 }

@@ -5,8 +5,7 @@ namespace rd {
 namespace {
 
 template <int EPI, bool PAIR>
-cudaError_t launch_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const Gemm4Args& args,
-                        int grid, cudaStream_t stream) {
+cudaError_t launch_impl(const Gemm4Maps& maps, const Gemm4Args& args, int grid, cudaStream_t stream) {
   constexpr size_t smem = gemm4_smem_bytes<PAIR>();
   static_assert(smem <= 232448, "shared memory of one CTA");
   const auto kernel = grouped_gemm_mxfp4_kernel<EPI, PAIR>;
@@ -20,11 +19,11 @@ cudaError_t launch_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, co
     attr_set[dev].store(true, std::memory_order_release);
   }
   if (!PAIR) {
-    kernel<<<grid, kThreads, smem, stream>>>(tmap_a, tmap_b, args);
+    kernel<<<grid, k4Threads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(k4Threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -47,25 +46,25 @@ cudaError_t launch_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, co
   }
   if (grid > 2 * clusters) grid = 2 * clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kernel, tmap_a, tmap_b, args);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, args);
 }
 
 template <bool PAIR>
-cudaError_t launch_epi(int epi, const CUtensorMap& a, const CUtensorMap& b, const Gemm4Args& args,
-                       int grid, cudaStream_t stream) {
+cudaError_t launch_epi(int epi, const Gemm4Maps& maps, const Gemm4Args& args, int grid,
+                       cudaStream_t stream) {
   switch (epi) {
-    case k4EpiNone: return launch_impl<k4EpiNone, PAIR>(a, b, args, grid, stream);
-    case k4EpiGlu: return launch_impl<k4EpiGlu, PAIR>(a, b, args, grid, stream);
-    default: return launch_impl<k4EpiGluQuant, PAIR>(a, b, args, grid, stream);
+    case k4EpiNone: return launch_impl<k4EpiNone, PAIR>(maps, args, grid, stream);
+    case k4EpiGlu: return launch_impl<k4EpiGlu, PAIR>(maps, args, grid, stream);
+    default: return launch_impl<k4EpiGluQuant, PAIR>(maps, args, grid, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_mxfp4(int epi, bool pair, const CUtensorMap& a, const CUtensorMap& b,
-                              const Gemm4Args& args, int grid, cudaStream_t stream) {
-  return pair ? launch_epi<true>(epi, a, b, args, grid, stream)
-              : launch_epi<false>(epi, a, b, args, grid, stream);
+cudaError_t launch_gemm_mxfp4(int epi, bool pair, const Gemm4Maps& maps, const Gemm4Args& args,
+                              int grid, cudaStream_t stream) {
+  return pair ? launch_epi<true>(epi, maps, args, grid, stream)
+              : launch_epi<false>(epi, maps, args, grid, stream);
 }
 
 }  // namespace rd

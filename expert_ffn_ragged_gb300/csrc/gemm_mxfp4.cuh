@@ -5,18 +5,24 @@
 //
 // The schedule (group boundaries, bands of m-tiles, the last m-tile of a group shifted back to its
 // end) is that of the bf16 products (gemm_kernel.cuh); what differs:
-//   * 128 bytes of a row are 256 elements of k, so one ring stage is 256 deep and the MMA takes it
-//     in four steps of 64.  Both operands are K-major;
+//   * 128 bytes of a row are 256 elements of k, which the MMA takes in four steps of 64.  Both
+//     operands are K-major.  A ring stage of the pair variant holds two such blocks: the MMA thread
+//     then waits and commits once per 8 MMAs (768 cycles of tensor work).  With a wait for the
+//     operands, one for the scales and two commits per 4 MMAs it was the thread's own instructions
+//     that bound the kernel (855 cycles per 256 elements of k instead of 384, whatever else was
+//     left out).  For the same reason the scales' arrival counts on the operands' barrier;
 //   * a tile is 192 columns wide (96 gate + 96 up columns with the GLU).  Tensor memory has 512
 //     columns: two 192-column accumulators leave 64 columns beside each for the scales, two
 //     256-column ones would leave none;
-//   * the scales of a tile are loaded in their natural row-major layout by two warps (16 bytes a
-//     row: 512 elements of k), laid out in shared memory the way the tensor core reads them (per
-//     128 rows and 128 elements of k: 32 rows of 16 bytes, row r's word at (r % 32) * 16 +
-//     (r / 32) * 4), and copied to tensor memory by the MMA thread just ahead of the MMAs that use
-//     them.  No padding of groups and no packing of the scales is needed, and the row shift of a
-//     group's last tile is free.
-// Warps: 0 TMA producer, 1 MMA issuer, 2-9 epilogue, 10-11 scales.  Zero rows are written by the
+//   * the scales keep their natural row-major layout in global memory: TMA brings 32 bytes a row
+//     (1024 elements of k) of the tile's 128 + 192 rows into shared memory, and four warps, one
+//     per lane quarter, move them from there to tensor memory, transposed on the way: the tensor
+//     core wants, for 128 elements of k, row r's four scale bytes in lane r % 32 of column r / 32,
+//     repeated in every lane quarter.  No padding of groups and no packing of the scales is needed,
+//     and the row shift of a group's last tile is free.  (Loaded straight from global memory into
+//     registers and passed on through shared memory, the scales held the MMAs to 1350 cycles per
+//     256 elements of k.)
+// Warps: 0 TMA producer, 1 MMA issuer, 2-9 epilogue, 10-13 scales.  Zero rows are written by the
 // epilogue warps when their tiles are done.
 #pragma once
 
@@ -26,12 +32,19 @@
 
 namespace rd {
 
-constexpr int k4BK = 256;       // elements of k per stage (128 bytes a row)
+constexpr int k4BK = 256;       // elements of k in 128 bytes of a row
 constexpr int k4BN = 192;       // output columns of a tile
 constexpr int k4Half = k4BN / 2;
-constexpr int k4Chunk = 512;    // elements of k per scale chunk (16 scale bytes a row)
-constexpr int k4ScaleSlots = 4;  // scale chunks in shared memory
-constexpr int k4ScaleWarps = 2;
+constexpr int k4Threads = 448;
+constexpr int k4ScaleWarps = 4;
+constexpr int k4Chunk = 512;    // elements of k of a tensor-memory scale slot
+constexpr int k4RawK = 1024;    // elements of k of a shared-memory scale slot (32 scale bytes a row)
+constexpr int k4RawSlots = 3;
+constexpr int k4RawA = kBM * 32;
+constexpr int k4RawBytes = (kBM + k4BN) * 32;
+// A tensor-memory slot holds the scales of 512 elements of k in the 64 columns beside an
+// accumulator: four words (128 elements each) of 4 columns for A's rows, then of 8 for B's.
+constexpr int k4SlotColB = 16;
 
 enum Gemm4Epi : int { k4EpiNone = 0, k4EpiGlu = 1, k4EpiGluQuant = 2 };
 
@@ -39,15 +52,11 @@ struct Gemm4Args {
   const int32_t* group_sizes;
   const int32_t* limit;
   int32_t* status;
-  const uint8_t* a_scales;  // [m, scale_width]
-  const uint8_t* b_scales;  // [g_local, n, scale_width]
   void* out;
   uint8_t* out_scales;
   int32_t m;
   int32_t kc;            // contraction length (elements)
-  int32_t n;             // rows of each b block
   int32_t n_out;         // output columns (n, or n / 2 with the GLU)
-  int32_t scale_width;   // bytes of a scale row of a and b
   int32_t out_scale_width;
   int32_t g_total;
   int32_t group_offset;
@@ -58,28 +67,32 @@ struct Gemm4Args {
   uint64_t timeout_ns;
 };
 
-template <bool PAIR>
-struct Tile4Cfg {
-  static constexpr int kStagesN = PAIR ? 6 : 4;
-  static constexpr int kTileM = PAIR ? 2 * kBM : kBM;
-  static constexpr int kBRows = PAIR ? k4Half : k4BN;  // B rows held by one CTA
-  static constexpr int kStageA = kBM * 128;            // 16 KB
-  static constexpr int kStageB = kBRows * 128;         // 12 KB (pair) or 24 KB
-  static constexpr int kStageBytes = kStageA + kStageB;
+// operands and their scales; boxes: a 128 rows, b 96 rows (of 128 bytes; scales: of 32)
+struct Gemm4Maps {
+  CUtensorMap a, b, a_scales, b_scales;
 };
 
-constexpr int k4WordA = 512;             // A scales of 128 rows x 128 k
-constexpr int k4WordB = 1024;            // B scales of 192 (256) rows x 128 k
-constexpr int k4SlotBytes = 4 * (k4WordA + k4WordB);
+template <bool PAIR>
+struct Tile4Cfg {
+  static constexpr int kStagesN = PAIR ? 3 : 4;
+  static constexpr int kSub = PAIR ? 2 : 1;            // 256-element blocks of a stage
+  static constexpr int kTileM = PAIR ? 2 * kBM : kBM;
+  static constexpr int kBRows = PAIR ? k4Half : k4BN;  // B rows held by one CTA
+  static constexpr int kSubA = kBM * 128;              // 16 KB
+  static constexpr int kSubB = kBRows * 128;           // 12 KB (pair) or 24 KB
+  static constexpr int kStageA = kSub * kSubA;
+  static constexpr int kStageB = kSub * kSubB;
+  static constexpr int kStageBytes = kStageA + kStageB;
+};
 
 template <bool PAIR>
 struct alignas(128) Gemm4Shared {
   static constexpr int S = Tile4Cfg<PAIR>::kStagesN;
-  uint8_t scales[k4ScaleSlots][k4SlotBytes];
+  uint8_t raw[k4RawSlots][k4RawBytes];  // first: TMA destinations (128-byte aligned)
   uint64_t full[S];
   uint64_t empty[S];
-  uint64_t sfull[k4ScaleSlots];
-  uint64_t sempty[k4ScaleSlots];
+  uint64_t rfull[k4RawSlots];
+  uint64_t rempty[k4RawSlots];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
@@ -112,7 +125,8 @@ __device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<PAIR>& sh, const 
   v.dw_m_tiles = 0;
   v.kc = a.kc;
   Tile tl = decode_tile_view<kOpFwd, Tile4Cfg<PAIR>::kTileM>(v, t);
-  tl.nkb = (a.kc + k4BK - 1) / k4BK;
+  constexpr int kStageK = Tile4Cfg<PAIR>::kSub * k4BK;
+  tl.nkb = (a.kc + kStageK - 1) / kStageK;  // stages of the tile
   return tl;
 }
 
@@ -124,10 +138,17 @@ __device__ __forceinline__ int b_row_of(int n_idx, int c, int n_out) {
   return c < k4Half ? n_idx * k4Half + c : n_out + n_idx * k4Half + (c - k4Half);
 }
 
+// One lane waits for the warp (polls by all lanes end at different times and then wait for each other).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t limit_ns, int lane) {
+  int ok = 1;
+  if (lane == 0) ok = ptx::mbar_wait_bounded(bar, parity, abort_flag, limit_ns) ? 1 : 0;
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
 template <int EPI, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                              const __grid_constant__ CUtensorMap tmap_b, const Gemm4Args args) {
+__global__ void __launch_bounds__(k4Threads, 1)
+    grouped_gemm_mxfp4_kernel(const __grid_constant__ Gemm4Maps maps, const Gemm4Args args) {
   constexpr bool GLU = EPI != k4EpiNone;
   using Cfg = Tile4Cfg<PAIR>;
   constexpr int S = Cfg::kStagesN;
@@ -149,12 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
+      // the producer's arrival (with the copies' bytes) and those of the scale warps
+      ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1 + (PAIR ? 2 : 1) * k4ScaleWarps);
       ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
     }
-    for (int s = 0; s < k4ScaleSlots; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&sh.sfull[s]), PAIR ? 2 * k4ScaleWarps : k4ScaleWarps);
-      ptx::mbar_init(ptx::smem_addr(&sh.sempty[s]), 1);
+    for (int s = 0; s < k4RawSlots; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&sh.rfull[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh.rempty[s]), k4ScaleWarps);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_addr(&sh.tfull[b]), 1);
@@ -165,8 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
   }
   if (warp == 0 && lane == 0 && args.kc > 0) {
-    ptx::prefetch_tmap(&tmap_a);
-    ptx::prefetch_tmap(&tmap_b);
+    ptx::prefetch_tmap(&maps.a);
+    ptx::prefetch_tmap(&maps.b);
+    ptx::prefetch_tmap(&maps.a_scales);
+    ptx::prefetch_tmap(&maps.b_scales);
   }
   if (warp == 1) {
     if (PAIR) {
@@ -189,36 +213,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0;
       uint32_t pend_mask = 0, pend_par = 0;
+      uint32_t rpend_mask = 0, rpend_par = 0;  // raw slots whose copies may be in flight
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = decode_tile4<PAIR>(sh, args, t);
         const int arow = tl.row_load + static_cast<int>(rank) * kBM;
         // the 96-row boxes of b: one per CTA of a pair, two on a single CTA
-        const int brow0 = b_row_of<GLU>(tl.n_idx, PAIR ? static_cast<int>(rank) * k4Half : 0, args.n_out);
+        const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
         const int brow1 = b_row_of<GLU>(tl.n_idx, k4Half, args.n_out);
         for (int kb = 0; kb < tl.nkb; ++kb) {
+          const int k0 = kb * Cfg::kSub * k4BK;
+          if (k0 % k4RawK == 0) {
+            // the scales of the next 1024 elements of k: A's rows of this CTA, all B rows of the tile
+            if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rempty[slot]), slot_phase ^ 1, abort_flag, tlimit)) {
+              ok = false;
+              break;
+            }
+            const uint32_t rb = ptx::smem_addr(&sh.rfull[slot]);
+            const uint32_t dst = ptx::smem_addr(sh.raw[slot]);
+            ptx::mbar_arrive_expect_tx(rb, k4RawBytes);
+            const int x = k0 / (2 * kMxBlock);  // two scale bytes a map element
+            ptx::tma_load_2d(dst, &maps.a_scales, rb, x, arow);
+            ptx::tma_load_3d(dst + k4RawA, &maps.b_scales, rb, x, brow0, tl.j);
+            ptx::tma_load_3d(dst + k4RawA + k4Half * 32, &maps.b_scales, rb, x, brow1, tl.j);
+            rpend_mask |= 1u << slot;
+            rpend_par = (rpend_par & ~(1u << slot)) | (slot_phase << slot);
+            if (++slot == k4RawSlots) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
+          }
           const uint32_t fb_local = ptx::smem_addr(&sh.full[stage]);
           const uint32_t fb = PAIR ? ptx::map_to_rank(fb_local, 0) : fb_local;
           const uint32_t a_dst = ptx::smem_addr(sA + stage * Cfg::kStageA);
           const uint32_t b_dst = ptx::smem_addr(sB + stage * Cfg::kStageB);
+          // the last stage of a row may hold fewer blocks
+          const int left = (args.kc - k0 + k4BK - 1) / k4BK;
+          const int subs = left < Cfg::kSub ? left : Cfg::kSub;
           if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, tlimit)) {
             ok = false;
             break;
           }
           pend_mask &= ~(1u << stage);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, (PAIR ? 2 : 1) * Cfg::kStageBytes);
-          // 128 bytes of a row are 64 two-byte elements of the maps
-          const int x = kb * 64;
-          if (PAIR) {
-            ptx::tma_load_2d_pair(a_dst, &tmap_a, fb, x, arow);
-            ptx::tma_load_3d_pair(b_dst, &tmap_b, fb, x, brow0, tl.j);
-          } else {
-            ptx::tma_load_2d(a_dst, &tmap_a, fb, x, arow);
-            ptx::tma_load_3d(b_dst, &tmap_b, fb, x, brow0, tl.j);
-            ptx::tma_load_3d(b_dst + k4Half * 128, &tmap_b, fb, x, brow1, tl.j);
+          if (rank == 0)
+            ptx::mbar_arrive_expect_tx(fb_local, (PAIR ? 2 : 1) * subs * (Cfg::kSubA + Cfg::kSubB));
+#pragma unroll
+          for (int i = 0; i < Cfg::kSub; ++i) {
+            if (i >= subs) break;
+            const int x = k0 / 4 + i * 64;  // four codes a map element
+            if (PAIR) {
+              ptx::tma_load_2d_pair(a_dst + i * Cfg::kSubA, &maps.a, fb, x, arow);
+              ptx::tma_load_3d_pair(b_dst + i * Cfg::kSubB, &maps.b, fb, x, rank == 0 ? brow0 : brow1, tl.j);
+            } else {
+              ptx::tma_load_2d(a_dst, &maps.a, fb, x, arow);
+              ptx::tma_load_3d(b_dst, &maps.b, fb, x, brow0, tl.j);
+              ptx::tma_load_3d(b_dst + k4Half * 128, &maps.b, fb, x, brow1, tl.j);
+            }
           }
           pend_mask |= 1u << stage;
           pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
@@ -228,20 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // leave only once every fill has been consumed (or, unwinding, has landed; the odd CTA
-      // of a pair cannot see its copies, which count on the even CTA's barrier: a grace period)
+      // Leave only once every fill has been consumed.  Unwinding, a fill's barrier may never
+      // complete (it also counts the scale warps, and in a pair the even CTA's holds the odd CTA's
+      // copies): the copies in flight get a grace period instead.  The scales' copies count on
+      // barriers of their own.
       volatile int no_abort = 0;
-      for (int s = 0; s < S; ++s) {
-        if (!(pend_mask & (1u << s))) continue;
-        const uint32_t par = (pend_par >> s) & 1u;
-        if (*abort_flag) {
-          if (!PAIR || rank == 0)
-            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[s]), par, &no_abort, kDrainNs);
-        } else {
-          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), par, &no_abort, kDrainNs);
-        }
+      if (!*abort_flag) {
+        for (int s = 0; s < S; ++s)
+          if (pend_mask & (1u << s))
+            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), (pend_par >> s) & 1u, abort_flag, kDrainNs);
       }
-      if (PAIR && rank != 0 && *abort_flag && pend_mask != 0) {
+      for (int s = 0; s < k4RawSlots; ++s)
+        if (rpend_mask & (1u << s))
+          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rfull[s]), (rpend_par >> s) & 1u, &no_abort, kDrainNs);
+      if (*abort_flag) {
         const uint64_t t0 = ptx::global_timer_ns();
         while (ptx::global_timer_ns() - t0 < kGraceNs) __nanosleep(1000);
       }
@@ -251,66 +304,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc0 = ptx::idesc_mxfp4_f32(TM, k4BN, 0);
       constexpr uint32_t idesc2 = ptx::idesc_mxfp4_f32(TM, k4BN, 2);
-      int stage = 0, acc = 0, slot = 0;
-      uint32_t acc_phase = 0, full_phase = 0, slot_phase = 0;
-      uint32_t sbuf = 0;  // which 64-column gap the next block's scales go to
+      // operand descriptors of stage 0; a stage, and a K step of 32 bytes, move the address field
+      const uint64_t a_desc0 = ptx::sw128_desc(ptx::smem_addr(sA), 16, 1024);
+      const uint64_t b_desc0 = ptx::sw128_desc(ptx::smem_addr(sB), 16, 1024);
+      int stage = 0, acc = 0;
+      uint32_t acc_phase = 0, full_phase = 0;
+      uint32_t slot = 0;  // tensor-memory slot of the scales
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = decode_tile4<PAIR>(sh, args, t);
         if (tl.nkb == 0) continue;
         ok = ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag, tlimit);
         if (!ok) break;
-        ptx::tc_fence_after();
         const uint32_t d_tmem = sh.tmem_base + static_cast<uint32_t>(acc * kBN);
         for (int kb = 0; kb < tl.nkb; ++kb) {
-          const uint32_t a_addr = ptx::smem_addr(sA + stage * Cfg::kStageA);
-          const uint32_t b_addr = ptx::smem_addr(sB + stage * Cfg::kStageB);
-          const uint32_t s_addr = ptx::smem_addr(sh.scales[slot]) + (kb & 1) * 2 * (k4WordA + k4WordB);
-          const uint32_t s_tmem = sh.tmem_base + k4BN + sbuf * kBN;
-          const int left = args.kc - kb * k4BK;
-          const int steps = left >= k4BK ? 4 : (left + 63) / 64;
-          if ((kb & 1) == 0) {
-            ok = PAIR ? ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.sfull[slot]), slot_phase, abort_flag, tlimit)
-                      : ptx::mbar_wait_bounded(ptx::smem_addr(&sh.sfull[slot]), slot_phase, abort_flag, tlimit);
-            if (!ok) break;
-          }
-          ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit);
+          const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage * (Cfg::kStageA >> 4));
+          const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage * (Cfg::kStageB >> 4));
+          // this stage's words of the scale slot (512 elements of k a slot)
+          const int word0 = (kb * Cfg::kSub * 2) & 3;
+          const uint32_t sfa = sh.tmem_base + k4BN + slot * kBN + word0 * 4;
+          const uint32_t sfb = sh.tmem_base + k4BN + slot * kBN + k4SlotColB + word0 * 8;
+          const bool last = kb == tl.nkb - 1;
+          constexpr int kSteps = 4 * Cfg::kSub;
+          const int steps = last ? (args.kc - kb * Cfg::kSub * k4BK + 63) / 64 : kSteps;
+          ok = PAIR ? ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit)
+                    : ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit);
           if (!ok) break;
           ptx::tc_fence_after();
+          auto mma = [&](int kk, uint32_t accum) {
+            const uint64_t ak = ad + (kk >> 2) * (Cfg::kSubA >> 4) + (kk & 3) * 2;
+            const uint64_t bk = bd + (kk >> 2) * (Cfg::kSubB >> 4) + (kk & 3) * 2;
+            const uint32_t fa = sfa + (kk >> 1) * 4, fb = sfb + (kk >> 1) * 8;
+            const uint32_t id = (kk & 1) ? idesc2 : idesc0;
+            if (PAIR) ptx::tc_mma_mxfp4_pair(d_tmem, ak, bk, id, fa, fb, accum);
+            else ptx::tc_mma_mxfp4(d_tmem, ak, bk, id, fa, fb, accum);
+          };
+          if (steps == kSteps) {
+            mma(0, kb > 0 ? 1u : 0u);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t sw = s_addr + w * (k4WordA + k4WordB);
-            auto cp = [&](uint32_t col, uint32_t saddr) {
-              if (PAIR) ptx::tc_copy_scales_pair(s_tmem + col, ptx::scales_desc(saddr));
-              else ptx::tc_copy_scales(s_tmem + col, ptx::scales_desc(saddr));
-            };
-            cp(w * 4, sw);
-            cp(8 + w * 8, sw + k4WordA);
-            cp(8 + w * 8 + 4, sw + k4WordA + 512);
-          }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= steps) break;
-            const uint64_t ad = ptx::sw128_desc(a_addr + kk * 32, 16, 1024);
-            const uint64_t bd = ptx::sw128_desc(b_addr + kk * 32, 16, 1024);
-            const uint32_t sfa = s_tmem + (kk >> 1) * 4, sfb = s_tmem + 8 + (kk >> 1) * 8;
-            const uint32_t accum = (kb > 0 || kk > 0) ? 1u : 0u;
-            if (PAIR) ptx::tc_mma_mxfp4_pair(d_tmem, ad, bd, (kk & 1) ? idesc2 : idesc0, sfa, sfb, accum);
-            else ptx::tc_mma_mxfp4(d_tmem, ad, bd, (kk & 1) ? idesc2 : idesc0, sfa, sfb, accum);
-          }
-          sbuf ^= 1;
-          const bool chunk_end = (kb & 1) || kb == tl.nkb - 1;
-          if (PAIR) {
-            if (chunk_end) ptx::tc_commit_pair(ptx::smem_addr(&sh.sempty[slot]), 0x3);
-            ptx::tc_commit_pair(ptx::smem_addr(&sh.empty[stage]), 0x3);
+            for (int kk = 1; kk < kSteps; ++kk) mma(kk, 1u);
           } else {
-            if (chunk_end) ptx::tc_commit(ptx::smem_addr(&sh.sempty[slot]));
-            ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
+#pragma unroll 1
+            for (int kk = 0; kk < steps; ++kk) mma(kk, (kb > 0 || kk > 0) ? 1u : 0u);
           }
-          if (chunk_end && ++slot == k4ScaleSlots) {
-            slot = 0;
-            slot_phase ^= 1;
-          }
+          if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.empty[stage]), 0x3);
+          else ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
+          if (word0 + 2 * Cfg::kSub == 4 || last) slot ^= 1;
           if (++stage == S) {
             stage = 0;
             full_phase ^= 1;
@@ -405,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = warp_wait(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit, lane);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t tbase =
@@ -442,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if (PAIR && rank != 0)
-          ptx::mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+          ptx::mbar_arrive_cluster_tmem(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
         else
           ptx::mbar_arrive(ptx::smem_addr(&sh.tempty[acc]));
       }
@@ -467,54 +505,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ scales
-    // Rows 0 .. 127 of the tile's 320 are A's (this CTA's half in a pair), the others B's.  A lane
-    // holds five rows: 16 bytes of each are 512 elements of k.  The next chunk is loaded into
-    // registers before the wait for its slot, so that global latency overlaps it.
-    const int sw = warp - (2 + kEpiWarps);
-    constexpr int kRows = 5;
-    const uint32_t sfull0 = PAIR ? ptx::map_to_rank(ptx::smem_addr(&sh.sfull[0]), 0)
-                                 : ptx::smem_addr(&sh.sfull[0]);
-    int slot = 0;
-    uint32_t phase = 0, pend_mask = 0, pend_par = 0;
+    // Each of the four warps writes one lane quarter of tensor memory, which repeats the scales of
+    // all rows: lane l holds those of rows l, 32 + l, ...  A raw row is 32 bytes, two halves of 16
+    // (512 elements of k) that the copy's 32-byte swizzle exchanges in every second group of four
+    // rows, which makes the 16-byte reads below free of bank conflicts.
+    const uint32_t full0 = PAIR ? ptx::map_to_rank(ptx::smem_addr(&sh.full[0]), 0)
+                                : ptx::smem_addr(&sh.full[0]);
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int raw_slot = 0, stage = 0;
+    uint32_t raw_phase = 0, slot = 0, phase = 0;
+    // per slot: the stage whose consumption frees it, and that fill's parity
+    int free_stage[2] = {-1, -1};
+    uint32_t free_par[2] = {0, 0};
     const int blocks = args.kc / kMxBlock;  // scale bytes of a row that count
+    constexpr int kStagesPerChunk = 2 / Cfg::kSub;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
       const Tile tl = decode_tile4<PAIR>(sh, args, t);
-      const uint8_t* src[kRows];
-      uint32_t dst[kRows];
-      uint32_t word[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = sw * kRows * 32 + i * 32 + lane;
-        if (r < kBM) {
-          const int row = tl.row_load + static_cast<int>(rank) * kBM + r;
-          src[i] = row >= 0 && row < args.m ? args.a_scales + static_cast<int64_t>(row) * args.scale_width : nullptr;
-          dst[i] = (r & 31) * 16 + (r >> 5) * 4;
-          word[i] = k4WordA;
-        } else {
-          const int c = r - kBM;
-          const int row = b_row_of<GLU>(tl.n_idx, c, args.n_out);
-          src[i] = row < args.n ? args.b_scales + (static_cast<int64_t>(tl.j) * args.n + row) * args.scale_width
-                                : nullptr;
-          dst[i] = (c >> 7) * 512 + (c & 31) * 16 + ((c >> 5) & 3) * 4;
-          word[i] = k4WordB;
-        }
-      }
-      const int chunks = (tl.nkb + 1) / 2;
-      auto load = [&](int ch, uint4 (&v)[kRows]) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (src[i] != nullptr) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + ch * 16));
-        }
-      };
-      uint4 next[kRows];
-      if (chunks > 0) load(0, next);
+      const int chunks = (args.kc + k4Chunk - 1) / k4Chunk;
       for (int ch = 0; ch < chunks; ++ch) {
-        uint4 v[kRows];
+        if ((ch & 1) == 0) {
+          ok = warp_wait(ptx::smem_addr(&sh.rfull[raw_slot]), raw_phase, abort_flag, tlimit, lane);
+          if (!ok) break;
+        }
+        const uint8_t* src = sh.raw[raw_slot] + lane * 32 + (((ch & 1) ^ ((lane >> 2) & 1)) * 16);
+        uint4 v[10];  // rows 0 .. 127 of A, 0 .. 191 of B, 32 apart
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) v[i] = next[i];
-        if (ch + 1 < chunks) load(ch + 1, next);
+        for (int i = 0; i < 10; ++i) v[i] = *reinterpret_cast<const uint4*>(src + i * 32 * 32);
+        if ((ch & 1) || ch == chunks - 1) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.rempty[raw_slot]));
+          if (++raw_slot == k4RawSlots) {
+            raw_slot = 0;
+            raw_phase ^= 1;
+          }
+        }
         // bytes past the end of k meet zero operands: they must not be NaN
         const int valid = blocks - ch * 16;
         if (valid < 16) {
@@ -523,43 +548,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             return nb >= 4 ? x : (nb <= 0 ? 0u : x & ((1u << (8 * nb)) - 1u));
           };
 #pragma unroll
-          for (int i = 0; i < kRows; ++i)
+          for (int i = 0; i < 10; ++i)
             v[i] = make_uint4(keep(v[i].x, 0), keep(v[i].y, 1), keep(v[i].z, 2), keep(v[i].w, 3));
         }
-        ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.sempty[slot]), phase ^ 1, abort_flag, tlimit);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        pend_mask &= ~(1u << slot);
-        uint8_t* base = sh.scales[slot];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          // a slot holds, per 128 elements of k, the words of A's rows, then those of B's
-          uint8_t* p = base + (word[i] == k4WordA ? 0 : k4WordA) + dst[i];
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<uint32_t*>(p + w * (k4WordA + k4WordB)) = w4[w];
+        if (free_stage[slot] >= 0) {
+          ok = warp_wait(ptx::smem_addr(&sh.empty[free_stage[slot]]), free_par[slot], abort_flag, tlimit, lane);
+          if (!ok) break;
         }
-        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_after();
+        const uint32_t col = sh.tmem_base + lane_base + k4BN + slot * kBN;
+        const uint32_t a01[8] = {v[0].x, v[1].x, v[2].x, v[3].x, v[0].y, v[1].y, v[2].y, v[3].y};
+        const uint32_t a23[8] = {v[0].z, v[1].z, v[2].z, v[3].z, v[0].w, v[1].w, v[2].w, v[3].w};
+        const uint32_t b0[8] = {v[4].x, v[5].x, v[6].x, v[7].x, v[8].x, v[9].x, 0, 0};
+        const uint32_t b1[8] = {v[4].y, v[5].y, v[6].y, v[7].y, v[8].y, v[9].y, 0, 0};
+        const uint32_t b2[8] = {v[4].z, v[5].z, v[6].z, v[7].z, v[8].z, v[9].z, 0, 0};
+        const uint32_t b3[8] = {v[4].w, v[5].w, v[6].w, v[7].w, v[8].w, v[9].w, 0, 0};
+        ptx::tmem_store_8cols(col, a01);
+        ptx::tmem_store_8cols(col + 8, a23);
+        ptx::tmem_store_8cols(col + k4SlotColB, b0);
+        ptx::tmem_store_8cols(col + k4SlotColB + 8, b1);
+        ptx::tmem_store_8cols(col + k4SlotColB + 16, b2);
+        ptx::tmem_store_8cols(col + k4SlotColB + 24, b3);
+        ptx::tmem_wait_stores();
+        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          const uint32_t b = sfull0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
-          if (PAIR) ptx::mbar_arrive_cluster(b);
-          else ptx::mbar_arrive(b);
+        // the chunk's stages (one of a pair, up to two of a single CTA) may be consumed
+#pragma unroll
+        for (int i = 0; i < kStagesPerChunk; ++i) {
+          if (ch * kStagesPerChunk + i >= tl.nkb) break;
+          if (lane == 0) {
+            const uint32_t b = full0 + static_cast<uint32_t>(stage * sizeof(uint64_t));
+            if (PAIR) ptx::mbar_arrive_cluster_tmem(b);
+            else ptx::mbar_arrive(b);
+          }
+          free_stage[slot] = stage;
+          free_par[slot] = phase;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-        pend_mask |= 1u << slot;
-        pend_par = (pend_par & ~(1u << slot)) | (phase << slot);
-        if (++slot == k4ScaleSlots) {
-          slot = 0;
-          phase ^= 1;
-        }
+        slot ^= 1;
       }
-    }
-    // every commit on a slot's barrier has arrived before the CTA leaves
-    volatile int no_abort = 0;
-    for (int s = 0; s < k4ScaleSlots; ++s) {
-      if ((pend_mask & (1u << s)) && !*abort_flag)
-        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.sempty[s]), (pend_par >> s) & 1u, &no_abort, kDrainNs);
     }
   }
 

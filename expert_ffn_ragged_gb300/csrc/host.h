@@ -26,9 +26,10 @@ inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return a0 < b0 + nb && b0 < a0 + na;
 }
 
-// tensor map of 2-byte elements with 128-byte swizzle; dims/strides innermost first
+// tensor map of 2-byte elements; dims/strides innermost first
 rd_status encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                 const uint64_t* strides_bytes, const uint32_t* box);
+                 const uint64_t* strides_bytes, const uint32_t* box,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // checks shared by the grouped calls
 rd_status check_groups(int64_t m, int64_t k, int64_t n, const int32_t* group_sizes,

@@ -73,9 +73,9 @@ cudaError_t launch_mxfp4_quantize_weights(const void* rhs, uint8_t* q, uint8_t* 
                                           int32_t k, int32_t n, int32_t scale_width,
                                           cudaStream_t stream);
 
+struct Gemm4Maps;
 struct Gemm4Args;
-cudaError_t launch_gemm_mxfp4(int epi, bool pair, const CUtensorMap& tmap_a,
-                              const CUtensorMap& tmap_b, const Gemm4Args& args, int grid,
-                              cudaStream_t stream);
+cudaError_t launch_gemm_mxfp4(int epi, bool pair, const Gemm4Maps& maps, const Gemm4Args& args,
+                              int grid, cudaStream_t stream);
 
 }  // namespace rd

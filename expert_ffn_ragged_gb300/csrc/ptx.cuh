@@ -95,6 +95,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t parity,
                                                           volatile int* abort_flag,
                                                           uint64_t limit_ns) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
   while (true) {
@@ -130,6 +131,14 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                : "memory");
+}
+
+// The same without the release at cluster scope, which holds the warp until its earlier accesses
+// are visible to the cluster (~1600 cycles next to busy tensor cores).  Enough to hand over tensor
+// memory: tcgen05.wait and the fence before thread synchronisation have ordered those accesses,
+// and nothing that the peer reads through generic memory is published with it.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA
@@ -312,17 +321,15 @@ __device__ __forceinline__ void tc_mma_mxfp4_pair(uint32_t d_tmem, uint64_t a_de
       : "memory");
 }
 
-// 32 rows x 16 bytes of shared memory into 32 lanes x 4 columns, repeated in all four lane
-// quarters (in a pair: in both CTAs, each from its own shared memory).  Runs in order with the
-// MMAs that the same thread issues after it.
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+// 32 lanes x 8 consecutive 32-bit columns of this warp's lane quarter (thread t writes lane t)
+__device__ __forceinline__ void tmem_store_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
-__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
-               : "memory");
+__device__ __forceinline__ void tmem_wait_stores() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread t of the warp receives
@@ -408,16 +415,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// Descriptor of a 512-byte block of scales (32 rows of 16 bytes, no swizzle): groups of 8 rows are
-// 128 bytes apart.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(128 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d;
 }
 
 // Instruction descriptor of tcgen05.mma.kind::mxf4: B scale byte bits 4-5, A format bits 7-9
