@@ -12,17 +12,19 @@
 //     that bound the kernel (855 cycles per 256 elements of k instead of 384, whatever else was
 //     left out).  For the same reason the scales' arrival counts on the operands' barrier;
 //   * a tile is 192 columns wide (96 gate + 96 up columns with the GLU).  Tensor memory has 512
-//     columns: two 192-column accumulators leave 64 columns beside each for the scales, two
-//     256-column ones would leave none;
+//     columns: two 192-column accumulators leave 128 for the scales, two 256-column ones would
+//     leave none;
 //   * the scales keep their natural row-major layout in global memory: TMA brings 32 bytes a row
 //     (1024 elements of k) of the tile's 128 + 192 rows into shared memory, and four warps, one
 //     per lane quarter, move them from there to tensor memory, transposed on the way: the tensor
 //     core wants, for 128 elements of k, row r's four scale bytes in lane r % 32 of column r / 32,
-//     repeated in every lane quarter.  No padding of groups and no packing of the scales is needed,
+//     repeated in every lane quarter.  Every ring stage has scale columns of its own, so the scales
+//     run as far ahead as the operands (with two slots of 512 elements for three such stages the
+//     MMAs waited for them: 710 cycles per 256 elements).  No padding of groups and no packing of the scales is needed,
 //     and the row shift of a group's last tile is free.  (Loaded straight from global memory into
 //     registers and passed on through shared memory, the scales held the MMAs to 1350 cycles per
 //     256 elements of k.)
-// Warps: 0 TMA producer, 1 MMA issuer, 2-9 epilogue, 10-13 scales.  Zero rows are written by the
+// Warps: 0 operand producer, 1 MMA issuer, 2-9 epilogue, 10-13 scales, 14 scale producer.  Zero rows are written by the
 // epilogue warps when their tiles are done.
 #pragma once
 
@@ -35,16 +37,17 @@ namespace rd {
 constexpr int k4BK = 256;       // elements of k in 128 bytes of a row
 constexpr int k4BN = 192;       // output columns of a tile
 constexpr int k4Half = k4BN / 2;
-constexpr int k4Threads = 448;
+constexpr int k4Threads = 480;
 constexpr int k4ScaleWarps = 4;
-constexpr int k4Chunk = 512;    // elements of k of a tensor-memory scale slot
 constexpr int k4RawK = 1024;    // elements of k of a shared-memory scale slot (32 scale bytes a row)
 constexpr int k4RawSlots = 3;
 constexpr int k4RawA = kBM * 32;
 constexpr int k4RawBytes = (kBM + k4BN) * 32;
-// A tensor-memory slot holds the scales of 512 elements of k in the 64 columns beside an
-// accumulator: four words (128 elements each) of 4 columns for A's rows, then of 8 for B's.
-constexpr int k4SlotColB = 16;
+// Tensor memory: two accumulators, then the scale columns of each stage: per word (128 elements of
+// k) 4 columns for A's 128 rows, then per word 6 for B's 192.
+constexpr int k4ScaleCol = 2 * k4BN;
+constexpr int k4WordColsA = kBM / 32;
+constexpr int k4WordColsB = k4BN / 32;
 
 enum Gemm4Epi : int { k4EpiNone = 0, k4EpiGlu = 1, k4EpiGluQuant = 2 };
 
@@ -83,6 +86,10 @@ struct Tile4Cfg {
   static constexpr int kStageA = kSub * kSubA;
   static constexpr int kStageB = kSub * kSubB;
   static constexpr int kStageBytes = kStageA + kStageB;
+  static constexpr int kWords = 2 * kSub;              // scale words of a row per stage
+  static constexpr int kColsA = kWords * k4WordColsA;  // scale columns of a stage: A's, then B's
+  static constexpr int kCols = kColsA + kWords * k4WordColsB;
+  static_assert(k4ScaleCol + kStagesN * kCols <= kTmemCols, "tensor memory");
 };
 
 template <bool PAIR>
@@ -161,10 +168,13 @@ __global__ void __launch_bounds__(k4Threads, 1)
   uint8_t* sB = smem + S * Cfg::kStageA;
   Gemm4Shared<PAIR>& sh = *reinterpret_cast<Gemm4Shared<PAIR>*>(smem + S * Cfg::kStageBytes);
 
-  const int warp = threadIdx.x >> 5;
+  // the same in every lane of a warp, which the compiler cannot see of threadIdx.x >> 5
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh.abort_flag;
-  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  // rank in the cluster of two along x; the even CTA issues the MMAs
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;
+  const bool leader = rank == 0;
   const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
   const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
 
@@ -213,10 +223,9 @@ __global__ void __launch_bounds__(k4Threads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0;
+      int stage = 0;
+      uint32_t phase = 0;
       uint32_t pend_mask = 0, pend_par = 0;
-      uint32_t rpend_mask = 0, rpend_par = 0;  // raw slots whose copies may be in flight
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = decode_tile4<PAIR>(sh, args, t);
@@ -226,26 +235,6 @@ __global__ void __launch_bounds__(k4Threads, 1)
         const int brow1 = b_row_of<GLU>(tl.n_idx, k4Half, args.n_out);
         for (int kb = 0; kb < tl.nkb; ++kb) {
           const int k0 = kb * Cfg::kSub * k4BK;
-          if (k0 % k4RawK == 0) {
-            // the scales of the next 1024 elements of k: A's rows of this CTA, all B rows of the tile
-            if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rempty[slot]), slot_phase ^ 1, abort_flag, tlimit)) {
-              ok = false;
-              break;
-            }
-            const uint32_t rb = ptx::smem_addr(&sh.rfull[slot]);
-            const uint32_t dst = ptx::smem_addr(sh.raw[slot]);
-            ptx::mbar_arrive_expect_tx(rb, k4RawBytes);
-            const int x = k0 / (2 * kMxBlock);  // two scale bytes a map element
-            ptx::tma_load_2d(dst, &maps.a_scales, rb, x, arow);
-            ptx::tma_load_3d(dst + k4RawA, &maps.b_scales, rb, x, brow0, tl.j);
-            ptx::tma_load_3d(dst + k4RawA + k4Half * 32, &maps.b_scales, rb, x, brow1, tl.j);
-            rpend_mask |= 1u << slot;
-            rpend_par = (rpend_par & ~(1u << slot)) | (slot_phase << slot);
-            if (++slot == k4RawSlots) {
-              slot = 0;
-              slot_phase ^= 1;
-            }
-          }
           const uint32_t fb_local = ptx::smem_addr(&sh.full[stage]);
           const uint32_t fb = PAIR ? ptx::map_to_rank(fb_local, 0) : fb_local;
           const uint32_t a_dst = ptx::smem_addr(sA + stage * Cfg::kStageA);
@@ -283,17 +272,12 @@ __global__ void __launch_bounds__(k4Threads, 1)
       }
       // Leave only once every fill has been consumed.  Unwinding, a fill's barrier may never
       // complete (it also counts the scale warps, and in a pair the even CTA's holds the odd CTA's
-      // copies): the copies in flight get a grace period instead.  The scales' copies count on
-      // barriers of their own.
-      volatile int no_abort = 0;
+      // copies): the copies in flight get a grace period instead.
       if (!*abort_flag) {
         for (int s = 0; s < S; ++s)
           if (pend_mask & (1u << s))
             ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), (pend_par >> s) & 1u, abort_flag, kDrainNs);
       }
-      for (int s = 0; s < k4RawSlots; ++s)
-        if (rpend_mask & (1u << s))
-          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rfull[s]), (rpend_par >> s) & 1u, &no_abort, kDrainNs);
       if (*abort_flag) {
         const uint64_t t0 = ptx::global_timer_ns();
         while (ptx::global_timer_ns() - t0 < kGraceNs) __nanosleep(1000);
@@ -301,70 +285,79 @@ __global__ void __launch_bounds__(k4Threads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the loop, so that what the MMAs take (descriptors, tensor-memory
+    // addresses) is known to be the same in every lane and stays in uniform registers; one elected
+    // lane issues.  A wait that gives up only raises the abort flag: the MMAs after it compute on
+    // whatever is there, and the loop is left at the next tile.
+    if (leader) {
       constexpr uint32_t idesc0 = ptx::idesc_mxfp4_f32(TM, k4BN, 0);
       constexpr uint32_t idesc2 = ptx::idesc_mxfp4_f32(TM, k4BN, 2);
       // operand descriptors of stage 0; a stage, and a K step of 32 bytes, move the address field
       const uint64_t a_desc0 = ptx::sw128_desc(ptx::smem_addr(sA), 16, 1024);
       const uint64_t b_desc0 = ptx::sw128_desc(ptx::smem_addr(sB), 16, 1024);
+      const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
+      const int tiles = __shfl_sync(0xFFFFFFFFu, total, 0);
       int stage = 0, acc = 0;
       uint32_t acc_phase = 0, full_phase = 0;
-      uint32_t slot = 0;  // tensor-memory slot of the scales
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = decode_tile4<PAIR>(sh, args, t);
-        if (tl.nkb == 0) continue;
-        ok = ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag, tlimit);
-        if (!ok) break;
-        const uint32_t d_tmem = sh.tmem_base + static_cast<uint32_t>(acc * kBN);
-        for (int kb = 0; kb < tl.nkb; ++kb) {
+      // every tile has the same stages, so none need be decoded here
+      const int nkb = (args.kc + Cfg::kSub * k4BK - 1) / (Cfg::kSub * k4BK);
+      for (int t = unit; t < tiles && nkb > 0; t += units) {
+        ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag, tlimit);
+        __syncwarp();
+        if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) break;
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * k4BN);
+        for (int kb = 0; kb < nkb; ++kb) {
           const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage * (Cfg::kStageA >> 4));
           const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage * (Cfg::kStageB >> 4));
-          // this stage's words of the scale slot (512 elements of k a slot)
-          const int word0 = (kb * Cfg::kSub * 2) & 3;
-          const uint32_t sfa = sh.tmem_base + k4BN + slot * kBN + word0 * 4;
-          const uint32_t sfb = sh.tmem_base + k4BN + slot * kBN + k4SlotColB + word0 * 8;
-          const bool last = kb == tl.nkb - 1;
+          const uint32_t sfa = tmem + k4ScaleCol + static_cast<uint32_t>(stage * Cfg::kCols);
+          const uint32_t sfb = sfa + Cfg::kColsA;
           constexpr int kSteps = 4 * Cfg::kSub;
-          const int steps = last ? (args.kc - kb * Cfg::kSub * k4BK + 63) / 64 : kSteps;
-          ok = PAIR ? ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit)
-                    : ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit);
-          if (!ok) break;
+          const int left = (args.kc - kb * Cfg::kSub * k4BK + 63) / 64;
+          const int steps = left < kSteps ? left : kSteps;
+          ptx::mbar_wait_bounded_cluster(ptx::smem_addr(&sh.full[stage]), full_phase, abort_flag, tlimit);
+          __syncwarp();
           ptx::tc_fence_after();
-          auto mma = [&](int kk, uint32_t accum) {
-            const uint64_t ak = ad + (kk >> 2) * (Cfg::kSubA >> 4) + (kk & 3) * 2;
-            const uint64_t bk = bd + (kk >> 2) * (Cfg::kSubB >> 4) + (kk & 3) * 2;
-            const uint32_t fa = sfa + (kk >> 1) * 4, fb = sfb + (kk >> 1) * 8;
-            const uint32_t id = (kk & 1) ? idesc2 : idesc0;
-            if (PAIR) ptx::tc_mma_mxfp4_pair(d_tmem, ak, bk, id, fa, fb, accum);
-            else ptx::tc_mma_mxfp4(d_tmem, ak, bk, id, fa, fb, accum);
-          };
-          if (steps == kSteps) {
-            mma(0, kb > 0 ? 1u : 0u);
+          if (ptx::elect_one()) {
+            auto mma = [&](int kk, uint32_t accum) {
+              const uint64_t ak = ad + (kk >> 2) * (Cfg::kSubA >> 4) + (kk & 3) * 2;
+              const uint64_t bk = bd + (kk >> 2) * (Cfg::kSubB >> 4) + (kk & 3) * 2;
+              const uint32_t fa = sfa + (kk >> 1) * k4WordColsA, fb = sfb + (kk >> 1) * k4WordColsB;
+              const uint32_t id = (kk & 1) ? idesc2 : idesc0;
+              if (PAIR) ptx::tc_mma_mxfp4_pair(d_tmem, ak, bk, id, fa, fb, accum);
+              else ptx::tc_mma_mxfp4(d_tmem, ak, bk, id, fa, fb, accum);
+            };
+            if (steps == kSteps) {
+              mma(0, kb > 0 ? 1u : 0u);
 #pragma unroll
-            for (int kk = 1; kk < kSteps; ++kk) mma(kk, 1u);
-          } else {
+              for (int kk = 1; kk < kSteps; ++kk) mma(kk, 1u);
+            } else {
 #pragma unroll 1
-            for (int kk = 0; kk < steps; ++kk) mma(kk, (kb > 0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < steps; ++kk) mma(kk, (kb > 0 || kk > 0) ? 1u : 0u);
+            }
+            if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.empty[stage]), 0x3);
+            else ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
           }
-          if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.empty[stage]), 0x3);
-          else ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
-          if (word0 + 2 * Cfg::kSub == 4 || last) slot ^= 1;
+          __syncwarp();
           if (++stage == S) {
             stage = 0;
             full_phase ^= 1;
           }
         }
-        if (!ok) break;
-        if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.tfull[acc]), 0x3);
-        else ptx::tc_commit(ptx::smem_addr(&sh.tfull[acc]));
+        if (ptx::elect_one()) {
+          if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.tfull[acc]), 0x3);
+          else ptx::tc_commit(ptx::smem_addr(&sh.tfull[acc]));
+        }
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
       if (*abort_flag) {
+        // every MMA issued has completed before TMEM is freed
         volatile int no_abort = 0;
-        if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.drain), 0x1);
-        else ptx::tc_commit(ptx::smem_addr(&sh.drain));
+        if (ptx::elect_one()) {
+          if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.drain), 0x1);
+          else ptx::tc_commit(ptx::smem_addr(&sh.drain));
+        }
         ptx::mbar_wait_bounded(ptx::smem_addr(&sh.drain), 0, &no_abort, kDrainNs);
       }
     }
@@ -448,7 +441,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t tbase =
-          sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kBN);
+          sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * k4BN);
 #pragma unroll 1
       for (int c = half; c < kChunks; c += 2) {
         if (GLU) {
@@ -503,36 +496,85 @@ __global__ void __launch_bounds__(k4Threads, 1)
     } else {
       zero(out_q, static_cast<int64_t>(args.n_out) * 2);
     }
+  } else if (warp == k4Threads / 32 - 1) {
+    // ------------------------------------------------------------ scale producer
+    // The tiles' scales, 1024 elements of k at a time, as far ahead as the slots allow: A's rows of
+    // this CTA and all B rows of the tile.  (Issued together with the operands they arrived after
+    // them, small rows that they are, and still had to be moved.)
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0, pend_mask = 0, pend_par = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const Tile tl = decode_tile4<PAIR>(sh, args, t);
+        const int arow = tl.row_load + static_cast<int>(rank) * kBM;
+        const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
+        const int brow1 = b_row_of<GLU>(tl.n_idx, k4Half, args.n_out);
+        for (int k0 = 0; k0 < args.kc; k0 += k4RawK) {
+          ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rempty[slot]), phase ^ 1, abort_flag, tlimit);
+          if (!ok) break;
+          const uint32_t rb = ptx::smem_addr(&sh.rfull[slot]);
+          const uint32_t dst = ptx::smem_addr(sh.raw[slot]);
+          ptx::mbar_arrive_expect_tx(rb, k4RawBytes);
+          const int x = k0 / (2 * kMxBlock);  // two scale bytes a map element
+          ptx::tma_load_2d(dst, &maps.a_scales, rb, x, arow);
+          ptx::tma_load_3d(dst + k4RawA, &maps.b_scales, rb, x, brow0, tl.j);
+          ptx::tma_load_3d(dst + k4RawA + k4Half * 32, &maps.b_scales, rb, x, brow1, tl.j);
+          pend_mask |= 1u << slot;
+          pend_par = (pend_par & ~(1u << slot)) | (phase << slot);
+          if (++slot == k4RawSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // leave only once the last copy of each slot has landed
+      volatile int no_abort = 0;
+      for (int s = 0; s < k4RawSlots; ++s)
+        if (pend_mask & (1u << s))
+          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rfull[s]), (pend_par >> s) & 1u, &no_abort, kDrainNs);
+    }
   } else {
     // ------------------------------------------------------------ scales
     // Each of the four warps writes one lane quarter of tensor memory, which repeats the scales of
     // all rows: lane l holds those of rows l, 32 + l, ...  A raw row is 32 bytes, two halves of 16
-    // (512 elements of k) that the copy's 32-byte swizzle exchanges in every second group of four
-    // rows, which makes the 16-byte reads below free of bank conflicts.
+    // that the copy's 32-byte swizzle exchanges in every second group of four rows, which makes
+    // the reads below free of bank conflicts.
     const uint32_t full0 = PAIR ? ptx::map_to_rank(ptx::smem_addr(&sh.full[0]), 0)
                                 : ptx::smem_addr(&sh.full[0]);
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col0 = sh.tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + k4ScaleCol;
+    constexpr int kW = Cfg::kWords;
+    constexpr int kStageK = Cfg::kSub * k4BK;
+    constexpr int kRowsL = (kBM + k4BN) / 32;  // rows of a lane
     int raw_slot = 0, stage = 0;
-    uint32_t raw_phase = 0, slot = 0, phase = 0;
-    // per slot: the stage whose consumption frees it, and that fill's parity
-    int free_stage[2] = {-1, -1};
-    uint32_t free_par[2] = {0, 0};
-    const int blocks = args.kc / kMxBlock;  // scale bytes of a row that count
-    constexpr int kStagesPerChunk = 2 / Cfg::kSub;
+    uint32_t raw_phase = 0, phase = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
       const Tile tl = decode_tile4<PAIR>(sh, args, t);
-      const int chunks = (args.kc + k4Chunk - 1) / k4Chunk;
-      for (int ch = 0; ch < chunks; ++ch) {
-        if ((ch & 1) == 0) {
+      for (int kb = 0; kb < tl.nkb; ++kb) {
+        const int k0 = kb * kStageK;
+        if (k0 % k4RawK == 0) {
           ok = warp_wait(ptx::smem_addr(&sh.rfull[raw_slot]), raw_phase, abort_flag, tlimit, lane);
           if (!ok) break;
         }
-        const uint8_t* src = sh.raw[raw_slot] + lane * 32 + (((ch & 1) ^ ((lane >> 2) & 1)) * 16);
-        uint4 v[10];  // rows 0 .. 127 of A, 0 .. 191 of B, 32 apart
+        const int at = (k0 % k4RawK) / kMxBlock;  // first byte of the stage in a raw row
+        const uint8_t* src = sh.raw[raw_slot] + lane * 32 + ((at ^ ((lane << 2) & 16)));
+        uint32_t v[kRowsL][kW];
 #pragma unroll
-        for (int i = 0; i < 10; ++i) v[i] = *reinterpret_cast<const uint4*>(src + i * 32 * 32);
-        if ((ch & 1) || ch == chunks - 1) {
+        for (int i = 0; i < kRowsL; ++i) {
+          if constexpr (kW == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + i * 32 * 32);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][2] = x.z;
+            v[i][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(src + i * 32 * 32);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+          }
+        }
+        if ((k0 + kStageK) % k4RawK == 0 || kb == tl.nkb - 1) {
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.rempty[raw_slot]));
           if (++raw_slot == k4RawSlots) {
@@ -541,54 +583,50 @@ __global__ void __launch_bounds__(k4Threads, 1)
           }
         }
         // bytes past the end of k meet zero operands: they must not be NaN
-        const int valid = blocks - ch * 16;
-        if (valid < 16) {
-          auto keep = [&](uint32_t x, int w) {
-            const int nb = valid - 4 * w;
-            return nb >= 4 ? x : (nb <= 0 ? 0u : x & ((1u << (8 * nb)) - 1u));
-          };
+        const int valid = (args.kc - k0) / kMxBlock;
+        if (valid < 4 * kW) {
 #pragma unroll
-          for (int i = 0; i < 10; ++i)
-            v[i] = make_uint4(keep(v[i].x, 0), keep(v[i].y, 1), keep(v[i].z, 2), keep(v[i].w, 3));
+          for (int w = 0; w < kW; ++w) {
+            const int nb = valid - 4 * w;
+            const uint32_t keep = nb >= 4 ? 0xFFFFFFFFu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
+#pragma unroll
+            for (int i = 0; i < kRowsL; ++i) v[i][w] &= keep;
+          }
         }
-        if (free_stage[slot] >= 0) {
-          ok = warp_wait(ptx::smem_addr(&sh.empty[free_stage[slot]]), free_par[slot], abort_flag, tlimit, lane);
-          if (!ok) break;
+        // the stage's columns, in the order of tensor memory
+        uint32_t c[Cfg::kCols];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+#pragma unroll
+          for (int i = 0; i < k4WordColsA; ++i) c[w * k4WordColsA + i] = v[i][w];
+#pragma unroll
+          for (int i = 0; i < k4WordColsB; ++i)
+            c[Cfg::kColsA + w * k4WordColsB + i] = v[k4WordColsA + i][w];
         }
+        // free once the stage's previous MMAs are done, as for the producer
+        ok = warp_wait(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, tlimit, lane);
+        if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t col = sh.tmem_base + lane_base + k4BN + slot * kBN;
-        const uint32_t a01[8] = {v[0].x, v[1].x, v[2].x, v[3].x, v[0].y, v[1].y, v[2].y, v[3].y};
-        const uint32_t a23[8] = {v[0].z, v[1].z, v[2].z, v[3].z, v[0].w, v[1].w, v[2].w, v[3].w};
-        const uint32_t b0[8] = {v[4].x, v[5].x, v[6].x, v[7].x, v[8].x, v[9].x, 0, 0};
-        const uint32_t b1[8] = {v[4].y, v[5].y, v[6].y, v[7].y, v[8].y, v[9].y, 0, 0};
-        const uint32_t b2[8] = {v[4].z, v[5].z, v[6].z, v[7].z, v[8].z, v[9].z, 0, 0};
-        const uint32_t b3[8] = {v[4].w, v[5].w, v[6].w, v[7].w, v[8].w, v[9].w, 0, 0};
-        ptx::tmem_store_8cols(col, a01);
-        ptx::tmem_store_8cols(col + 8, a23);
-        ptx::tmem_store_8cols(col + k4SlotColB, b0);
-        ptx::tmem_store_8cols(col + k4SlotColB + 8, b1);
-        ptx::tmem_store_8cols(col + k4SlotColB + 16, b2);
-        ptx::tmem_store_8cols(col + k4SlotColB + 24, b3);
+        const uint32_t col = col0 + static_cast<uint32_t>(stage * Cfg::kCols);
+        if constexpr (kW == 4) {
+          ptx::tmem_store_32cols(col, c);
+          ptx::tmem_store_8cols(col + 32, c + 32);
+        } else {
+          ptx::tmem_store_16cols(col, c);
+          ptx::tmem_store_4cols(col + 16, c + 16);
+        }
         ptx::tmem_wait_stores();
         ptx::tc_fence_before();
         __syncwarp();
-        // the chunk's stages (one of a pair, up to two of a single CTA) may be consumed
-#pragma unroll
-        for (int i = 0; i < kStagesPerChunk; ++i) {
-          if (ch * kStagesPerChunk + i >= tl.nkb) break;
-          if (lane == 0) {
-            const uint32_t b = full0 + static_cast<uint32_t>(stage * sizeof(uint64_t));
-            if (PAIR) ptx::mbar_arrive_cluster_tmem(b);
-            else ptx::mbar_arrive(b);
-          }
-          free_stage[slot] = stage;
-          free_par[slot] = phase;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-          }
+        if (lane == 0) {
+          const uint32_t b = full0 + static_cast<uint32_t>(stage * sizeof(uint64_t));
+          if (PAIR) ptx::mbar_arrive_cluster_tmem(b);
+          else ptx::mbar_arrive(b);
         }
-        slot ^= 1;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
   }
