@@ -26,6 +26,7 @@ struct RouteArgs {
   int32_t score;
   int32_t renormalize;
   float scale;
+  bool vec;              // rows start on vector boundaries (set by the launcher)
 };
 
 cudaError_t launch_route(const RouteArgs& a, int dtype, int sms, cudaStream_t stream);

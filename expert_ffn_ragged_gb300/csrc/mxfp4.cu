@@ -2,6 +2,7 @@
 //
 // HBM streams: quantisation reads 2 bytes an element and writes 17/32 (times topk when the rows go
 // to their packed places at once), dequantisation the other way round.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,61 +37,106 @@ __device__ __forceinline__ uint32_t pack_scaled(uint4 v, float inv) {
   return mx_pack8(f);
 }
 
-// A warp takes 256 elements of a row: lane i eight of them, four lanes a block.
+constexpr int kQuantBatch = 4;  // pieces of 256 elements of a row that a warp has in flight
+
+// A warp takes up to four pieces of 256 elements of a row: lane i eight of each, four lanes a block.
+template <bool SEND>
 __global__ void __launch_bounds__(kQuantThreads) mxfp4_quantize_kernel(const QuantArgs a) {
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.rows);
-  const int pieces = (a.k + 255) / 256;
-  const int64_t units = static_cast<int64_t>(L) * pieces;
-  const uint4* x = static_cast<const uint4*>(a.x);
   const int vecs = a.k / 8, blocks = a.k / kMxBlock;
+  const unsigned runs = (vecs + 32 * kQuantBatch - 1) / (32 * kQuantBatch);  // of four pieces, a row
+  const int64_t units = static_cast<int64_t>(L) * runs;
+  const uint4* x = static_cast<const uint4*>(a.x);
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5); u < units;
        u += static_cast<int64_t>(gridDim.x) * kQuantWarps) {
-    const int64_t r = u / pieces;
-    const int piece = static_cast<int>(u - r * pieces);
-    const int v = piece * 32 + lane;
-    uint4 xv = make_uint4(0, 0, 0, 0);
-    if (v < vecs) xv = x[r * vecs + v];
-    uint32_t m = amax8(xv);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t sb = mx_scale_byte(m);
-    uint32_t codes = pack_scaled(xv, mx_inverse(sb));
-    if (sb == 255u) codes = 0;  // inf * 0 is NaN: the codes of such a block are 0
-    const int block = piece * 8 + (lane >> 2);
+    const int64_t r = units <= 0xFFFFFFFFll ? static_cast<unsigned>(u) / runs : u / runs;
+    const int run = static_cast<int>(u - r * runs);
+    const int v0 = run * 32 * kQuantBatch + lane;
+    uint4 xv[kQuantBatch];
+    uint32_t codes[kQuantBatch], sb[kQuantBatch];
+#pragma unroll
+    for (int b = 0; b < kQuantBatch; ++b) {
+      xv[b] = make_uint4(0, 0, 0, 0);
+      if (v0 + 32 * b < vecs) xv[b] = __ldg(x + r * vecs + v0 + 32 * b);
+    }
+    const int32_t p_lane = SEND && lane < a.topk ? a.pos[r * a.topk + lane] : -1;
+#pragma unroll
+    for (int b = 0; b < kQuantBatch; ++b) {
+      uint32_t m = amax8(xv[b]);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      sb[b] = mx_scale_byte(m);
+      codes[b] = sb[b] == 255u ? 0u : pack_scaled(xv[b], mx_inverse(sb[b]));  // inf * 0 is NaN
+    }
     auto put = [&](int64_t row) {
-      if (v < vecs) reinterpret_cast<uint32_t*>(a.q + row * (a.k / 2))[v] = codes;
+      uint32_t* q = reinterpret_cast<uint32_t*>(a.q + row * (a.k / 2));
       uint8_t* s = a.scales + row * a.scale_width;
-      if ((lane & 3) == 0 && block < blocks) s[block] = static_cast<uint8_t>(sb);
-      if (piece == pieces - 1 && blocks + lane < a.scale_width) s[blocks + lane] = 0;
+#pragma unroll
+      for (int b = 0; b < kQuantBatch; ++b) {
+        const int v = v0 + 32 * b;
+        if (v < vecs) {
+          q[v] = codes[b];
+          if ((lane & 3) == 0) s[v >> 2] = static_cast<uint8_t>(sb[b]);
+        }
+      }
+      if (run == static_cast<int>(runs) - 1 && blocks + lane < a.scale_width) s[blocks + lane] = 0;
     };
-    if (a.pos == nullptr) {
+    if (!SEND) {
       put(r);
     } else {
       for (int k = 0; k < a.topk; ++k) {
-        const int32_t p = a.pos[r * a.topk + k];
+        const int32_t p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
         if (p >= 0 && p < a.out_rows) put(p);
       }
     }
   }
 }
 
+// two values of a byte of codes
+__device__ __forceinline__ float2 code_pair(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 lo, hi;\n\t"
+      "mov.b16 {lo, hi}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, lo;\n\t}"
+      : "=r"(h)
+      : "h"(static_cast<unsigned short>(byte)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A warp takes up to four pieces of 256 elements of a row, as above.
 __global__ void __launch_bounds__(kQuantThreads)
     mxfp4_dequantize_kernel(const QuantArgs a, uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.rows);
   const int vecs = a.k / 8;
-  const int64_t units = static_cast<int64_t>(L) * vecs;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x; u < units;
-       u += static_cast<int64_t>(gridDim.x) * kQuantThreads) {
-    const int64_t r = u / vecs;
-    const int v = static_cast<int>(u - r * vecs);
-    const uint32_t c = reinterpret_cast<const uint32_t*>(a.q)[u];
-    const float s = mx_scale(a.scales[r * a.scale_width + v / 4]);
-    float f[8];
+  const unsigned runs = (vecs + 32 * kQuantBatch - 1) / (32 * kQuantBatch);
+  const int64_t units = static_cast<int64_t>(L) * runs;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5); u < units;
+       u += static_cast<int64_t>(gridDim.x) * kQuantWarps) {
+    const int64_t r = units <= 0xFFFFFFFFll ? static_cast<unsigned>(u) / runs : u / runs;
+    const int v0 = static_cast<int>(u - r * runs) * 32 * kQuantBatch + lane;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + r * (a.k / 2));
+    const uint8_t* s = a.scales + r * a.scale_width;
+    uint32_t c[kQuantBatch], sb[kQuantBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = mx_code_value(c >> (4 * i)) * s;
-    out[u] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                        pack_bf16x2(f[6], f[7]));
+    for (int b = 0; b < kQuantBatch; ++b) {
+      const int v = v0 + 32 * b;
+      c[b] = v < vecs ? __ldg(q + v) : 0u;
+      sb[b] = v < vecs ? __ldg(s + (v >> 2)) : 0u;
+    }
+#pragma unroll
+    for (int b = 0; b < kQuantBatch; ++b) {
+      if (v0 + 32 * b >= vecs) break;
+      const float f = mx_scale(sb[b]);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = code_pair((c[b] >> (8 * i)) & 0xFFu);
+        w[i] = pack_bf16x2(v.x * f, v.y * f);
+      }
+      out[r * vecs + v0 + 32 * b] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -138,16 +184,17 @@ int quant_grid(int64_t blocks, int sms) {
 }  // namespace
 
 cudaError_t launch_mxfp4_quantize(const QuantArgs& a, int sms, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 255) / 256);
-  mxfp4_quantize_kernel<<<quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms), kQuantThreads, 0,
-                          stream>>>(a);
+  const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
+  const int grid = quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms);
+  if (a.pos != nullptr) mxfp4_quantize_kernel<true><<<grid, kQuantThreads, 0, stream>>>(a);
+  else mxfp4_quantize_kernel<false><<<grid, kQuantThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_mxfp4_dequantize(const QuantArgs& a, void* out, int sms, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(a.rows) * (a.k / 8);
-  mxfp4_dequantize_kernel<<<quant_grid((units + kQuantThreads - 1) / kQuantThreads, sms),
-                            kQuantThreads, 0, stream>>>(a, static_cast<uint4*>(out));
+  const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
+  mxfp4_dequantize_kernel<<<quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms), kQuantThreads, 0,
+                            stream>>>(a, static_cast<uint4*>(out));
   return cudaGetLastError();
 }
 

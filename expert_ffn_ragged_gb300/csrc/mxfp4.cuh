@@ -44,13 +44,4 @@ __device__ __forceinline__ uint32_t mx_pack8(const float (&v)[8]) {
   return r;
 }
 
-// magnitude bits of a code (0..7) as f32: 0, 0.5, then 1 + m / 2 times 2^e
-__device__ __forceinline__ float mx_code_value(uint32_t code) {
-  const uint32_t mag = code & 7u;
-  // magnitudes 2..7 are normal numbers: exponent (mag >> 1) - 1, one mantissa bit
-  const float normal = __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-  const float v = mag < 2u ? 0.5f * static_cast<float>(mag) : normal;
-  return (code & 8u) ? -v : v;
-}
-
 }  // namespace rd

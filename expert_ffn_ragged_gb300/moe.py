@@ -74,28 +74,78 @@ def declare(lib):
         fn.restype = ctypes.c_int
 
 
-def _check_tensor(t, name, shape, dtype):
-    """t must be a contiguous CUDA tensor of this dtype and shape (None: any extent)."""
-    if (t.dtype != dtype or t.dim() != len(shape) or not t.is_cuda or not t.is_contiguous()
-            or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
-                         f"{['any' if w is None else w for w in shape]}")
+# A call's host work is part of its latency, so the checks below are written out where a helper
+# would cost more than it checks: dtype objects are compared by identity, shapes as tuples, devices
+# as indices, and the settings of a router are marshalled once.
+
+def _refuse(name, shape, dtype, idx):
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{idx}")
 
 
-def _given(t, name, shape, dtype, device):
-    """The caller's output buffer after its checks, or a new one."""
+def _want(t, name, shape, dtype, idx):
+    """t must be a contiguous tensor of this dtype and shape on CUDA device idx."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+        _refuse(name, shape, dtype, idx)
+
+
+def _matrix(t, name, dtype):
+    """Extents and device index of the matrix that a call's other tensors are held against."""
+    if t.dtype is not dtype or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D {dtype} CUDA tensor")
+    rows, cols = t.shape
+    return rows, cols, t.get_device()
+
+
+def _word(t, name, idx):
+    """The address of an optional one-element int32 tensor."""
     if t is None:
-        return _rd._torch().empty(shape, dtype=dtype, device=device)
-    _check_tensor(t, name, shape, dtype)
-    return t
+        return None
+    if t.dtype is not _rd._torch().int32 or t.numel() != 1 or t.get_device() != idx:
+        raise ValueError(f"{name} must be a one-element int32 tensor on cuda:{idx}")
+    return t.data_ptr()
 
 
-def _logits_type(logits):
+_current_device = None
+
+
+def _launch(fn, name, idx, device, stream, *args):
+    """Call an entry point on the tensors' device, on its current stream or ``stream``."""
+    global _current_device
+    if _current_device is None:
+        torch = _rd._torch()
+        # without the lazy-initialisation check of the public function, where it exists
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    handle = _rd._stream(stream, device)
+    if _current_device() == idx:
+        code = fn(*args, handle)
+    else:
+        with _rd._on_device(device):
+            code = fn(*args, handle)
+    if code != 0:
+        _rd._check(code, name)
+
+
+_configs = {}
+
+
+def _config(*settings):
+    """rd_route_config of these settings, by reference (one object for each set of settings)."""
+    c = _configs.get(settings)
+    if c is None:
+        if len(_configs) >= 256:
+            _configs.clear()
+        c = _configs[settings] = ctypes.byref(_RouteConfig(*settings))
+    return c
+
+
+def _logits(logits):
     torch = _rd._torch()
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype = logits.dtype
+    if dtype is torch.float32:
+        return (_F32,) + _matrix(logits, "logits", dtype)
+    if dtype is not torch.bfloat16:
         raise ValueError("logits must be float32 or bfloat16")
-    _check_tensor(logits, "logits", (None, None), logits.dtype)
-    return _F32 if logits.dtype == torch.float32 else _BF16
+    return (_BF16,) + _matrix(logits, "logits", dtype)
 
 
 def route(logits, topk: int, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1,
@@ -106,140 +156,128 @@ def route(logits, topk: int, score: int = SCORE_SOFTMAX, bias=None, groups: int 
     ``topk_groups`` defaults to all groups.  ``out``: a Routing of buffers to write into.
     """
     torch = _rd._torch()
-    lib = _rd.load()
-    dtype = _logits_type(logits)
-    tokens, experts = logits.shape
-    dev = logits.device
+    lib = _rd._lib or _rd.load()
+    dtype, tokens, experts, idx = _logits(logits)
+    dev, i32 = logits.device, torch.int32
+    slots = (tokens, topk)
+    if out is None:
+        empty = torch.empty
+        out = Routing(empty(slots, dtype=i32, device=dev), empty(slots, dtype=torch.float32, device=dev),
+                      empty((experts,), dtype=i32, device=dev), empty(slots, dtype=i32, device=dev),
+                      empty((1,), dtype=i32, device=dev))
+    else:
+        _want(out.ids, "ids", slots, i32, idx)
+        _want(out.weights, "weights", slots, torch.float32, idx)
+        _want(out.group_sizes, "group_sizes", (experts,), i32, idx)
+        _want(out.pos, "pos", slots, i32, idx)
+        _want(out.rows, "rows", (1,), i32, idx)
     if bias is not None:
-        _check_tensor(bias, "bias", (experts,), torch.float32)
-    _rd._scalar_i32(limit, "limit")
-    o = out if out is not None else Routing(None, None, None, None, None)
-    i32 = torch.int32
-    r = Routing(_given(o.ids, "ids", (tokens, topk), i32, dev),
-                _given(o.weights, "weights", (tokens, topk), torch.float32, dev),
-                _given(o.group_sizes, "group_sizes", (experts,), i32, dev),
-                _given(o.pos, "pos", (tokens, topk), i32, dev),
-                _given(o.rows, "rows", (1,), i32, dev))
-    _rd._same_device(dev, bias, limit, *r)
-    cfg = _RouteConfig(int(topk), int(score), int(groups),
-                       int(groups if topk_groups is None else topk_groups), int(bool(renormalize)),
-                       float(scale))
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_route(ptr(logits), dtype, ptr(bias), tokens, experts, ctypes.byref(cfg),
-                            ptr(limit), ptr(r.ids), ptr(r.weights), ptr(r.group_sizes), ptr(r.pos),
-                            ptr(r.rows), _rd._stream(stream, dev))
-    _rd._check(code, "rd_route")
-    return r
+        _want(bias, "bias", (experts,), torch.float32, idx)
+        bias = bias.data_ptr()
+    cfg = _config(topk, score, groups, groups if topk_groups is None else topk_groups,
+                  1 if renormalize else 0, scale)
+    ids, weights, sizes, pos, rows = out
+    _launch(lib.rd_route, "rd_route", idx, dev, stream, logits.data_ptr(), dtype, bias, tokens, experts,
+            cfg, _word(limit, "limit", idx), ids.data_ptr(), weights.data_ptr(), sizes.data_ptr(),
+            pos.data_ptr(), rows.data_ptr())
+    return out
 
 
 def route_bwd(logits, ids, d_weights, score: int = SCORE_SOFTMAX, renormalize: bool = True,
               scale: float = 1.0, limit=None, out=None, stream=None):
     """Gradient of the logits from that of the weights (rd_route_bwd); settings as in ``route``."""
     torch = _rd._torch()
-    lib = _rd.load()
-    dtype = _logits_type(logits)
-    tokens, experts = logits.shape
-    dev = logits.device
-    _check_tensor(ids, "ids", (tokens, None), torch.int32)
-    _check_tensor(d_weights, "d_weights", tuple(ids.shape), torch.float32)
-    _rd._scalar_i32(limit, "limit")
-    out = _given(out, "out", (tokens, experts), logits.dtype, dev)
-    _rd._same_device(dev, ids, d_weights, limit, out)
-    cfg = _RouteConfig(ids.shape[1], int(score), 1, 1, int(bool(renormalize)), float(scale))
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_route_bwd(ptr(logits), dtype, ptr(ids), ptr(d_weights), tokens, experts,
-                                ctypes.byref(cfg), ptr(limit), ptr(out), _rd._stream(stream, dev))
-    _rd._check(code, "rd_route_bwd")
+    lib = _rd._lib or _rd.load()
+    dtype, tokens, experts, idx = _logits(logits)
+    topk = ids.shape[-1] if ids.dim() == 2 else 0
+    _want(ids, "ids", (tokens, topk), torch.int32, idx)
+    _want(d_weights, "d_weights", (tokens, topk), torch.float32, idx)
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _want(out, "out", (tokens, experts), logits.dtype, idx)
+    cfg = _config(topk, score, 1, 1, 1 if renormalize else 0, scale)
+    _launch(lib.rd_route_bwd, "rd_route_bwd", idx, logits.device, stream, logits.data_ptr(), dtype,
+            ids.data_ptr(), d_weights.data_ptr(), tokens, experts, cfg, _word(limit, "limit", idx),
+            out.data_ptr())
     return out
 
 
 def sort_rows(ids, experts: int, limit=None, stream=None):
     """(group_sizes [experts], pos [tokens, topk], rows [1]) of expert ids (rd_sort_rows)."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(ids, "ids", (None, None), torch.int32)
-    _rd._scalar_i32(limit, "limit")
-    tokens, topk = ids.shape
+    lib = _rd._lib or _rd.load()
+    i32 = torch.int32
+    tokens, topk, idx = _matrix(ids, "ids", i32)
     dev = ids.device
-    sizes = torch.empty((max(int(experts), 0),), dtype=torch.int32, device=dev)
+    sizes = torch.empty((max(int(experts), 0),), dtype=i32, device=dev)
     pos = torch.empty_like(ids)
-    rows = torch.empty((1,), dtype=torch.int32, device=dev)
-    _rd._same_device(dev, limit)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_sort_rows(ptr(ids), tokens, topk, int(experts), ptr(limit), ptr(sizes), ptr(pos),
-                                ptr(rows), _rd._stream(stream, dev))
-    _rd._check(code, "rd_sort_rows")
+    rows = torch.empty((1,), dtype=i32, device=dev)
+    _launch(lib.rd_sort_rows, "rd_sort_rows", idx, dev, stream, ids.data_ptr(), tokens, topk, int(experts),
+            _word(limit, "limit", idx), sizes.data_ptr(), pos.data_ptr(), rows.data_ptr())
     return sizes, pos, rows
 
 
 def dispatch_rows(x, pos, out_rows: Optional[int] = None, limit=None, out=None, stream=None):
     """out[pos[t, k]] = x[t] (rd_dispatch_rows); out_rows defaults to tokens * topk."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(x, "x", (None, None), torch.bfloat16)
-    tokens, hidden = x.shape
-    _check_tensor(pos, "pos", (tokens, None), torch.int32)
-    _rd._scalar_i32(limit, "limit")
-    topk, dev = pos.shape[1], x.device
-    n = tokens * topk if out_rows is None else int(out_rows)
-    if out is not None and out_rows is None:
-        n = out.shape[0]
-    out = _given(out, "out", (n, hidden), torch.bfloat16, dev)
-    _rd._same_device(dev, pos, limit, out)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_dispatch_rows(ptr(x), ptr(pos), ptr(out), tokens, topk, hidden, n, ptr(limit),
-                                    _rd._stream(stream, dev))
-    _rd._check(code, "rd_dispatch_rows")
+    lib = _rd._lib or _rd.load()
+    bf16 = torch.bfloat16
+    tokens, hidden, idx = _matrix(x, "x", bf16)
+    topk = pos.shape[-1] if pos.dim() == 2 else 0
+    _want(pos, "pos", (tokens, topk), torch.int32, idx)
+    if out_rows is None:
+        out_rows = tokens * topk if out is None else out.shape[0]
+    if out is None:
+        out = torch.empty((out_rows, hidden), dtype=bf16, device=x.device)
+    else:
+        _want(out, "out", (out_rows, hidden), bf16, idx)
+    _launch(lib.rd_dispatch_rows, "rd_dispatch_rows", idx, x.device, stream, x.data_ptr(), pos.data_ptr(),
+            out.data_ptr(), tokens, topk, hidden, out_rows, _word(limit, "limit", idx))
     return out
 
 
 def combine_rows(y, pos, w=None, limit=None, out=None, stream=None):
     """out[t] = sum_k w[t, k] y[pos[t, k]] (rd_combine_rows); without ``w`` every weight is one."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(y, "y", (None, None), torch.bfloat16)
-    _check_tensor(pos, "pos", (None, None), torch.int32)
-    tokens, topk = pos.shape
+    lib = _rd._lib or _rd.load()
+    bf16 = torch.bfloat16
+    rows, hidden, idx = _matrix(y, "y", bf16)
+    tokens, topk = pos.shape if pos.dim() == 2 else (0, 0)
+    _want(pos, "pos", (tokens, topk), torch.int32, idx)
     if w is not None:
-        _check_tensor(w, "w", (tokens, topk), torch.float32)
-    _rd._scalar_i32(limit, "limit")
-    rows, hidden = y.shape
-    dev = y.device
-    out = _given(out, "out", (tokens, hidden), torch.bfloat16, dev)
-    _rd._same_device(dev, pos, w, limit, out)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_combine_rows(ptr(y), ptr(pos), ptr(w), ptr(out), tokens, topk, hidden, rows,
-                                   ptr(limit), _rd._stream(stream, dev))
-    _rd._check(code, "rd_combine_rows")
+        _want(w, "w", (tokens, topk), torch.float32, idx)
+        w = w.data_ptr()
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=bf16, device=y.device)
+    else:
+        _want(out, "out", (tokens, hidden), bf16, idx)
+    _launch(lib.rd_combine_rows, "rd_combine_rows", idx, y.device, stream, y.data_ptr(), pos.data_ptr(), w,
+            out.data_ptr(), tokens, topk, hidden, rows, _word(limit, "limit", idx))
     return out
 
 
 def combine_rows_bwd(d_out, y, pos, w, limit=None, d_y=None, d_w=None, stream=None):
     """(d_y, d_w) of ``combine_rows`` (rd_combine_rows_bwd)."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(y, "y", (None, None), torch.bfloat16)
-    rows, hidden = y.shape
-    _check_tensor(d_out, "d_out", (None, hidden), torch.bfloat16)
-    tokens = d_out.shape[0]
-    _check_tensor(pos, "pos", (tokens, None), torch.int32)
-    topk = pos.shape[1]
-    _check_tensor(w, "w", (tokens, topk), torch.float32)
-    _rd._scalar_i32(limit, "limit")
-    dev = y.device
-    d_y = _given(d_y, "d_y", (rows, hidden), torch.bfloat16, dev)
-    d_w = _given(d_w, "d_w", (tokens, topk), torch.float32, dev)
-    _rd._same_device(dev, d_out, pos, w, limit, d_y, d_w)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_combine_rows_bwd(ptr(d_out), ptr(y), ptr(pos), ptr(w), ptr(d_y), ptr(d_w), tokens,
-                                       topk, hidden, rows, ptr(limit), _rd._stream(stream, dev))
-    _rd._check(code, "rd_combine_rows_bwd")
+    lib = _rd._lib or _rd.load()
+    bf16, f32 = torch.bfloat16, torch.float32
+    rows, hidden, idx = _matrix(y, "y", bf16)
+    tokens, topk = pos.shape if pos.dim() == 2 else (0, 0)
+    _want(d_out, "d_out", (tokens, hidden), bf16, idx)
+    _want(pos, "pos", (tokens, topk), torch.int32, idx)
+    _want(w, "w", (tokens, topk), f32, idx)
+    if d_y is None:
+        d_y = torch.empty_like(y)
+    else:
+        _want(d_y, "d_y", (rows, hidden), bf16, idx)
+    if d_w is None:
+        d_w = torch.empty_like(w)
+    else:
+        _want(d_w, "d_w", (tokens, topk), f32, idx)
+    _launch(lib.rd_combine_rows_bwd, "rd_combine_rows_bwd", idx, y.device, stream, d_out.data_ptr(),
+            y.data_ptr(), pos.data_ptr(), w.data_ptr(), d_y.data_ptr(), d_w.data_ptr(), tokens, topk, hidden,
+            rows, _word(limit, "limit", idx))
     return d_y, d_w
 
 
@@ -252,65 +290,62 @@ def mxfp4_quantize(x, pos=None, out_rows: Optional[int] = None, limit=None,
                    out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
     """bf16 rows [rows, k] to 4-bit rows; with ``pos`` straight to their packed rows (rd_mxfp4_quantize)."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(x, "x", (None, None), torch.bfloat16)
-    rows, k = x.shape
-    dev = x.device
-    topk = 1
+    lib = _rd._lib or _rd.load()
+    u8 = torch.uint8
+    rows, k, idx = _matrix(x, "x", torch.bfloat16)
+    topk, at = 1, None
     if pos is not None:
-        _check_tensor(pos, "pos", (rows, None), torch.int32)
-        topk = pos.shape[1]
-    _rd._scalar_i32(limit, "limit")
-    n = rows * topk if out_rows is None else int(out_rows)
-    o = out if out is not None else Mxfp4(None, None)
-    if out is not None and out_rows is None:
-        n = out.q.shape[0]
-    q = _given(o.q, "q", (n, k // 2), torch.uint8, dev)
-    scales = _given(o.scales, "scales", (n, mxfp4_scale_width(k)), torch.uint8, dev)
-    _rd._same_device(dev, pos, limit, q, scales)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_mxfp4_quantize(ptr(x), ptr(pos), ptr(q), ptr(scales), rows, topk, k, n, ptr(limit),
-                                     _rd._stream(stream, dev))
-    _rd._check(code, "rd_mxfp4_quantize")
-    return Mxfp4(q, scales)
+        topk = pos.shape[-1] if pos.dim() == 2 else 0
+        _want(pos, "pos", (rows, topk), torch.int32, idx)
+        at = pos.data_ptr()
+    if out_rows is None:
+        out_rows = rows * topk if out is None else out.q.shape[0]
+    width = mxfp4_scale_width(k)
+    if out is None:
+        dev = x.device
+        out = Mxfp4(torch.empty((out_rows, k // 2), dtype=u8, device=dev),
+                    torch.empty((out_rows, width), dtype=u8, device=dev))
+    else:
+        _want(out.q, "q", (out_rows, k // 2), u8, idx)
+        _want(out.scales, "scales", (out_rows, width), u8, idx)
+    _launch(lib.rd_mxfp4_quantize, "rd_mxfp4_quantize", idx, x.device, stream, x.data_ptr(), at,
+            out.q.data_ptr(), out.scales.data_ptr(), rows, topk, k, out_rows, _word(limit, "limit", idx))
+    return out
 
 
 def mxfp4_quantize_weights(rhs, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
     """Expert weights [g, k, n] bf16 to 4-bit rows along k: q [g, n, k / 2] (rd_mxfp4_quantize_weights)."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(rhs, "rhs", (None, None, None), torch.bfloat16)
+    lib = _rd._lib or _rd.load()
+    u8 = torch.uint8
+    if rhs.dtype is not torch.bfloat16 or rhs.dim() != 3 or not rhs.is_cuda or not rhs.is_contiguous():
+        raise ValueError("rhs must be a contiguous [g, k, n] bf16 CUDA tensor")
     g, k, n = rhs.shape
-    dev = rhs.device
-    o = out if out is not None else Mxfp4(None, None)
-    q = _given(o.q, "q", (g, n, k // 2), torch.uint8, dev)
-    scales = _given(o.scales, "scales", (g, n, mxfp4_scale_width(k)), torch.uint8, dev)
-    _rd._same_device(dev, q, scales)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_mxfp4_quantize_weights(ptr(rhs), ptr(q), ptr(scales), g, k, n,
-                                             _rd._stream(stream, dev))
-    _rd._check(code, "rd_mxfp4_quantize_weights")
-    return Mxfp4(q, scales)
+    idx, dev, width = rhs.get_device(), rhs.device, mxfp4_scale_width(k)
+    if out is None:
+        out = Mxfp4(torch.empty((g, n, k // 2), dtype=u8, device=dev),
+                    torch.empty((g, n, width), dtype=u8, device=dev))
+    else:
+        _want(out.q, "q", (g, n, k // 2), u8, idx)
+        _want(out.scales, "scales", (g, n, width), u8, idx)
+    _launch(lib.rd_mxfp4_quantize_weights, "rd_mxfp4_quantize_weights", idx, dev, stream, rhs.data_ptr(),
+            out.q.data_ptr(), out.scales.data_ptr(), g, k, n)
+    return out
 
 
 def mxfp4_dequantize(q, scales, limit=None, out=None, stream=None):
     """The values of 4-bit rows [rows, k / 2] as bf16 [rows, k] (rd_mxfp4_dequantize)."""
     torch = _rd._torch()
-    lib = _rd.load()
-    _check_tensor(q, "q", (None, None), torch.uint8)
-    rows, k = q.shape[0], 2 * q.shape[1]
-    _check_tensor(scales, "scales", (rows, mxfp4_scale_width(k)), torch.uint8)
-    _rd._scalar_i32(limit, "limit")
-    dev = q.device
-    out = _given(out, "out", (rows, k), torch.bfloat16, dev)
-    _rd._same_device(dev, scales, limit, out)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_mxfp4_dequantize(ptr(q), ptr(scales), ptr(out), rows, k, ptr(limit),
-                                       _rd._stream(stream, dev))
-    _rd._check(code, "rd_mxfp4_dequantize")
+    lib = _rd._lib or _rd.load()
+    rows, half, idx = _matrix(q, "q", torch.uint8)
+    k = 2 * half
+    _want(scales, "scales", (rows, mxfp4_scale_width(k)), torch.uint8, idx)
+    if out is None:
+        out = torch.empty((rows, k), dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", (rows, k), torch.bfloat16, idx)
+    _launch(lib.rd_mxfp4_dequantize, "rd_mxfp4_dequantize", idx, q.device, stream, q.data_ptr(),
+            scales.data_ptr(), out.data_ptr(), rows, k, _word(limit, "limit", idx))
     return out
 
 
@@ -321,30 +356,36 @@ def ragged_dot_mxfp4(a, a_scales, b, b_scales, group_sizes, group_offset: int = 
     EPI_NONE and EPI_SILU_GLU give bf16 rows, EPI_SILU_GLU_MXFP4 an Mxfp4 of 4-bit rows.
     """
     torch = _rd._torch()
-    lib = _rd.load()
+    lib = _rd._lib or _rd.load()
     u8 = torch.uint8
-    _check_tensor(a, "a", (None, None), u8)
-    m, k = a.shape[0], 2 * a.shape[1]
-    _check_tensor(b, "b", (None, None, k // 2), u8)
-    g_local, n = b.shape[0], b.shape[1]
+    m, half, idx = _matrix(a, "a", u8)
+    if b.dim() != 3:
+        raise ValueError("b must be [g_local, n, k / 2]")
+    g_local, n, k = b.shape[0], b.shape[1], 2 * half
     width = mxfp4_scale_width(k)
-    _check_tensor(a_scales, "a_scales", (m, width), u8)
-    _check_tensor(b_scales, "b_scales", (g_local, n, width), u8)
-    _rd._group_args(group_sizes, limit, status)
-    dev = a.device
-    if epilogue == EPI_SILU_GLU_MXFP4:
-        out = _given(out, "out", (m, n // 4), u8, dev)
-        out_scales = _given(out_scales, "out_scales", (m, mxfp4_scale_width(n // 2)), u8, dev)
+    _want(b, "b", (g_local, n, half), u8, idx)
+    _want(a_scales, "a_scales", (m, width), u8, idx)
+    _want(b_scales, "b_scales", (g_local, n, width), u8, idx)
+    g_total = group_sizes.numel()
+    _want(group_sizes, "group_sizes", (g_total,), torch.int32, idx)
+    quant = epilogue == EPI_SILU_GLU_MXFP4
+    if quant:
+        shape, dtype = (m, n // 4), u8
+        scale_shape = (m, mxfp4_scale_width(n // 2))
+        if out_scales is None:
+            out_scales = torch.empty(scale_shape, dtype=u8, device=a.device)
+        else:
+            _want(out_scales, "out_scales", scale_shape, u8, idx)
     else:
+        shape, dtype = (m, n // 2 if epilogue == _rd.EPI_SILU_GLU else n), torch.bfloat16
         if out_scales is not None:
             raise ValueError("out_scales belongs to EPI_SILU_GLU_MXFP4")
-        out = _given(out, "out", (m, n // 2 if epilogue == _rd.EPI_SILU_GLU else n), torch.bfloat16, dev)
-    _rd._same_device(dev, a_scales, b, b_scales, group_sizes, limit, status, out, out_scales)
-    ptr = _rd._ptr
-    with _rd._on_device(dev):
-        code = lib.rd_ragged_dot_mxfp4(ptr(a), ptr(a_scales), ptr(b), ptr(b_scales), ptr(out),
-                                       ptr(out_scales), m, k, n, ptr(group_sizes), group_sizes.numel(),
-                                       int(group_offset), g_local, ptr(limit), int(epilogue),
-                                       ptr(status), _rd._stream(stream, dev))
-    _rd._check(code, "rd_ragged_dot_mxfp4")
-    return out if out_scales is None else Mxfp4(out, out_scales)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=a.device)
+    else:
+        _want(out, "out", shape, dtype, idx)
+    _launch(lib.rd_ragged_dot_mxfp4, "rd_ragged_dot_mxfp4", idx, a.device, stream, a.data_ptr(),
+            a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), out.data_ptr(),
+            out_scales.data_ptr() if quant else None, m, k, n, group_sizes.data_ptr(), g_total,
+            group_offset, g_local, _word(limit, "limit", idx), epilogue, _word(status, "status", idx))
+    return Mxfp4(out, out_scales) if quant else out
