@@ -4,18 +4,20 @@
 // One warp owns a token; lane l holds the EPL consecutive experts from l * EPL in registers, so a
 // row is read in 16-byte vectors and a lower lane always means a lower expert index.
 //
-// Choice: up to 8 keys a lane are sorted once (a network of stable compare-exchanges), and each of
-// the topk rounds is one warp-wide maximum of the lanes' heads, a ballot for the lowest lane that
-// has it, and a pop in that lane.  More keys a lane (over 256 experts) are scanned in every round,
-// as sorting them would cost more than the rounds.  The two largest keys of a group, where groups are whole lanes, are two
-// maxima over the group's lanes.
+// Choice: topk warp-wide maxima over the lanes' largest keys give the topk-th largest of these; no
+// key below it can be chosen, and the few that are left (hardly more than topk) are gathered in
+// shared memory and ranked against each other.  Popping the best key topk times, with the keys of
+// a lane sorted first, took 1.3 times the instructions.  The two largest keys of a group, where
+// groups are whole lanes, are two maxima over the group's lanes.
 //
-// Bound: instructions, not memory.  At 32771 x 256 in f32 (36.7 MB: 5.4 us at the measured copy
-// rate) a token costs some 500 warp instructions, a third of them the exp and the reciprocal of
-// the sigmoid, whose exact f32 values the choice is defined by.
+// Bound: instructions, not memory: at 32771 x 256 in f32 (36.7 MB: 5.4 us at the measured copy
+// rate) the exp and the reciprocal of the sigmoid, whose exact f32 values the choice is defined by,
+// are a third of them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "moe_args.h"
 
@@ -35,9 +37,20 @@ __device__ __forceinline__ int32_t tokens_below(const int32_t* limit, int32_t to
   return v < 0 ? 0 : (v > tokens ? tokens : v);
 }
 
-// the logistic in the elementwise f32 arithmetic that the keys are defined by (a correctly rounded
-// reciprocal is the division 1 / x)
-__device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
+// The correctly rounded 1 / d for d in [1, inf]: the hardware approximation and one Newton step with
+// fused multiply-adds, r + r (1 - d r), which rounds correctly when r is within an ulp (P. Markstein,
+// IA-64 and Elementary Functions, 2000, for all mantissas but the one of all ones).  Checked
+// against the correctly rounded reciprocal for every float of [1, 2) and all exponents.  Where 1 / d
+// would be subnormal, and at infinity, the step is left out for the exact operation.
+__device__ __forceinline__ float reciprocal_rn(float d) {
+  if (!(d < 1.0e37f)) return __frcp_rn(d);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
+}
+
+// the logistic in the elementwise f32 arithmetic that the keys are defined by
+__device__ __forceinline__ float sigmoid_f32(float l) { return reciprocal_rn(__fadd_rn(1.0f, expf(-l))); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -126,27 +139,6 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, int e0, int expert
   }
 }
 
-constexpr int kSortedKeys = 8;  // keys a lane sorts rather than scans
-
-// Sort this lane's keys, largest first, equal keys by index: an odd-even transposition network
-// (only neighbours are exchanged, and only when strictly out of order, which keeps it stable).
-template <int EPL>
-__device__ __forceinline__ void sort_keys(float (&key)[EPL], int (&idx)[EPL]) {
-#pragma unroll
-  for (int round = 0; round < EPL; ++round) {
-#pragma unroll
-    for (int i = round & 1; i + 1 < EPL; i += 2) {
-      const bool swap = key[i] < key[i + 1];
-      const float a = swap ? key[i + 1] : key[i], b = swap ? key[i] : key[i + 1];
-      const int ia = swap ? idx[i + 1] : idx[i], ib = swap ? idx[i] : idx[i + 1];
-      key[i] = a;
-      key[i + 1] = b;
-      idx[i] = ia;
-      idx[i + 1] = ib;
-    }
-  }
-}
-
 // What a slot's weight is made of, in the lane that holds the slot: part (its exp or sigmoid) and
 // the warp-wide sum it is divided by (1 for sigmoid scores as they are).  ex: the exps of this
 // lane's logits, filled for softmax scores over all experts.
@@ -179,9 +171,13 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
 }
 
 template <int EPL, class T>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
-  extern __shared__ float smem_keys[];  // [warps][experts], for groups that are not whole lanes
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
+  // per warp: the keys of the candidates [32 * EPL], their experts [32 * EPL], the chosen ids [32]
+  extern __shared__ float smem_route[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* ckey = smem_route + warp * (64 * EPL + 32);
+  int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL);
+  int* chosen = cexp + 32 * EPL;
   const int32_t L = tokens_below(a.limit, a.tokens);
   const T* logits = static_cast<const T*>(a.logits);
   const int gsize = a.experts / a.groups;
@@ -191,10 +187,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   const int lpg = lane_groups ? gsize / EPL : 1;
   const int my_group = lane / lpg;
   const unsigned group_mask = (lpg >= 32 ? kAll : ((1u << lpg) - 1u)) << (my_group * lpg);
-  float bias[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    bias[i] = a.bias != nullptr && e0 + i < a.experts ? a.bias[e0 + i] : 0.0f;
   const int stride = gridDim.x * kRouteWarps;
   int t = blockIdx.x * kRouteWarps + warp;
   float next[EPL];
@@ -202,7 +194,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   for (; t < L; t += stride) {
     const T* row = logits + static_cast<int64_t>(t) * a.experts;
     float logit[EPL], key[EPL];
-    int idx[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) logit[i] = next[i];
     if (t + stride < L)  // the next token's row, under this one's work
@@ -210,59 +201,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       float k = a.score == RD_SCORE_SOFTMAX ? logit[i] : sigmoid_f32(logit[i]);
-      if (a.bias != nullptr) k = __fadd_rn(k, bias[i]);
+      if (a.bias != nullptr) k = __fadd_rn(k, e0 + i < a.experts ? __ldg(a.bias + e0 + i) : 0.0f);
       key[i] = is_masked(logit[i]) || is_masked(k) ? kLow : k;
-      idx[i] = i;
     }
-    if (a.groups > 1 && !lane_groups) {
-      // groups across lane boundaries: lane g scores group g from shared memory, and the experts
-      // of the groups that are not kept are masked before the sort
-      float* sk = smem_keys + warp * a.experts;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (e0 + i < a.experts) sk[e0 + i] = key[i];
-      __syncwarp();
-      float score = kLow;
-      if (lane < a.groups) {
-        float first = kLow, second = kLow;
-        for (int e = lane * gsize; e < (lane + 1) * gsize; ++e) {
-          const float v = sk[e];
-          second = fmaxf(second, fminf(first, v));
-          first = fmaxf(first, v);
-        }
-        score = first;
-        if (a.score == RD_SCORE_SIGMOID && second > kLow) score = __fadd_rn(first, second);
-      }
-      uint32_t kept = 0;
-      for (int r = 0; r < a.topk_groups; ++r) {
-        const float best = lanes_max(score, kAll);
-        if (!(best > kLow)) break;
-        const int g = __ffs(__ballot_sync(kAll, score == best)) - 1;
-        kept |= 1u << g;
-        if (lane == g) score = kLow;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (e0 + i < a.experts && !((kept >> ((e0 + i) / gsize)) & 1u)) key[i] = kLow;
-    }
-    constexpr bool kSorted = EPL <= kSortedKeys;
-    if (kSorted) sort_keys<EPL>(key, idx);
+    float mine1 = key[0];  // this lane's largest key
     if (a.groups > 1 && lane_groups) {
+      float mine2 = kLow;
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) {
+        mine2 = fmaxf(mine2, fminf(mine1, key[i]));
+        mine1 = fmaxf(mine1, key[i]);
+      }
       // the group's largest key; then its second largest, for which the (lowest) lane that has
       // the largest offers its own second
       float score = kLow;
       if (my_group < a.groups) {
-        float mine1 = key[0], mine2 = kLow;
-        if (kSorted) {
-          if (EPL > 1) mine2 = key[EPL > 1 ? 1 : 0];
-        } else {
-#pragma unroll
-          for (int i = 1; i < EPL; ++i) {
-            mine2 = fmaxf(mine2, fminf(mine1, key[i]));
-            mine1 = fmaxf(mine1, key[i]);
-          }
-        }
         const float first = lanes_max(mine1, group_mask);
         score = first;
         if (a.score == RD_SCORE_SIGMOID) {
@@ -273,62 +226,109 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
         }
       }
       __syncwarp();
-      bool mine = false;
+      bool kept = false;
       for (int r = 0; r < a.topk_groups; ++r) {
         const float best = lanes_max(score, kAll);
         if (!(best > kLow)) break;
-        const int g = (__ffs(__ballot_sync(kAll, score == best)) - 1) / lpg;
-        if (my_group == g) {
-          mine = true;
+        const int first_lane = __ffs(__ballot_sync(kAll, score == best)) - 1;
+        if ((group_mask >> first_lane) & 1u) {
+          kept = true;
           score = kLow;
         }
       }
-      if (!mine) {
+      if (!kept) {
+        mine1 = kLow;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = kLow;
       }
-    }
-    int my_id = -1;
-    for (int k = 0; k < a.topk; ++k) {
-      float head = key[0];
-      if (!kSorted) {
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) head = fmaxf(head, key[i]);
-      }
-      const float best = lanes_max(head, kAll);
-      if (!(best > kLow)) break;
-      const int owner = __ffs(__ballot_sync(kAll, head == best)) - 1;
-      int at = idx[0];
-      if (kSorted) {
-        if (lane == owner) {
-#pragma unroll
-          for (int i = 0; i + 1 < EPL; ++i) {
-            key[i] = key[i + 1];
-            idx[i] = idx[i + 1];
-          }
-          key[EPL - 1] = kLow;
-        }
-      } else {
-#pragma unroll
-        for (int i = EPL - 1; i >= 0; --i)
-          if (key[i] == best) at = i;
+    } else {
+      if (a.groups > 1) {
+        // groups across lane boundaries: lane g scores group g from shared memory
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (lane == owner && i == at) key[i] = kLow;
+          if (e0 + i < a.experts) ckey[e0 + i] = key[i];
+        __syncwarp();
+        float score = kLow;
+        if (lane < a.groups) {
+          float first = kLow, second = kLow;
+          for (int e = lane * gsize; e < (lane + 1) * gsize; ++e) {
+            const float v = ckey[e];
+            second = fmaxf(second, fminf(first, v));
+            first = fmaxf(first, v);
+          }
+          score = first;
+          if (a.score == RD_SCORE_SIGMOID && second > kLow) score = __fadd_rn(first, second);
+        }
+        uint32_t kept = 0;
+        for (int r = 0; r < a.topk_groups; ++r) {
+          const float best = lanes_max(score, kAll);
+          if (!(best > kLow)) break;
+          const int g = __ffs(__ballot_sync(kAll, score == best)) - 1;
+          kept |= 1u << g;
+          if (lane == g) score = kLow;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (e0 + i < a.experts && !((kept >> ((e0 + i) / gsize)) & 1u)) key[i] = kLow;
+        mine1 = key[0];
       }
-      const int e = owner * EPL + __shfl_sync(kAll, at, owner);
-      if (lane == k) my_id = e;
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) mine1 = fmaxf(mine1, key[i]);
     }
+    // tau: the topk-th largest of the lanes' largest keys (-inf where fewer lanes have one)
+    float tau = kLow, rest = mine1;
+    for (int k = 0; k < a.topk; ++k) {
+      tau = lanes_max(rest, kAll);
+      if (!(tau > kLow)) break;
+      const unsigned has = __ballot_sync(kAll, rest == tau);
+      if (lane == __ffs(has) - 1) rest = kLow;
+    }
+    // the candidates, in the order of their experts
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) count += key[i] >= tau && key[i] > kLow ? 1 : 0;
+    int at = count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, at, d);
+      if (lane >= d) at += o;
+    }
+    const int total_c = __shfl_sync(kAll, at, 31);
+    at -= count;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (key[i] >= tau && key[i] > kLow) {
+        ckey[at] = key[i];
+        cexp[at] = e0 + i;
+        ++at;
+      }
+    }
+    chosen[lane] = -1;
+    __syncwarp();
+    // a candidate's rank: those with a larger key, and of equal ones the earlier
+    for (int c = lane; c < total_c; c += 32) {
+      const float mine = ckey[c];
+      int rank = 0;
+      for (int j = 0; j < total_c; ++j) {
+        const float other = ckey[j];
+        rank += other > mine || (other == mine && j < c) ? 1 : 0;
+      }
+      if (rank < a.topk) chosen[rank] = cexp[c];
+    }
+    __syncwarp();
+    const int my_id = lane < a.topk ? chosen[lane] : -1;
     const bool there = my_id >= 0;
-    const float at = there ? load_logit(row + my_id) : 0.0f;
+    const float own = there ? load_logit(row + my_id) : 0.0f;
     float part, total, ex[EPL];
-    slot_parts<EPL>(a, there, at, logit, ex, part, total);
+    slot_parts<EPL>(a, there, own, logit, ex, part, total);
     if (lane < a.topk) {
       const int64_t o = static_cast<int64_t>(t) * a.topk + lane;
       a.ids[o] = my_id;
       // !(total <= 0) lets a NaN sum through
       a.weights[o] = there && !(total <= 0.0f) ? __fmul_rn(__fdiv_rn(part, total), a.scale) : 0.0f;
     }
+    __syncwarp();  // the candidates are read: the next token may write its own
   }
 }
 
@@ -422,9 +422,19 @@ cudaError_t launch_epl(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
   if (bwd) {
     route_bwd_kernel<EPL, T><<<grid, kRouteWarps * 32, sizeof(float) * kRouteWarps * 32 * EPL, stream>>>(a);
   } else {
-    const bool shared = a.groups > 1 && (a.experts / a.groups) % EPL != 0;
-    route_kernel<EPL, T><<<grid, kRouteWarps * 32, shared ? sizeof(float) * kRouteWarps * a.experts : 0,
-                           stream>>>(a);
+    constexpr size_t smem = sizeof(float) * kRouteWarps * (64 * EPL + 32);
+    if (smem > 48 * 1024) {
+      static std::atomic<bool> attr_set[64];
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+      if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            route_kernel<EPL, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+      }
+    }
+    route_kernel<EPL, T><<<grid, kRouteWarps * 32, smem, stream>>>(a);
   }
   return cudaGetLastError();
 }
