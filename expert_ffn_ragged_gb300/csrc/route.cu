@@ -37,20 +37,36 @@ __device__ __forceinline__ int32_t tokens_below(const int32_t* limit, int32_t to
   return v < 0 ? 0 : (v > tokens ? tokens : v);
 }
 
-// The correctly rounded 1 / d for d in [1, inf]: the hardware approximation and one Newton step with
-// fused multiply-adds, r + r (1 - d r), which rounds correctly when r is within an ulp (P. Markstein,
-// IA-64 and Elementary Functions, 2000, for all mantissas but the one of all ones).  Checked
-// against the correctly rounded reciprocal for every float of [1, 2) and all exponents.  Where 1 / d
-// would be subnormal, and at infinity, the step is left out for the exact operation.
-__device__ __forceinline__ float reciprocal_rn(float d) {
-  if (!(d < 1.0e37f)) return __frcp_rn(d);
+// The correctly rounded 1 / d for d in [1, kFastRcp): the hardware approximation and one Newton step
+// with fused multiply-adds, r + r (1 - d r), which rounds correctly when r is within an ulp
+// (P. Markstein, IA-64 and Elementary Functions, 2000, for all mantissas but the one of all ones);
+// checked against the correctly rounded reciprocal for every float in the range.
+constexpr float kFastRcp = 1.0e37f;
+__device__ __forceinline__ float reciprocal_fast(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
 }
 
 // the logistic in the elementwise f32 arithmetic that the keys are defined by
-__device__ __forceinline__ float sigmoid_f32(float l) { return reciprocal_rn(__fadd_rn(1.0f, expf(-l))); }
+__device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
+
+// the same for a lane's logits, with one test for those so negative that 1 / d leaves the normal
+// numbers (a test for each made the branches as expensive as the arithmetic)
+template <int EPL>
+__device__ __forceinline__ void sigmoids_f32(const float (&l)[EPL], float (&s)[EPL]) {
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const float d = __fadd_rn(1.0f, expf(-l[i]));
+    s[i] = reciprocal_fast(d);
+    most = fmaxf(most, l[i] > kLow ? d : 0.0f);  // -inf is masked, whatever its sigmoid
+  }
+  if (!(most < kFastRcp)) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] = sigmoid_f32(l[i]);
+  }
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -142,11 +158,11 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, int e0, int expert
 // What a slot's weight is made of, in the lane that holds the slot: part (its exp or sigmoid) and
 // the warp-wide sum it is divided by (1 for sigmoid scores as they are).  ex: the exps of this
 // lane's logits, filled for softmax scores over all experts.
-template <int EPL>
+template <int EPL, int SCORE>
 __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float at,
                                            const float (&logit)[EPL], float (&ex)[EPL], float& part,
                                            float& total) {
-  if (a.score == RD_SCORE_SOFTMAX) {
+  if (SCORE == RD_SCORE_SOFTMAX) {
     float top = there ? at : kLow;
     if (!a.renormalize) {
 #pragma unroll
@@ -170,14 +186,25 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
   }
 }
 
-template <int EPL, class T>
+// Shared memory (words): the biases, then per warp the keys of the candidates (and four that never
+// win), their experts and the chosen ids.
+constexpr int route_warp_words(int epl) { return 32 * epl + 4 + 32 * epl + 4 + 32; }
+constexpr size_t route_smem_bytes(int epl) {
+  return sizeof(float) * (32 * epl + kRouteWarps * route_warp_words(epl));
+}
+
+template <int EPL, class T, int SCORE>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
-  // per warp: the keys of the candidates [32 * EPL], their experts [32 * EPL], the chosen ids [32]
-  extern __shared__ float smem_route[];
+  extern __shared__ __align__(16) float smem_route[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* ckey = smem_route + warp * (64 * EPL + 32);
-  int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL);
-  int* chosen = cexp + 32 * EPL;
+  float* sbias = smem_route;
+  float* ckey = sbias + 32 * EPL + warp * route_warp_words(EPL);
+  int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL + 4);
+  int* chosen = cexp + 32 * EPL + 4;
+  if (a.bias != nullptr) {
+    for (int e = threadIdx.x; e < 32 * EPL; e += kRouteWarps * 32) sbias[e] = e < a.experts ? a.bias[e] : 0.0f;
+    __syncthreads();
+  }
   const int32_t L = tokens_below(a.limit, a.tokens);
   const T* logits = static_cast<const T*>(a.logits);
   const int gsize = a.experts / a.groups;
@@ -198,12 +225,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     for (int i = 0; i < EPL; ++i) logit[i] = next[i];
     if (t + stride < L)  // the next token's row, under this one's work
       load_row<EPL>(row + static_cast<int64_t>(stride) * a.experts, e0, a.experts, a.vec, next);
+    if (SCORE == RD_SCORE_SIGMOID) {
+      sigmoids_f32<EPL>(logit, key);
+    } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      float k = a.score == RD_SCORE_SOFTMAX ? logit[i] : sigmoid_f32(logit[i]);
-      if (a.bias != nullptr) k = __fadd_rn(k, e0 + i < a.experts ? __ldg(a.bias + e0 + i) : 0.0f);
-      key[i] = is_masked(logit[i]) || is_masked(k) ? kLow : k;
+      for (int i = 0; i < EPL; ++i) key[i] = logit[i];
     }
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = __fadd_rn(key[i], sbias[e0 + i]);
+    }
+    // a masked logit's softmax key is -inf or NaN by itself; its sigmoid key is not
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      key[i] = (SCORE == RD_SCORE_SOFTMAX || logit[i] > kLow) && key[i] > kLow ? key[i] : kLow;
     float mine1 = key[0];  // this lane's largest key
     if (a.groups > 1 && lane_groups) {
       float mine2 = kLow;
@@ -218,7 +253,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
       if (my_group < a.groups) {
         const float first = lanes_max(mine1, group_mask);
         score = first;
-        if (a.score == RD_SCORE_SIGMOID) {
+        if (SCORE == RD_SCORE_SIGMOID) {
           const unsigned has = __ballot_sync(group_mask, mine1 == first);
           const float offer = lane == __ffs(has & group_mask) - 1 ? mine2 : mine1;
           const float second = lanes_max(offer, group_mask);
@@ -257,7 +292,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
             first = fmaxf(first, v);
           }
           score = first;
-          if (a.score == RD_SCORE_SIGMOID && second > kLow) score = __fadd_rn(first, second);
+          if (SCORE == RD_SCORE_SIGMOID && second > kLow) score = __fadd_rn(first, second);
         }
         uint32_t kept = 0;
         for (int r = 0; r < a.topk_groups; ++r) {
@@ -298,21 +333,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     at -= count;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (key[i] >= tau && key[i] > kLow) {
-        ckey[at] = key[i];
-        cexp[at] = e0 + i;
-        ++at;
-      }
+      const bool in = key[i] >= tau && key[i] > kLow;
+      if (in) ckey[at] = key[i];
+      if (in) cexp[at] = e0 + i;
+      at += in ? 1 : 0;
     }
+    if (lane < 4) ckey[total_c + lane] = kLow;
     chosen[lane] = -1;
     __syncwarp();
     // a candidate's rank: those with a larger key, and of equal ones the earlier
     for (int c = lane; c < total_c; c += 32) {
       const float mine = ckey[c];
       int rank = 0;
-      for (int j = 0; j < total_c; ++j) {
-        const float other = ckey[j];
-        rank += other > mine || (other == mine && j < c) ? 1 : 0;
+      for (int j = 0; j < total_c; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(ckey + j);
+        rank += (o.x > mine || (o.x == mine && j < c)) + (o.y > mine || (o.y == mine && j + 1 < c)) +
+                (o.z > mine || (o.z == mine && j + 2 < c)) + (o.w > mine || (o.w == mine && j + 3 < c));
       }
       if (rank < a.topk) chosen[rank] = cexp[c];
     }
@@ -321,7 +357,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     const bool there = my_id >= 0;
     const float own = there ? load_logit(row + my_id) : 0.0f;
     float part, total, ex[EPL];
-    slot_parts<EPL>(a, there, own, logit, ex, part, total);
+    slot_parts<EPL, SCORE>(a, there, own, logit, ex, part, total);
     if (lane < a.topk) {
       const int64_t o = static_cast<int64_t>(t) * a.topk + lane;
       a.ids[o] = my_id;
@@ -334,13 +370,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
 
 // The row's gradients are put together in shared memory, where the chosen experts add theirs to
 // what every expert gets, and leave in vectors.
-template <int EPL, class T>
+template <int EPL, class T, int SCORE>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const RouteArgs a) {
   extern __shared__ __align__(16) float smem_rows[];  // [warps][32 * EPL]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* srow = smem_rows + warp * 32 * EPL;
   const int32_t L = tokens_below(a.limit, a.tokens);
-  const bool dense = a.score == RD_SCORE_SOFTMAX && !a.renormalize;
+  const bool dense = SCORE == RD_SCORE_SOFTMAX && !a.renormalize;
   const int e0 = lane * EPL;
   const int stride = gridDim.x * kRouteWarps;
   const T* logits = static_cast<const T*>(a.logits);
@@ -369,7 +405,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     const float at = there ? load_logit(row + id) : 0.0f;
     if (t + stride < L) fetch(t + stride);
     float part, total, ex[EPL];
-    slot_parts<EPL>(a, there, at, logit, ex, part, total);
+    slot_parts<EPL, SCORE>(a, there, at, logit, ex, part, total);
     const float inv = !(total <= 0.0f) ? __fdiv_rn(1.0f, total) : 0.0f;
     const float q = part * inv;
     const float mean = warp_sum(there ? q * d : 0.0f);
@@ -388,7 +424,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     __syncwarp();
     if (there) {
       float g;
-      if (a.score == RD_SCORE_SOFTMAX) g = a.scale * q * (d - mean);
+      if (SCORE == RD_SCORE_SOFTMAX) g = a.scale * q * (d - mean);
       else g = a.scale * (a.renormalize ? (d - mean) * inv : d) * part * (1.0f - part);
       srow[id] = g;
     }
@@ -411,8 +447,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
   }
 }
 
-template <int EPL, class T>
-cudaError_t launch_epl(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
+template <int EPL, class T, int SCORE>
+cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
   const int64_t blocks = (a.tokens + kRouteWarps - 1) / kRouteWarps;
   const int grid = static_cast<int>(blocks < sms * 8 ? blocks : sms * 8);
   // rows and lanes start on vector boundaries (16 bytes of f32, 8 of bf16: four elements)
@@ -420,23 +456,30 @@ cudaError_t launch_epl(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
   a.vec = a.experts % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % unit == 0 &&
           reinterpret_cast<uintptr_t>(a.d_logits) % unit == 0;
   if (bwd) {
-    route_bwd_kernel<EPL, T><<<grid, kRouteWarps * 32, sizeof(float) * kRouteWarps * 32 * EPL, stream>>>(a);
-  } else {
-    constexpr size_t smem = sizeof(float) * kRouteWarps * (64 * EPL + 32);
-    if (smem > 48 * 1024) {
-      static std::atomic<bool> attr_set[64];
-      int dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-      if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            route_kernel<EPL, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        attr_set[dev].store(true, std::memory_order_release);
-      }
-    }
-    route_kernel<EPL, T><<<grid, kRouteWarps * 32, smem, stream>>>(a);
+    route_bwd_kernel<EPL, T, SCORE>
+        <<<grid, kRouteWarps * 32, sizeof(float) * kRouteWarps * 32 * EPL, stream>>>(a);
+    return cudaGetLastError();
   }
+  constexpr size_t smem = route_smem_bytes(EPL);
+  if (smem > 48 * 1024) {
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          route_kernel<EPL, T, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+      attr_set[dev].store(true, std::memory_order_release);
+    }
+  }
+  route_kernel<EPL, T, SCORE><<<grid, kRouteWarps * 32, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int EPL, class T>
+cudaError_t launch_epl(const RouteArgs& a, bool bwd, int sms, cudaStream_t stream) {
+  return a.score == RD_SCORE_SOFTMAX ? launch_score<EPL, T, RD_SCORE_SOFTMAX>(a, bwd, sms, stream)
+                                     : launch_score<EPL, T, RD_SCORE_SIGMOID>(a, bwd, sms, stream);
 }
 
 template <class T>
