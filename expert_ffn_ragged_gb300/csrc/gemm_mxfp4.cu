@@ -18,35 +18,32 @@ cudaError_t launch_impl(const Gemm4Maps& maps, const Gemm4Args& args, int grid, 
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  if (!PAIR) {
-    kernel<<<grid, k4Threads, smem, stream>>>(maps, args);
-    return cudaGetLastError();
+  if (PAIR) {
+    // as for the bf16 products: no more CTA pairs than can be resident at once
+    static std::atomic<int> max_clusters[64];
+    int clusters = max_clusters[dev].load(std::memory_order_acquire);
+    if (clusters == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+      cfg.blockDim = dim3(k4Threads, 1, 1);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      clusters = n > 0 ? n : 1;
+      max_clusters[dev].store(clusters, std::memory_order_release);
+    }
+    if (grid > 2 * clusters) grid = 2 * clusters;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(k4Threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // as for the bf16 products: no more CTA pairs than can be resident at once
-  static std::atomic<int> max_clusters[64];
-  int clusters = max_clusters[dev].load(std::memory_order_acquire);
-  if (clusters == 0) {
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    clusters = n > 0 ? n : 1;
-    max_clusters[dev].store(clusters, std::memory_order_release);
-  }
-  if (grid > 2 * clusters) grid = 2 * clusters;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kernel, maps, args);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), k4Threads, smem, PAIR ? 2 : 1, stream, maps,
+                    args);
 }
 
 template <bool PAIR>

@@ -29,6 +29,7 @@
 #pragma once
 
 #include "gemm_kernel.cuh"
+#include "launch.h"
 #include "moe_args.h"
 #include "mxfp4.cuh"
 
@@ -120,19 +121,46 @@ constexpr size_t gemm4_smem_bytes() {
          sizeof(Gemm4Shared<PAIR>);
 }
 
+// Tile t, as decode_tile_view has it.  A role's tiles only ever move forward, so the group is searched
+// from that of its last tile on (`hint`); the divisions are left out where a group is one m-tile
+// high, as in decoding, or one band.
 template <bool PAIR>
-__device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<PAIR>& sh, const Gemm4Args& a, int t) {
-  SchedView v;
-  v.bound = sh.bound;
-  v.tile_start = sh.tile_start;
-  v.group_offset = a.group_offset;
-  v.g_local = a.g_local;
-  v.n_tiles = a.n_tiles;
-  v.band_tiles = a.band_tiles;
-  v.dw_m_tiles = 0;
-  v.kc = a.kc;
-  Tile tl = decode_tile_view<kOpFwd, Tile4Cfg<PAIR>::kTileM>(v, t);
+__device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<PAIR>& sh, const Gemm4Args& a, int t,
+                                             int& hint) {
+  constexpr int TM = Tile4Cfg<PAIR>::kTileM;
   constexpr int kStageK = Tile4Cfg<PAIR>::kSub * k4BK;
+  int j = hint;
+  if (sh.tile_start[j + 1] <= t) {
+    int hi = a.g_local;  // tile_start[j] <= t < tile_start[hi]
+    while (hi - j > 1) {
+      const int mid = (j + hi) >> 1;
+      if (sh.tile_start[mid] <= t) j = mid;
+      else hi = mid;
+    }
+    hint = j;
+  }
+  Tile tl;
+  tl.j = j;
+  tl.rs = sh.bound[a.group_offset + j];
+  tl.re = sh.bound[a.group_offset + j + 1];
+  int u = t - sh.tile_start[j];
+  const int mt = (tl.re - tl.rs + TM - 1) / TM;
+  if (mt == 1) {
+    tl.m_idx = 0;
+    tl.n_idx = u;
+  } else {
+    int first = 0, bw = mt;
+    if (mt > a.band_tiles) {
+      const int per_band = a.band_tiles * a.n_tiles;
+      const int band = u / per_band;
+      u -= band * per_band;
+      first = band * a.band_tiles;
+      bw = min(a.band_tiles, mt - first);
+    }
+    tl.n_idx = u / bw;
+    tl.m_idx = first + u - tl.n_idx * bw;
+  }
+  tl.row_load = tl.m_idx == mt - 1 ? tl.re - TM : tl.rs + tl.m_idx * TM;
   tl.nkb = (a.kc + kStageK - 1) / kStageK;  // stages of the tile
   return tl;
 }
@@ -211,6 +239,9 @@ __global__ void __launch_bounds__(k4Threads, 1)
       ptx::tmem_relinquish();
     }
   }
+  // everything above touches no memory of the stream's earlier work
+  pdl_trigger();
+  pdl_wait();
   if (warp == 2) build_schedule<kOpFwd, TM>(sh, args, lane);
   ptx::tc_fence_before();
   __syncthreads();
@@ -219,6 +250,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
 
   const int total = sh.total_tiles;
   const uint64_t tlimit = args.timeout_ns;
+  int group = 0;  // of this role's last tile
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -228,7 +260,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       uint32_t pend_mask = 0, pend_par = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = decode_tile4<PAIR>(sh, args, t);
+        const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
         const int arow = tl.row_load + static_cast<int>(rank) * kBM;
         // the 96-row boxes of b: one per CTA of a pair, two on a single CTA
         const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
@@ -380,7 +412,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = unit; t < total; t += units) {
-      const Tile tl = decode_tile4<PAIR>(sh, args, t);
+      const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
       const int wrow0 = tl.row_load + static_cast<int>(rank) * kBM + q * 32;
       const int lo = tile_store_lo(tl, TM), hi = tile_store_hi(tl);
       const int col0 = tl.n_idx * tile_w;
@@ -402,6 +434,29 @@ __global__ void __launch_bounds__(k4Threads, 1)
             *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * args.n_out + c) = val;
         }
         __syncwarp();
+      };
+      // 64 columns of each row: whole 128-byte lines, 4 rows a store, in two passes of 16 rows
+      auto emit_wide = [&](const uint32_t (&p)[32], int col) {
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+          if ((lane >> 4) == pass) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              stg[(lane & 15) * 8 + (v ^ (lane & 7))] =
+                  make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int rl = it * 4 + (lane >> 3);
+            const uint4 val = stg[rl * 8 + ((lane & 7) ^ (rl & 7))];
+            const int row = wrow0 + pass * 16 + rl;
+            const int c = col + (lane & 7) * 8;
+            if (row >= lo && row < hi && c + 8 <= args.n_out)
+              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * args.n_out + c) = val;
+          }
+          __syncwarp();
+        }
       };
       // the same columns as a 4-bit block: 16 bytes of codes and a scale byte
       auto emit_quant = [&](const float (&h)[32], int col) {
@@ -442,9 +497,9 @@ __global__ void __launch_bounds__(k4Threads, 1)
       ptx::tc_fence_after();
       const uint32_t tbase =
           sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * k4BN);
+      if (GLU) {
 #pragma unroll 1
-      for (int c = half; c < kChunks; c += 2) {
-        if (GLU) {
+        for (int c = half; c < kChunks; c += 2) {
           uint32_t g[32], u[32];
           ptx::tmem_load_32cols(tbase + c * 32, g);
           ptx::tmem_load_32cols(tbase + k4Half + c * 32, u);
@@ -460,14 +515,26 @@ __global__ void __launch_bounds__(k4Threads, 1)
             for (int i = 0; i < 16; ++i) p[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
             emit(p, col0 + c * 32);
           }
-        } else {
-          uint32_t v[32], p[16];
-          ptx::tmem_load_32cols(tbase + c * 32, v);
+        }
+      } else {
+        // each of the two warps takes 96 columns: 64 that are whole lines and 32 that are not
+        const int wide = half == 0 ? 0 : 128, narrow = half == 0 ? 64 : 96;
+        uint32_t p[32];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t v[32];
+          ptx::tmem_load_32cols(tbase + wide + part * 32, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          emit(p, col0 + c * 32);
+            p[part * 16 + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
+        emit_wide(p, col0 + wide);
+        uint32_t v[32], pn[16];
+        ptx::tmem_load_32cols(tbase + narrow, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pn[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        emit(pn, col0 + narrow);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -506,7 +573,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       uint32_t phase = 0, pend_mask = 0, pend_par = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = decode_tile4<PAIR>(sh, args, t);
+        const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
         const int arow = tl.row_load + static_cast<int>(rank) * kBM;
         const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
         const int brow1 = b_row_of<GLU>(tl.n_idx, k4Half, args.n_out);
@@ -550,7 +617,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
     uint32_t raw_phase = 0, phase = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      const Tile tl = decode_tile4<PAIR>(sh, args, t);
+      const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
       for (int kb = 0; kb < tl.nkb; ++kb) {
         const int k0 = kb * kStageK;
         if (k0 % k4RawK == 0) {

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "glu_math.cuh"
+#include "launch.h"
 #include "moe_args.h"
 
 namespace rd {
@@ -32,6 +33,8 @@ __device__ __forceinline__ uint4 ld_row(const uint4* p) {
 }
 
 __global__ void __launch_bounds__(kRowThreads) dispatch_rows_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
@@ -68,6 +71,8 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], uint4 y, float w) {
 }
 
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int pieces = (a.vecs + 31) / 32;
@@ -106,6 +111,8 @@ __device__ __forceinline__ uint32_t scale_dot(uint32_t d, uint32_t y, float w, f
 }
 
 __global__ void __launch_bounds__(kRowThreads) combine_rows_bwd_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int64_t slots = static_cast<int64_t>(L) * a.topk;
@@ -153,19 +160,17 @@ int row_grid(int64_t units, int sms) {
 
 cudaError_t launch_dispatch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   const int64_t pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
-  dispatch_rows_kernel<<<row_grid(a.tokens * pieces, sms), kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(dispatch_rows_kernel, dim3(row_grid(a.tokens * pieces, sms)), kRowThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_combine_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   const int64_t pieces = (a.vecs + 31) / 32;
-  combine_rows_kernel<<<row_grid(a.tokens * pieces, sms), kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(combine_rows_kernel, dim3(row_grid(a.tokens * pieces, sms)), kRowThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_combine_rows_bwd(const RowsArgs& a, int sms, cudaStream_t stream) {
-  combine_rows_bwd_kernel<<<row_grid(static_cast<int64_t>(a.tokens) * a.topk, sms), kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(combine_rows_bwd_kernel, dim3(row_grid(static_cast<int64_t>(a.tokens) * a.topk, sms)),
+                    kRowThreads, 0, 1, stream, a);
 }
 
 }  // namespace rd

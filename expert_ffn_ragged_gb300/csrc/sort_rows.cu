@@ -18,6 +18,7 @@
 
 #include <atomic>
 
+#include "launch.h"
 #include "moe_args.h"
 
 namespace cg = cooperative_groups;
@@ -46,6 +47,8 @@ __global__ void __launch_bounds__(WARPS * 32)
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
   int32_t L = tokens;
   if (limit != nullptr) {
     const int32_t v = *limit;
@@ -185,20 +188,8 @@ cudaError_t launch_sort_rows(const int32_t* ids, int32_t tokens, int32_t topk, i
   const int64_t slots = static_cast<int64_t>(tokens) * topk;
   int ctas = 1;
   while (ctas < kSortCluster && slots > static_cast<int64_t>(ctas) * warps * 32 * kSortBatch) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(warps * 32, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * (2 * warps + 2) * experts;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ids, tokens, topk, experts, limit, group_sizes,
-                            pos, rows);
+  return launch_pdl(kernel, dim3(ctas), warps * 32, sizeof(uint32_t) * (2 * warps + 2) * experts, ctas,
+                    stream, ids, tokens, topk, experts, limit, group_sizes, pos, rows);
 }
 
 }  // namespace rd
