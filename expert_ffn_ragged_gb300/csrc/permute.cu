@@ -70,36 +70,62 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], uint4 y, float w) {
   }
 }
 
+// A warp owns B * 32 vectors of a token's row; the rows of S slots are in flight at once.
+template <int B, int S>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const RowsArgs a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
-  const int pieces = (a.vecs + 31) / 32;
+  const int pieces = (a.vecs + 32 * B - 1) / (32 * B);
   const int64_t units = static_cast<int64_t>(L) * pieces;
   const uint4* y = static_cast<const uint4*>(a.x);
   uint4* out = static_cast<uint4*>(a.out);
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units;
        u += static_cast<int64_t>(gridDim.x) * kRowWarps) {
     const int64_t t = u / pieces;
-    const int v = static_cast<int>(u - t * pieces) * 32 + lane;
+    const int v0 = static_cast<int>(u - t * pieces) * 32 * B + lane;
     int32_t p_lane = -1;
     float w_lane = 0.0f;
     if (lane < a.topk) {
       p_lane = a.pos[t * a.topk + lane];
       w_lane = a.w != nullptr ? a.w[t * a.topk + lane] : 1.0f;
     }
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-    for (int k = 0; k < a.topk; ++k) {
-      const int32_t p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
-      const float w = __shfl_sync(0xFFFFFFFFu, w_lane, k);
-      if (p >= 0 && p < a.packed_rows && v < a.vecs)
-        add_scaled(acc, ld_row(y + static_cast<int64_t>(p) * a.vecs + v), w);
+    float acc[B][8];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[b][i] = 0.0f;
+    for (int k0 = 0; k0 < a.topk; k0 += S) {
+      uint4 v[S][B];
+      float w[S];
+      bool on[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const int32_t p = __shfl_sync(0xFFFFFFFFu, p_lane, (k0 + i) & 31);
+        w[i] = __shfl_sync(0xFFFFFFFFu, w_lane, (k0 + i) & 31);
+        on[i] = k0 + i < a.topk && p >= 0 && p < a.packed_rows;
+        if (on[i]) {
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (v0 + 32 * b < a.vecs) v[i][b] = ld_row(y + static_cast<int64_t>(p) * a.vecs + v0 + 32 * b);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if (on[i]) {
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (v0 + 32 * b < a.vecs) add_scaled(acc[b], v[i][b], w[i]);
+        }
+      }
     }
-    if (v < a.vecs)
-      out[t * a.vecs + v] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                       pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (v0 + 32 * b < a.vecs)
+        out[t * a.vecs + v0 + 32 * b] =
+            make_uint4(pack_bf16x2(acc[b][0], acc[b][1]), pack_bf16x2(acc[b][2], acc[b][3]),
+                       pack_bf16x2(acc[b][4], acc[b][5]), pack_bf16x2(acc[b][6], acc[b][7]));
   }
 }
 
@@ -164,8 +190,15 @@ cudaError_t launch_dispatch_rows(const RowsArgs& a, int sms, cudaStream_t stream
 }
 
 cudaError_t launch_combine_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
-  const int64_t pieces = (a.vecs + 31) / 32;
-  return launch_pdl(combine_rows_kernel, dim3(row_grid(a.tokens * pieces, sms)), kRowThreads, 0, 1, stream, a);
+  // Enough work for every warp of the GPU (64 an SM): two vectors a lane and two slots at once.
+  // Less: one vector, so that a few tokens spread over more SMs, and up to four slots, since a warp
+  // has little else to hide a load behind.
+  const int64_t twos = static_cast<int64_t>(a.tokens) * ((a.vecs + 63) / 64);
+  if (twos >= 64 * static_cast<int64_t>(sms))
+    return launch_pdl(combine_rows_kernel<2, 2>, dim3(row_grid(twos, sms)), kRowThreads, 0, 1, stream, a);
+  const int64_t ones = static_cast<int64_t>(a.tokens) * ((a.vecs + 31) / 32);
+  return launch_pdl(a.topk > 2 ? combine_rows_kernel<1, 4> : combine_rows_kernel<1, 2>,
+                    dim3(row_grid(ones, sms)), kRowThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_combine_rows_bwd(const RowsArgs& a, int sms, cudaStream_t stream) {
