@@ -76,7 +76,8 @@ def declare(lib):
 
 # A call's host work is part of its latency, so the checks below are written out where a helper
 # would cost more than it checks: dtype objects are compared by identity, shapes as tuples, devices
-# as indices, and the settings of a router are marshalled once.
+# as indices, and the settings of a router are marshalled once.  An argument's name stays bound to its
+# tensor until the launch: it may be the last reference, and a new output would take its memory.
 
 def _refuse(name, shape, dtype, idx):
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{idx}")
@@ -125,6 +126,13 @@ def _launch(fn, name, idx, device, stream, *args):
         _rd._check(code, name)
 
 
+def _used_on(stream, *outputs):
+    """Outputs were allocated on the current stream and are written on ``stream`` (which the caller has
+    ordered after the inputs): their memory is not handed out again before that work is done."""
+    for t in outputs:
+        t.record_stream(stream)
+
+
 _configs = {}
 
 
@@ -171,15 +179,18 @@ def route(logits, topk: int, score: int = SCORE_SOFTMAX, bias=None, groups: int 
         _want(out.group_sizes, "group_sizes", (experts,), i32, idx)
         _want(out.pos, "pos", slots, i32, idx)
         _want(out.rows, "rows", (1,), i32, idx)
+    bias_at = None
     if bias is not None:
         _want(bias, "bias", (experts,), torch.float32, idx)
-        bias = bias.data_ptr()
+        bias_at = bias.data_ptr()
     cfg = _config(topk, score, groups, groups if topk_groups is None else topk_groups,
                   1 if renormalize else 0, scale)
     ids, weights, sizes, pos, rows = out
-    _launch(lib.rd_route, "rd_route", idx, dev, stream, logits.data_ptr(), dtype, bias, tokens, experts,
-            cfg, _word(limit, "limit", idx), ids.data_ptr(), weights.data_ptr(), sizes.data_ptr(),
+    _launch(lib.rd_route, "rd_route", idx, dev, stream, logits.data_ptr(), dtype, bias_at, tokens,
+            experts, cfg, _word(limit, "limit", idx), ids.data_ptr(), weights.data_ptr(), sizes.data_ptr(),
             pos.data_ptr(), rows.data_ptr())
+    if stream is not None:
+        _used_on(stream, *out)
     return out
 
 
@@ -200,6 +211,8 @@ def route_bwd(logits, ids, d_weights, score: int = SCORE_SOFTMAX, renormalize: b
     _launch(lib.rd_route_bwd, "rd_route_bwd", idx, logits.device, stream, logits.data_ptr(), dtype,
             ids.data_ptr(), d_weights.data_ptr(), tokens, experts, cfg, _word(limit, "limit", idx),
             out.data_ptr())
+    if stream is not None:
+        _used_on(stream, out)
     return out
 
 
@@ -215,6 +228,8 @@ def sort_rows(ids, experts: int, limit=None, stream=None):
     rows = torch.empty((1,), dtype=i32, device=dev)
     _launch(lib.rd_sort_rows, "rd_sort_rows", idx, dev, stream, ids.data_ptr(), tokens, topk, int(experts),
             _word(limit, "limit", idx), sizes.data_ptr(), pos.data_ptr(), rows.data_ptr())
+    if stream is not None:
+        _used_on(stream, sizes, pos, rows)
     return sizes, pos, rows
 
 
@@ -234,6 +249,8 @@ def dispatch_rows(x, pos, out_rows: Optional[int] = None, limit=None, out=None, 
         _want(out, "out", (out_rows, hidden), bf16, idx)
     _launch(lib.rd_dispatch_rows, "rd_dispatch_rows", idx, x.device, stream, x.data_ptr(), pos.data_ptr(),
             out.data_ptr(), tokens, topk, hidden, out_rows, _word(limit, "limit", idx))
+    if stream is not None:
+        _used_on(stream, out)
     return out
 
 
@@ -245,15 +262,18 @@ def combine_rows(y, pos, w=None, limit=None, out=None, stream=None):
     rows, hidden, idx = _matrix(y, "y", bf16)
     tokens, topk = pos.shape if pos.dim() == 2 else (0, 0)
     _want(pos, "pos", (tokens, topk), torch.int32, idx)
+    w_at = None
     if w is not None:
         _want(w, "w", (tokens, topk), torch.float32, idx)
-        w = w.data_ptr()
+        w_at = w.data_ptr()
     if out is None:
         out = torch.empty((tokens, hidden), dtype=bf16, device=y.device)
     else:
         _want(out, "out", (tokens, hidden), bf16, idx)
-    _launch(lib.rd_combine_rows, "rd_combine_rows", idx, y.device, stream, y.data_ptr(), pos.data_ptr(), w,
-            out.data_ptr(), tokens, topk, hidden, rows, _word(limit, "limit", idx))
+    _launch(lib.rd_combine_rows, "rd_combine_rows", idx, y.device, stream, y.data_ptr(), pos.data_ptr(),
+            w_at, out.data_ptr(), tokens, topk, hidden, rows, _word(limit, "limit", idx))
+    if stream is not None:
+        _used_on(stream, out)
     return out
 
 
@@ -278,6 +298,8 @@ def combine_rows_bwd(d_out, y, pos, w, limit=None, d_y=None, d_w=None, stream=No
     _launch(lib.rd_combine_rows_bwd, "rd_combine_rows_bwd", idx, y.device, stream, d_out.data_ptr(),
             y.data_ptr(), pos.data_ptr(), w.data_ptr(), d_y.data_ptr(), d_w.data_ptr(), tokens, topk, hidden,
             rows, _word(limit, "limit", idx))
+    if stream is not None:
+        _used_on(stream, d_y, d_w)
     return d_y, d_w
 
 
@@ -310,6 +332,8 @@ def mxfp4_quantize(x, pos=None, out_rows: Optional[int] = None, limit=None,
         _want(out.scales, "scales", (out_rows, width), u8, idx)
     _launch(lib.rd_mxfp4_quantize, "rd_mxfp4_quantize", idx, x.device, stream, x.data_ptr(), at,
             out.q.data_ptr(), out.scales.data_ptr(), rows, topk, k, out_rows, _word(limit, "limit", idx))
+    if stream is not None:
+        _used_on(stream, *out)
     return out
 
 
@@ -330,6 +354,8 @@ def mxfp4_quantize_weights(rhs, out: Optional[Mxfp4] = None, stream=None) -> Mxf
         _want(out.scales, "scales", (g, n, width), u8, idx)
     _launch(lib.rd_mxfp4_quantize_weights, "rd_mxfp4_quantize_weights", idx, dev, stream, rhs.data_ptr(),
             out.q.data_ptr(), out.scales.data_ptr(), g, k, n)
+    if stream is not None:
+        _used_on(stream, *out)
     return out
 
 
@@ -346,6 +372,8 @@ def mxfp4_dequantize(q, scales, limit=None, out=None, stream=None):
         _want(out, "out", (rows, k), torch.bfloat16, idx)
     _launch(lib.rd_mxfp4_dequantize, "rd_mxfp4_dequantize", idx, q.device, stream, q.data_ptr(),
             scales.data_ptr(), out.data_ptr(), rows, k, _word(limit, "limit", idx))
+    if stream is not None:
+        _used_on(stream, out)
     return out
 
 
@@ -388,4 +416,6 @@ def ragged_dot_mxfp4(a, a_scales, b, b_scales, group_sizes, group_offset: int = 
             a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), out.data_ptr(),
             out_scales.data_ptr() if quant else None, m, k, n, group_sizes.data_ptr(), g_total,
             group_offset, g_local, _word(limit, "limit", idx), epilogue, _word(status, "status", idx))
+    if stream is not None:
+        _used_on(stream, *((out, out_scales) if quant else (out,)))
     return Mxfp4(out, out_scales) if quant else out

@@ -60,8 +60,8 @@ typedef struct {
  *                  sigmoid  scale * s, or, renormalised, scale * s / (sum of the chosen s),
  *                  which is 0 where that sum is 0.
  *   All in f32, with the accurate exp and division, so that the keys, and with them the ids,
- *   equal those of the same formulas in elementwise f32 arithmetic.  A logit of +inf gives NaN
- *   softmax weights.
+ *   equal those of the same formulas in elementwise f32 arithmetic (where exp(-l) overflows, at
+ *   l < -88.7, the sigmoid is 0).  A logit of +inf gives NaN softmax weights.
  *
  *   logits  [tokens, experts] f32 or bf16 (`dtype`), experts 1 .. RD_MAX_GROUPS
  *   bias    [experts] f32 or NULL (a load-balancing term: it moves the choice, not the weights)

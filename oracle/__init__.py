@@ -19,6 +19,8 @@ float64 unless the pages fix another precision:
 * ``glu.*``                        -- SiLU-GLU forward/backward in float64 and
                                       as the float32 op sequence
 * ``unsort.unsort_bwd_rows``        -- weighted gradient and routing-weight row dot
+* ``moe.*``                        -- routing and its gradient, the sort of the slots, combine,
+                                      4-bit microscaled rows
 * ``bf16.*``                       -- bf16 rounding and ulp helpers
 
 Parity status: every function here is pinned by tests under ``tests/``
@@ -26,7 +28,7 @@ Parity status: every function here is pinned by tests under ``tests/``
 none is "parity unpinned".  The pages print no numeric input/output example,
 so no pin comes from printed values.
 """
-from . import bf16, glu, ragged, unsort  # noqa: F401
+from . import bf16, glu, moe, ragged, unsort  # noqa: F401
 from .ragged import (  # noqa: F401
     group_bounds,
     ragged_dot,
