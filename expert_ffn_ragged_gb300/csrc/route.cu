@@ -4,11 +4,11 @@
 // One warp owns a token; lane l holds the EPL consecutive experts from l * EPL in registers, so a
 // row is read in 16-byte vectors and a lower lane always means a lower expert index.
 //
-// Choice: topk warp-wide maxima over the lanes' largest keys give the topk-th largest of these; no
-// key below it can be chosen, and the few that are left (hardly more than topk) are gathered in
-// shared memory and ranked against each other.  Popping the best key topk times, with the keys of
-// a lane sorted first, took 1.3 times the instructions.  The two largest keys of a group, where
-// groups are whole lanes, are two maxima over the group's lanes.
+// Choice: the lanes put their largest keys in shared memory and count which of them are larger; no key
+// below the topk-th largest of these can be chosen, and the few that are left (hardly more than
+// topk) are gathered and ranked against each other by counting again.  Popping the best key topk
+// times, with the keys of a lane sorted first, took 1.6 times the instructions.  The two largest keys
+// of a group that is a power of two of whole lanes are merged by exchanges among these.
 //
 // Bound: instructions, not memory: at 32771 x 256 in f32 (36.7 MB: 5.4 us at the measured copy
 // rate) the exp and the reciprocal of the sigmoid, whose exact f32 values the choice is defined by,
@@ -75,10 +75,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// maximum over the lanes of `mask` (which names the calling lane); NaN operands lose
-__device__ __forceinline__ float lanes_max(float v, unsigned mask) {
+// maximum over the warp; NaN operands lose
+__device__ __forceinline__ float warp_max(float v) {
   float r;
-  asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(mask));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -169,7 +169,7 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
 #pragma unroll
       for (int i = 0; i < EPL; ++i) top = fmaxf(top, logit[i]);  // a NaN logit loses
     }
-    top = lanes_max(top, kAll);
+      top = warp_max(top);
     part = there ? expf(at - top) : 0.0f;
     float sum = part;
     if (!a.renormalize) {
@@ -188,10 +188,23 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
 }
 
 // Shared memory (words): the biases, then per warp the keys of the candidates (and four that never
-// win), their experts and the chosen ids.
-constexpr int route_warp_words(int epl) { return 32 * epl + 4 + 32 * epl + 4 + 32; }
+// win), their experts, the chosen ids, and the values that are ranked by counting.
+constexpr int route_warp_words(int epl) { return 32 * epl + 4 + 32 * epl + 4 + 32 + 32; }
 constexpr size_t route_smem_bytes(int epl) {
   return sizeof(float) * (32 * epl + kRouteWarps * route_warp_words(epl));
+}
+
+// How many of the n values (a multiple of four, in shared memory) are larger than v.
+__device__ __forceinline__ int count_larger(const float* values, int n, float v) {
+  int c = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; j += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(values + j);
+    // the sign of a difference (never rounded to zero) in place of a comparison and a select
+    c += static_cast<int>(__float_as_uint(v - o.x) >> 31) + static_cast<int>(__float_as_uint(v - o.y) >> 31) +
+         static_cast<int>(__float_as_uint(v - o.z) >> 31) + static_cast<int>(__float_as_uint(v - o.w) >> 31);
+  }
+  return c;
 }
 
 template <int EPL, class T, int SCORE>
@@ -202,6 +215,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
   float* ckey = sbias + 32 * EPL + warp * route_warp_words(EPL);
   int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL + 4);
   int* chosen = cexp + 32 * EPL + 4;
+  float* ranked = reinterpret_cast<float*>(chosen + 32);
   pdl_trigger();
   pdl_wait();
   if (a.bias != nullptr) {
@@ -212,11 +226,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
   const T* logits = static_cast<const T*>(a.logits);
   const int gsize = a.experts / a.groups;
   const int e0 = lane * EPL;
-  const bool lane_groups = gsize % EPL == 0;
-  // the lanes of this lane's group
-  const int lpg = lane_groups ? gsize / EPL : 1;
-  const int my_group = lane / lpg;
-  const unsigned group_mask = (lpg >= 32 ? kAll : ((1u << lpg) - 1u)) << (my_group * lpg);
+  // the lanes of a group, where groups are a power of two of whole lanes
+  const int lpg = gsize / EPL;
+  const bool lane_groups = gsize % EPL == 0 && (lpg & (lpg - 1)) == 0;
+  const int my_group = lane_groups ? lane / lpg : 0;
   const int stride = gridDim.x * kRouteWarps;
   int t = blockIdx.x * kRouteWarps + warp;
   float next[EPL];
@@ -250,30 +263,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
         mine2 = fmaxf(mine2, fminf(mine1, key[i]));
         mine1 = fmaxf(mine1, key[i]);
       }
-      // the group's largest key; then its second largest, for which the (lowest) lane that has
-      // the largest offers its own second
-      float score = kLow;
-      if (my_group < a.groups) {
-        const float first = lanes_max(mine1, group_mask);
-        score = first;
-        if (SCORE == RD_SCORE_SIGMOID) {
-          const unsigned has = __ballot_sync(group_mask, mine1 == first);
-          const float offer = lane == __ffs(has & group_mask) - 1 ? mine2 : mine1;
-          const float second = lanes_max(offer, group_mask);
-          if (second > kLow) score = __fadd_rn(first, second);
-        }
+      // the group's two largest keys, merged among its lanes
+      float first = mine1, second = mine2;
+      for (int d = 1; d < lpg; d <<= 1) {
+        const float f = __shfl_xor_sync(kAll, first, d), g = __shfl_xor_sync(kAll, second, d);
+        second = fmaxf(fmaxf(second, g), fminf(first, f));
+        first = fmaxf(first, f);
+      }
+      float score = first;
+      if (SCORE == RD_SCORE_SIGMOID && second > kLow) score = __fadd_rn(first, second);
+      // the groups before this one: those with a larger score, and of equal ones the lower
+      ranked[lane] = kLow;
+      __syncwarp();
+      if (lane % lpg == 0 && my_group < a.groups) ranked[my_group] = score;
+      __syncwarp();
+      int before = 0;
+      for (int g = 0; g < a.groups; g += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(ranked + g);
+        before += (o.x > score || (o.x == score && g < my_group)) +
+                  (o.y > score || (o.y == score && g + 1 < my_group)) +
+                  (o.z > score || (o.z == score && g + 2 < my_group)) +
+                  (o.w > score || (o.w == score && g + 3 < my_group));
       }
       __syncwarp();
-      bool kept = false;
-      for (int r = 0; r < a.topk_groups; ++r) {
-        const float best = lanes_max(score, kAll);
-        if (!(best > kLow)) break;
-        const int first_lane = __ffs(__ballot_sync(kAll, score == best)) - 1;
-        if ((group_mask >> first_lane) & 1u) {
-          kept = true;
-          score = kLow;
-        }
-      }
+      const bool kept = before < a.topk_groups;  // one without an expert has no key to offer
       if (!kept) {
         mine1 = kLow;
 #pragma unroll
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
         }
         uint32_t kept = 0;
         for (int r = 0; r < a.topk_groups; ++r) {
-          const float best = lanes_max(score, kAll);
+          const float best = warp_max(score);
           if (!(best > kLow)) break;
           const int g = __ffs(__ballot_sync(kAll, score == best)) - 1;
           kept |= 1u << g;
@@ -314,18 +327,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
 #pragma unroll
       for (int i = 1; i < EPL; ++i) mine1 = fmaxf(mine1, key[i]);
     }
-    // tau: the topk-th largest of the lanes' largest keys (-inf where fewer lanes have one)
-    float tau = kLow, rest = mine1;
-    for (int k = 0; k < a.topk; ++k) {
-      tau = lanes_max(rest, kAll);
-      if (!(tau > kLow)) break;
-      const unsigned has = __ballot_sync(kAll, rest == tau);
-      if (lane == __ffs(has) - 1) rest = kLow;
-    }
+    // tau: the topk-th largest of the lanes' largest keys.  Where fewer lanes have one, every key
+    // that is not -inf is a candidate.
+    ranked[lane] = mine1;
+    __syncwarp();
+    const bool among = count_larger(ranked, 32, mine1) < a.topk;
+    const float tau = fmaxf(-warp_max(among ? -mine1 : kLow), -3.402823466e38f);
     // the candidates, in the order of their experts
     int count = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) count += key[i] >= tau && key[i] > kLow ? 1 : 0;
+    for (int i = 0; i < EPL; ++i) count += key[i] >= tau ? 1 : 0;
     int at = count;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     at -= count;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const bool in = key[i] >= tau && key[i] > kLow;
+      const bool in = key[i] >= tau;
       if (in) ckey[at] = key[i];
       if (in) cexp[at] = e0 + i;
       at += in ? 1 : 0;
@@ -344,16 +355,24 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     if (lane < 4) ckey[total_c + lane] = kLow;
     chosen[lane] = -1;
     __syncwarp();
-    // a candidate's rank: those with a larger key, and of equal ones the earlier
-    for (int c = lane; c < total_c; c += 32) {
-      const float mine = ckey[c];
-      int rank = 0;
-      for (int j = 0; j < total_c; j += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(ckey + j);
-        rank += (o.x > mine || (o.x == mine && j < c)) + (o.y > mine || (o.y == mine && j + 1 < c)) +
-                (o.z > mine || (o.z == mine && j + 2 < c)) + (o.w > mine || (o.w == mine && j + 3 < c));
+    // a candidate's rank: those with a larger key; equal ones, which then meet at one rank, are told
+    // apart by their order
+    const int padded = (total_c + 3) & ~3;
+    if (total_c <= 32) {
+      const float mine = lane < total_c ? ckey[lane] : kLow;
+      int rank = count_larger(ckey, padded, mine);
+      const unsigned mine_at = lane < total_c ? 1u << rank : 0u;
+      if (__popc(__reduce_or_sync(kAll, mine_at)) != total_c) {
+        for (int j = 0; j < total_c; ++j) rank += j < lane && ckey[j] == mine ? 1 : 0;
       }
-      if (rank < a.topk) chosen[rank] = cexp[c];
+      if (lane < total_c && rank < a.topk) chosen[rank] = cexp[lane];
+    } else {
+      for (int c = lane; c < total_c; c += 32) {
+        const float mine = ckey[c];
+        int rank = count_larger(ckey, padded, mine);
+        for (int j = 0; j < c; ++j) rank += ckey[j] == mine ? 1 : 0;
+        if (rank < a.topk) chosen[rank] = cexp[c];
+      }
     }
     __syncwarp();
     const int my_id = lane < a.topk ? chosen[lane] : -1;
