@@ -184,8 +184,11 @@ __global__ void __launch_bounds__(kQuantThreads)
   *s = static_cast<uint8_t>(sb);
 }
 
+// at most 24 blocks an SM (16381 rows of 4096, there and back: 8 an SM 57.9 us, 12 55.6, 24 53.9,
+// 64 55.3: enough for an even end, few enough that the starts do not count)
 int quant_grid(int64_t blocks, int sms) {
-  return static_cast<int>(blocks < 8 * static_cast<int64_t>(sms) ? blocks : 8 * static_cast<int64_t>(sms));
+  const int64_t most = 24 * static_cast<int64_t>(sms);
+  return static_cast<int>(blocks < most ? blocks : most);
 }
 
 }  // namespace
