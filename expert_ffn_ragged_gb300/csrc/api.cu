@@ -18,7 +18,6 @@ namespace rd {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 4000000000ull;  // default bound of any single wait in a kernel
-constexpr int32_t kBandRows = 6144;              // default rows per band of the fwd/dx tile order
 
 // Process-wide tuning overrides (rd_set_tuning); 0 = the default.
 std::atomic<int32_t> g_variant{RD_VARIANT_AUTO};
@@ -187,9 +186,9 @@ bool use_pair(int sms, int64_t m, int32_t g_total) {
 
 // m-tiles per band of the forward / dx tile order: the band's lhs rows stay in
 // L2 while the band sweeps every output column block.
-int32_t band_tiles(bool pair) {
+int32_t band_tiles(bool pair, int32_t default_rows) {
   const int32_t r = g_band_rows.load(std::memory_order_relaxed);
-  const int64_t rows = r > 0 ? r : kBandRows;
+  const int64_t rows = r > 0 ? r : default_rows;
   const int64_t tile = pair ? 2 * kBM : kBM;
   const int64_t t = rows / tile;
   return static_cast<int32_t>(t < 1 ? 1 : t);

@@ -426,7 +426,9 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   g.group_offset = group_offset;
   g.g_local = g_local;
   g.n_tiles = static_cast<int32_t>((n_out + tile_w - 1) / tile_w);
-  g.band_tiles = band_tiles(pair);
+  // a 4-bit row is a quarter of a bf16 row: bands of four times the rows keep as many bytes in L2
+  // (32768 x 4096 x 14336: 623 -> 617 us, means of six)
+  g.band_tiles = band_tiles(pair, 4 * kBandRows);
   g.timeout_ns = wait_timeout_ns();
   const int tm = pair ? 2 * kBM : kBM;
   const int64_t tiles = ((m + tm - 1) / tm + g_local) * g.n_tiles;

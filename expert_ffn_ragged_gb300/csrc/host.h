@@ -39,7 +39,8 @@ rd_status check_groups(int64_t m, int64_t k, int64_t n, const int32_t* group_siz
 int grid_for(int sms, int64_t tiles_upper_bound);
 int pair_grid(int sms, int64_t pair_tiles_upper_bound);
 // whether a grouped product runs on CTA pairs, and the m-tiles per band of its tile order
+constexpr int32_t kBandRows = 6144;  // default rows of a band (bf16 rows: 48 MB at k = 4096)
 bool use_pair(int sms, int64_t m, int32_t g_total);
-int32_t band_tiles(bool pair);
+int32_t band_tiles(bool pair, int32_t default_rows = kBandRows);
 
 }  // namespace rd
