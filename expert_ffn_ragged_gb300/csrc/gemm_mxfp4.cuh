@@ -435,29 +435,6 @@ __global__ void __launch_bounds__(k4Threads, 1)
         }
         __syncwarp();
       };
-      // 64 columns of each row: whole 128-byte lines, 4 rows a store, in two passes of 16 rows
-      auto emit_wide = [&](const uint32_t (&p)[32], int col) {
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          if ((lane >> 4) == pass) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              stg[(lane & 15) * 8 + (v ^ (lane & 7))] =
-                  make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int rl = it * 4 + (lane >> 3);
-            const uint4 val = stg[rl * 8 + ((lane & 7) ^ (rl & 7))];
-            const int row = wrow0 + pass * 16 + rl;
-            const int c = col + (lane & 7) * 8;
-            if (row >= lo && row < hi && c + 8 <= args.n_out)
-              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * args.n_out + c) = val;
-          }
-          __syncwarp();
-        }
-      };
       // the same columns as a 4-bit block: 16 bytes of codes and a scale byte
       auto emit_quant = [&](const float (&h)[32], int col) {
         uint32_t amax = 0;
@@ -497,9 +474,9 @@ __global__ void __launch_bounds__(k4Threads, 1)
       ptx::tc_fence_after();
       const uint32_t tbase =
           sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * k4BN);
-      if (GLU) {
 #pragma unroll 1
-        for (int c = half; c < kChunks; c += 2) {
+      for (int c = half; c < kChunks; c += 2) {
+        if (GLU) {
           uint32_t g[32], u[32];
           ptx::tmem_load_32cols(tbase + c * 32, g);
           ptx::tmem_load_32cols(tbase + k4Half + c * 32, u);
@@ -515,26 +492,17 @@ __global__ void __launch_bounds__(k4Threads, 1)
             for (int i = 0; i < 16; ++i) p[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
             emit(p, col0 + c * 32);
           }
-        }
-      } else {
-        // each of the two warps takes 96 columns: 64 that are whole lines and 32 that are not
-        const int wide = half == 0 ? 0 : 128, narrow = half == 0 ? 64 : 96;
-        uint32_t p[32];
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t v[32];
-          ptx::tmem_load_32cols(tbase + wide + part * 32, v);
+        } else {
+          // chunk by chunk: all three read at once and the accumulator given back before the stores
+          // was slower (32768 x 4096 x 14336 605 -> 630 us, 131072 x 768 x 4096 297 -> 334), as were
+          // stores of whole 128-byte lines (620) and of 32 bytes a lane without the transpose (680)
+          uint32_t v[32], p[16];
+          ptx::tmem_load_32cols(tbase + c * 32, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            p[part * 16 + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          emit(p, col0 + c * 32);
         }
-        emit_wide(p, col0 + wide);
-        uint32_t v[32], pn[16];
-        ptx::tmem_load_32cols(tbase + narrow, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pn[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        emit(pn, col0 + narrow);
       }
       ptx::tc_fence_before();
       __syncwarp();
