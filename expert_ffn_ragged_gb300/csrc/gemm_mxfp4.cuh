@@ -493,9 +493,10 @@ __global__ void __launch_bounds__(k4Threads, 1)
             emit(p, col0 + c * 32);
           }
         } else {
-          // chunk by chunk: all three read at once and the accumulator given back before the stores
-          // was slower (32768 x 4096 x 14336 605 -> 630 us, 131072 x 768 x 4096 297 -> 334), as were
-          // stores of whole 128-byte lines (620) and of 32 bytes a lane without the transpose (680)
+          // Chunk by chunk.  All three read at once and the accumulator given back before the stores
+          // was slower where the outputs dominate (131072 x 768 x 4096: 297 -> 334 us), as were stores
+          // of 32 bytes a lane without the transpose (32768 x 4096 x 14336: 620 -> 680); stores of
+          // whole 128-byte lines made no difference.
           uint32_t v[32], p[16];
           ptx::tmem_load_32cols(tbase + c * 32, v);
 #pragma unroll

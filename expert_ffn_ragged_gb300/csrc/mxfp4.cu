@@ -25,16 +25,24 @@ __device__ __forceinline__ int32_t rows_below(const int32_t* limit, int32_t rows
 
 // largest magnitude bits of eight packed bf16 values, as f32 bits
 __device__ __forceinline__ uint32_t amax8(uint4 v) {
-  const uint32_t c[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(c[i] << 16, c[i] & 0xFFFF0000u));
-  return m;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                              __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
+// Eight bf16 values times an exact power of two (a bf16 number too), in bf16: exact, except that
+// values far below the smallest level may become 0, which they round to.
 __device__ __forceinline__ uint32_t pack_scaled(uint4 v, float inv) {
-  const float f[8] = {bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv, bf16_hi(v.y) * inv,
-                      bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv, bf16_hi(v.w) * inv};
+  const __nv_bfloat162 f2 = __float2bfloat162_rn(inv);
+  const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&c[i]), f2);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
+    f[2 * i] = bf16_lo(u);
+    f[2 * i + 1] = bf16_hi(u);
+  }
   return mx_pack8(f);
 }
 
