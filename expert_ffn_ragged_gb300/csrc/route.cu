@@ -169,7 +169,7 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
 #pragma unroll
       for (int i = 0; i < EPL; ++i) top = fmaxf(top, logit[i]);  // a NaN logit loses
     }
-      top = warp_max(top);
+    top = warp_max(top);
     part = there ? expf(at - top) : 0.0f;
     float sum = part;
     if (!a.renormalize) {
@@ -216,8 +216,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
   int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL + 4);
   int* chosen = cexp + 32 * EPL + 4;
   float* ranked = reinterpret_cast<float*>(chosen + 32);
-  pdl_trigger();
-  pdl_wait();
   if (a.bias != nullptr) {
     for (int e = threadIdx.x; e < 32 * EPL; e += kRouteWarps * 32) sbias[e] = e < a.experts ? a.bias[e] : 0.0f;
     __syncthreads();
@@ -397,8 +395,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
   extern __shared__ __align__(16) float smem_rows[];  // [warps][32 * EPL]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* srow = smem_rows + warp * 32 * EPL;
-  pdl_trigger();
-  pdl_wait();
   const int32_t L = tokens_below(a.limit, a.tokens);
   const bool dense = SCORE == RD_SCORE_SOFTMAX && !a.renormalize;
   const int e0 = lane * EPL;
@@ -485,8 +481,8 @@ cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
   a.vec = a.experts % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % unit == 0 &&
           reinterpret_cast<uintptr_t>(a.d_logits) % unit == 0;
   if (bwd) {
-    return launch_pdl(route_bwd_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32,
-                      sizeof(float) * kRouteWarps * 32 * EPL, 1, stream, a);
+    return launch_kernel(route_bwd_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32,
+                         sizeof(float) * kRouteWarps * 32 * EPL, 1, stream, a);
   }
   constexpr size_t smem = route_smem_bytes(EPL);
   if (smem > 48 * 1024) {
@@ -500,7 +496,7 @@ cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
       attr_set[dev].store(true, std::memory_order_release);
     }
   }
-  return launch_pdl(route_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32, smem, 1, stream, a);
+  return launch_kernel(route_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32, smem, 1, stream, a);
 }
 
 template <int EPL, class T>

@@ -47,8 +47,6 @@ __global__ void __launch_bounds__(WARPS * 32)
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  pdl_wait();
   int32_t L = tokens;
   if (limit != nullptr) {
     const int32_t v = *limit;
@@ -188,8 +186,8 @@ cudaError_t launch_sort_rows(const int32_t* ids, int32_t tokens, int32_t topk, i
   const int64_t slots = static_cast<int64_t>(tokens) * topk;
   int ctas = 1;
   while (ctas < kSortCluster && slots > static_cast<int64_t>(ctas) * warps * 32 * kSortBatch) ctas *= 2;
-  return launch_pdl(kernel, dim3(ctas), warps * 32, sizeof(uint32_t) * (2 * warps + 2) * experts, ctas,
-                    stream, ids, tokens, topk, experts, limit, group_sizes, pos, rows);
+  return launch_kernel(kernel, dim3(ctas), warps * 32, sizeof(uint32_t) * (2 * warps + 2) * experts, ctas,
+                       stream, ids, tokens, topk, experts, limit, group_sizes, pos, rows);
 }
 
 }  // namespace rd
