@@ -397,7 +397,6 @@ def run_ops(rd, device, stream, peaks):
                      "bound": "hbm" if B / BW > F / P else "tensor",
                      "frac": max(F / P, B / BW) / t}
         clock_probe(dx_call, "dx", F)
-        # dw through per-group tensor maps, in a workspace allocated once
         ws = torch.empty(rd.dw_workspace_bytes(device), dtype=torch.uint8, device=device)
         dw_call = lambda: rd.trans_ragged_dot(x, do, gs, out=dw, workspace=ws)
         t = med(dw_call, entry="dw")

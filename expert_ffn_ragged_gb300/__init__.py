@@ -13,7 +13,7 @@ Functions (same names as the C ABI, without the ``rd_`` prefix):
 * ``trans_ragged_dot(x, y, group_sizes, ...)``           -> out [g_local, k, n]
 * ``trans_ragged_dot_f32(x, y, group_sizes, ..., accumulate=False)`` -> f32 out [g_local, k, n]
 * ``dw_workspace_bytes(device)``                         -> the dw calls' workspace size
-* ``trans_ragged_dot_no_alloc(x, y, group_sizes, ...)``  -> dw with no allocation (library scratch)
+* ``trans_ragged_dot_no_alloc(x, y, group_sizes, ...)``  -> dw with no allocation
 * ``glu_fwd(fused, limit=None)``                         -> out [rows, f]
 * ``glu_bwd(fused, d_out, limit=None)``                  -> d_fused [rows, 2f]
 * ``unsort_bwd_rows(g, y, w, limit=None)``                -> (grad [rows, hidden], dot [rows])
@@ -405,8 +405,8 @@ def dw_workspace_bytes(device=None) -> int:
     return _ws_bytes[dev.index]
 
 
-def _dw_workspace(workspace, dev, stream):
-    """The workspace argument of the dw calls: "auto" allocates one for this call."""
+def _dw_workspace(workspace):
+    """The workspace argument of the dw calls, which they check and do not use: "auto" is none."""
     torch = _torch()
 
     if workspace is None:
@@ -414,10 +414,7 @@ def _dw_workspace(workspace, dev, stream):
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
-        ws = torch.empty(dw_workspace_bytes(dev), dtype=torch.uint8, device=dev)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            ws.record_stream(stream)     # freed after the call: keep it until the stream is done
-        return ws
+        return None
     if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
     return workspace
@@ -440,8 +437,8 @@ def trans_ragged_dot(x, y, group_sizes, group_offset: int = 0, g_local: Optional
                      limit=None, out=None, status=None, stream=None, workspace="auto"):
     """out[j] = x[rows_j]^T @ y[rows_j] for the local groups; x [m, k], y [m, n].
 
-    workspace: "auto" (a workspace of dw_workspace_bytes() allocated for the
-    call), None (the form without one), or a caller's uint8 CUDA tensor.
+    workspace: "auto" or None, or a caller's uint8 CUDA tensor of dw_workspace_bytes()
+    (checked, not used).
     """
     torch = _torch()
 
@@ -451,7 +448,7 @@ def trans_ragged_dot(x, y, group_sizes, group_offset: int = 0, g_local: Optional
     if out is None:
         out = torch.empty((g_local, k, n), dtype=torch.bfloat16, device=dev)
     _out(out, (g_local, k, n), torch.bfloat16)
-    ws = _dw_workspace(workspace, dev, stream)
+    ws = _dw_workspace(workspace)
     _same_device(dev, y, out, group_sizes, limit, status, ws)
     with _on_device(dev):
         code = lib.rd_trans_ragged_dot(_ptr(x), _ptr(y), _ptr(out), m, k, n, _ptr(group_sizes),
@@ -467,10 +464,6 @@ def trans_ragged_dot_no_alloc(x, y, group_sizes, group_offset: int = 0,
                               stream=None):
     """trans_ragged_dot for callers that cannot allocate device memory at the call.
 
-    The same per-group-descriptor dw as trans_ragged_dot with a workspace, its
-    scratch taken from an array inside the library (see
-    rd_trans_ragged_dot_no_alloc: up to 256 SMs; calls that overlap on the GPU
-    race on the array; make the first call on a device outside stream capture).
     Pass ``out`` to allocate nothing at all.
     """
     torch = _torch()
@@ -509,7 +502,7 @@ def trans_ragged_dot_f32(x, y, group_sizes, group_offset: int = 0, g_local: Opti
             raise ValueError("accumulate needs an existing out buffer")
         out = torch.empty((g_local, k, n), dtype=torch.float32, device=dev)
     _out(out, (g_local, k, n), torch.float32)
-    ws = _dw_workspace(workspace, dev, stream)
+    ws = _dw_workspace(workspace)
     _same_device(dev, y, out, group_sizes, limit, status, ws)
     with _on_device(dev):
         code = lib.rd_trans_ragged_dot_f32(_ptr(x), _ptr(y), _ptr(out), m, k, n,

@@ -17,6 +17,7 @@
 namespace rd {
 namespace {
 
+constexpr size_t kWorkspaceBytesPerSm = 2048;   // size of a dw workspace
 constexpr uint64_t kTimeoutNs = 4000000000ull;  // default bound of any single wait in a kernel
 
 // Process-wide tuning overrides (rd_set_tuning); 0 = the default.
@@ -381,9 +382,8 @@ rd_status trans_ragged_impl(const void* x, const void* y, void* out, int64_t m, 
     return RD_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = current_device(&sms)) != RD_OK) return st;
-  // the workspace holds the per-group maps of every CTA; it must not overlap
-  // anything the call reads or writes
-  const uint64_t ws_need = static_cast<uint64_t>(sms) * kMapBytesPerCta;
+  // a workspace is not used (see rd.h), but one that could not be is still refused
+  const uint64_t ws_need = static_cast<uint64_t>(sms) * kWorkspaceBytesPerSm;
   if (workspace != nullptr &&
       (workspace_bytes < ws_need ||
        out_aliases(workspace, workspace_bytes, x, static_cast<uint64_t>(m) * k * 2, y,
@@ -444,15 +444,6 @@ rd_status trans_ragged_impl(const void* x, const void* y, void* out, int64_t m, 
   a.g_local = g_local;
   a.n_tiles = static_cast<int32_t>((n + kBN - 1) / kBN);
   a.dw_m_tiles = static_cast<int32_t>((k + tile_rows - 1) / tile_rows);
-  // with a workspace each CTA rebases the maps to each group it works on (rows
-  // outside the group then arrive as zeros); without one the edge rows of each
-  // group's first block are zeroed in shared memory
-  a.group_maps = workspace != nullptr ? 1 : 0;
-  a.x_base = x;
-  a.y_base = y;
-  a.x_row_bytes = k * 2;
-  a.y_row_bytes = n * 2;
-  a.maps = static_cast<CUtensorMap*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   const int64_t tiles = static_cast<int64_t>(g_local) * a.dw_m_tiles * a.n_tiles;
   if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
@@ -479,7 +470,7 @@ extern "C" rd_status rd_trans_ragged_dot_workspace_size(size_t* bytes) {
   int sms = 0;
   const rd_status st = current_device(&sms);
   if (st != RD_OK) return st;
-  *bytes = static_cast<size_t>(sms) * kMapBytesPerCta;
+  *bytes = static_cast<size_t>(sms) * kWorkspaceBytesPerSm;
   return RD_OK;
 }
 
@@ -579,55 +570,13 @@ extern "C" rd_status rd_unsort_bwd_rows(const void* g, const void* y, const floa
              : RD_ERR_CUDA;
 }
 
-// ------------------------------------------------ dw without any allocation
-// Some callers cannot allocate device memory at the point where they run the
-// weight gradient: code inside an allocator's own callbacks, a runtime that
-// owns every allocation and hands out no scratch, or a process that must not
-// grow its footprint once set up.  For them rd_trans_ragged_dot_no_alloc runs
-// the per-group-descriptor form of the dw kernel with its scratch in this
-// file-scope array, which every GPU that loads the library holds until exit.
-// It covers devices of up to kNoAllocMaxSms SMs (2 KB of descriptors per SM).
-constexpr int kNoAllocMaxSms = 256;
-constexpr size_t kNoAllocScratchBytes = static_cast<size_t>(kNoAllocMaxSms) * kMapBytesPerCta;
-static __device__ __align__(256) unsigned char g_no_alloc_scratch[kNoAllocScratchBytes];
-
-namespace {
-// The array's device address on the current device.  In host code the array's
-// name only stands in for the symbol: its address must come from the runtime,
-// once per device, with that device current.
-rd_status no_alloc_scratch(void** ptr) {
-  static std::mutex mu;
-  static void* addr[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return RD_ERR_CUDA;
-  if (dev < 0 || dev >= 64) return RD_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lock(mu);
-  if (addr[dev] == nullptr) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_no_alloc_scratch) != cudaSuccess || p == nullptr)
-      return RD_ERR_CUDA;
-    addr[dev] = p;
-  }
-  *ptr = addr[dev];
-  return RD_OK;
-}
-}  // namespace
-
 extern "C" rd_status rd_trans_ragged_dot_no_alloc(const void* x, const void* y, void* out, int64_t m,
                                                   int64_t k, int64_t n, const int32_t* group_sizes,
                                                   int32_t g_total, int32_t group_offset,
                                                   int32_t g_local, const int32_t* limit,
                                                   int32_t* status, rd_stream_t stream) {
-  // the argument checks every dw call makes, before any CUDA call
-  rd_status st = check_groups(m, k, n, group_sizes, g_total, group_offset, g_local, limit, status);
-  if (st != RD_OK) return st;
-  int sms = 0;
-  if ((st = current_device(&sms)) != RD_OK) return st;
-  if (sms > kNoAllocMaxSms) return RD_ERR_UNSUPPORTED;  // more CTAs than the array has room for
-  void* scratch = nullptr;
-  if ((st = no_alloc_scratch(&scratch)) != RD_OK) return st;
   return trans_ragged_impl(x, y, out, m, k, n, group_sizes, g_total, group_offset, g_local, limit,
-                           kEpiNone, scratch, kNoAllocScratchBytes, status, stream);
+                           kEpiNone, nullptr, 0, status, stream);
 }
 
 extern "C" rd_status rd_set_tuning(const rd_tuning* t) {

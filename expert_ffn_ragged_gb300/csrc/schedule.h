@@ -151,8 +151,9 @@ RD_HD int dw_edge(const Tile& tl, int kb, int& z0, int& z1) {
   return zrows >> 4;
 }
 
-// dw through per-group tensor maps (the map's rows are the group's rows, so
-// rows outside the group are out of bounds and land as zeros): the K blocks
+// dw blocks counted from a group's own first row, as a map of the group's rows would have them (rows
+// outside the group are out of bounds and land as zeros; the enumeration test is its only user: the
+// kernels load from maps of the whole operand, dw_block_row): the K blocks
 // are aligned to end at the group end, block kb starting at group row
 // rem - 64 + 64 kb with rem = the rows of the last block (1..64); the first
 // block's rows above the group start arrive as zeros, and its whole 16-row

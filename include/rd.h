@@ -4,8 +4,7 @@
  *
  * Every entry point takes plain device pointers and sizes, enqueues work on
  * the caller's CUDA stream and returns at once.  The library never
- * synchronises, never copies device data to the host and allocates nothing
- * (the dw calls can use a small workspace the caller provides); group_sizes
+ * synchronises, never copies device data to the host and allocates nothing; group_sizes
  * and limit stay on the device and are read by the kernels themselves.  A call can therefore be captured in a CUDA graph,
  * and replays follow device-side changes to group_sizes and limit.  The
  * first call of each entry point in a process sets a kernel attribute
@@ -164,17 +163,11 @@ rd_status rd_ragged_dot_trans_rhs_glu_bwd(const void* d_out, const void* rhs, co
  *   x [m, k] bf16, y [m, n] bf16, out [g_local, k, n] bf16 (f32 accumulated).
  *   workspace        device scratch of at least the size rd_trans_ragged_dot_
  *                    workspace_size reports for the current device, 128-byte
- *                    aligned, or NULL.  With it the kernel builds, per group,
- *                    TMA descriptors whose rows are exactly the group's rows
- *                    (rows outside the group then arrive as zeros); without
- *                    it the rows of each group's first K block that precede
- *                    the group are zeroed in shared memory, which is slower
- *                    when group sizes are not multiples of 16.  The results
- *                    agree within the stated accuracy (only the f32
- *                    summation order differs).  The workspace is the call's
- *                    own until the call completes on its stream: calls that
- *                    may run at the same time need separate workspaces.  The
- *                    library never reads what the workspace held before.
+ *                    aligned, or NULL.  It is checked and not used: the form
+ *                    that built TMA descriptors of each group in it ended in an
+ *                    illegal address in one order of calls and was taken out.
+ *                    The rows of each group's last K block that precede the
+ *                    group are skipped or zeroed in shared memory.
  *   workspace_bytes  its size in bytes (ignored when workspace is NULL).
  *   Other arguments as rd_ragged_dot.
  * Requires k % 8 == 0, n % 8 == 0, 16-byte aligned pointers, no overlap
@@ -189,8 +182,8 @@ rd_status rd_trans_ragged_dot(const void* x, const void* y, void* out, int64_t m
 
 /*
  * rd_trans_ragged_dot_workspace_size -- the workspace rd_trans_ragged_dot and
- * rd_trans_ragged_dot_f32 take on the current device: 2 KB per SM (the
- * per-group TMA descriptors of each CTA).  RD_ERR_INVALID_ARG for a NULL
+ * rd_trans_ragged_dot_f32 take on the current device: 2 KB per SM.
+ * RD_ERR_INVALID_ARG for a NULL
  * pointer, RD_ERR_UNSUPPORTED on a device other than sm_103.
  */
 rd_status rd_trans_ragged_dot_workspace_size(size_t* bytes);
@@ -220,22 +213,11 @@ rd_status rd_trans_ragged_dot_f32(const void* x, const void* y, float* out, int6
  * point exists for code that has no way to provide the workspace, such as a
  * caller running inside a memory allocator's own callbacks, a runtime that
  * owns every device allocation and hands out no scratch, or a process that
- * must not grow its footprint after set-up.  It computes what
- * rd_trans_ragged_dot computes with a workspace (the per-group-descriptor
- * form), taking its 2 KB of descriptors per SM from a 512 KB array inside the
- * library that every GPU loading the library holds until the process exits;
- * it allocates nothing and calls no allocating routine.
+ * must not grow its footprint after set-up.  It allocates nothing, calls no
+ * allocating routine, uses no device memory but its arguments, and computes
+ * what rd_trans_ragged_dot does.
  *
  *   Arguments as rd_trans_ragged_dot, without the workspace.
- *   Limit: devices of up to 256 SMs; on a larger device it returns
- *   RD_ERR_UNSUPPORTED and enqueues nothing.
- *   Set-up: the first call on each device asks the CUDA runtime for the
- *   array's device address (once per device, with that device current); make
- *   that first call before any stream capture on the device.
- *   Sharing: every call on a device uses the same array, which keeps the last
- *   call's descriptors; no call reads what an earlier one left there.  Calls
- *   whose kernels overlap on the GPU (other streams, other threads) race on
- *   the array and give wrong results: order such calls on one stream.
  */
 rd_status rd_trans_ragged_dot_no_alloc(const void* x, const void* y, void* out, int64_t m,
                                        int64_t k, int64_t n, const int32_t* group_sizes,
