@@ -1,7 +1,9 @@
 // mxfp4.cu -- rows to 4-bit microscaled blocks and back, and the layout of 4-bit expert weights.
 //
 // HBM streams: quantisation reads 2 bytes an element and writes 17/32 (times topk when the rows go
-// to their packed places at once), dequantisation the other way round.
+// to their packed places at once), dequantisation the other way round.  16381 rows of 4096 take 27 us one
+// way (170 MB: 6.3 TB/s) and 28 us the other; the issue slots are 64 % busy, so the arithmetic stays
+// packed: maxima of two bf16 halves at once, and the scaling in bf16, where a power of two is exact.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -4,14 +4,16 @@
 // up to 16 CTAs does the whole sort in one launch: every warp counts a contiguous piece of the
 // slots into its own histogram in shared memory, the CTAs exchange their sums through distributed
 // shared memory, and every warp then walks its piece again, 32 slots at a time: each slot sets its
-// lane's bit in a mask of its expert, whose lower bits then count the slots before it.  The ids are read twice (the second time from L2)
-// and pos is written once: 4 + 4 bytes a slot.
+// lane's bit in a mask of its expert, whose lower bits then count the slots before it.  The ids are
+// read twice (the second time from L2) and pos is written once: 4 + 4 bytes a slot.
 //
 // Bound: latency, that of the walk's dependent steps.  Each warp therefore loads eight steps' ids
 // before it works on them (a load a step made 262144 slots take 40 us on 8 CTAs), and the cluster
 // grows with the slots until a warp has one such batch.  The walk of 262168 slots over 256 experts
 // took 17 us with a warp match for equal experts (60 cycles a step of a whole SM) and 12 us with
-// a ballot per bit of the index.
+// a ballot per bit of the index.  262168 slots over 256 experts: 15.4 us in all, 8 slots: 4.4 us.  Two
+// launches over all SMs, the counts passed through memory, saved 2 us there and cost 0.2 us where a call
+// is small.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
