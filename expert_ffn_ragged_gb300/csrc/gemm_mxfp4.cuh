@@ -478,8 +478,10 @@ __global__ void __launch_bounds__(k4Threads, 1)
       ptx::tc_fence_after();
       const uint32_t tbase =
           sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * k4BN);
+      // a group of a few rows leaves most warps' rows without an owner
+      const bool any_rows = wrow0 < hi && wrow0 + 32 > lo;
 #pragma unroll 1
-      for (int c = half; c < kChunks; c += 2) {
+      for (int c = half; c < kChunks && any_rows; c += 2) {
         if (GLU) {
           uint32_t g[32], u[32];
           ptx::tmem_load_32cols(tbase + c * 32, g);

@@ -11,7 +11,7 @@
 // of a group that is a power of two of whole lanes are merged by exchanges among these.
 //
 // Bound: instructions, not memory: 32771 tokens, 256 experts in 8 groups, sigmoid, top-8, f32 logits
-// (36.7 MB: 5.4 us at the measured copy rate) take 27.5 us, with the issue slots 67 % busy and DRAM 14 %;
+// (36.7 MB: 5.4 us at the measured copy rate) take 26.4 us, with the issue slots 67 % busy and DRAM 14 %;
 // the exp and the reciprocal of the sigmoid, whose exact f32 values the choice is defined by, are a
 // third of the instructions.  The gradient, 65536 x 128 softmax over all experts: 71.3 MB in 16.8 us
 // (4.2 TB/s; issue 64 %).  One token: 2.4 us, 4.2 more for the plan.
@@ -54,8 +54,9 @@ __device__ __forceinline__ float reciprocal_fast(float d) {
 // the logistic in the elementwise f32 arithmetic that the keys are defined by
 __device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
-// the same for a lane's logits, with one test for those so negative that 1 / d leaves the normal
-// numbers (a test for each made the branches as expensive as the arithmetic)
+// The same for a lane's logits, NaN for a masked one (d is infinite, and infinity times 0 is NaN in the
+// step), with one test for those so negative that 1 / d leaves the normal numbers (a test for each made
+// the branches as expensive as the arithmetic).
 template <int EPL>
 __device__ __forceinline__ void sigmoids_f32(const float (&l)[EPL], float (&s)[EPL]) {
   float most = 0.0f;
@@ -67,7 +68,7 @@ __device__ __forceinline__ void sigmoids_f32(const float (&l)[EPL], float (&s)[E
   }
   if (!(most < kFastRcp)) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = sigmoid_f32(l[i]);
+    for (int i = 0; i < EPL; ++i) s[i] = l[i] > kLow ? sigmoid_f32(l[i]) : NAN;
   }
 }
 
@@ -209,6 +210,24 @@ __device__ __forceinline__ int count_larger(const float* values, int n, float v)
   return c;
 }
 
+// EPL values of shared memory, from a boundary of EPL
+template <int EPL>
+__device__ __forceinline__ void load_shared(const float* p, float (&v)[EPL]) {
+  if (EPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < EPL; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[i + 2] = x.z;
+      v[i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = p[i];
+  }
+}
+
 template <int EPL, class T, int SCORE>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
   extern __shared__ __align__(16) float smem_route[];
@@ -248,13 +267,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
       for (int i = 0; i < EPL; ++i) key[i] = logit[i];
     }
     if (a.bias != nullptr) {
+      float b[EPL];
+      load_shared<EPL>(sbias + e0, b);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) key[i] = __fadd_rn(key[i], sbias[e0 + i]);
+      for (int i = 0; i < EPL; ++i) key[i] = __fadd_rn(key[i], b[i]);
     }
-    // a masked logit's softmax key is -inf or NaN by itself; its sigmoid key is not
+    // a masked expert's key is -inf or NaN by itself
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      key[i] = (SCORE == RD_SCORE_SOFTMAX || logit[i] > kLow) && key[i] > kLow ? key[i] : kLow;
+    for (int i = 0; i < EPL; ++i) key[i] = fmaxf(key[i], kLow);
     float mine1 = key[0];  // this lane's largest key
     if (a.groups > 1 && lane_groups) {
       float mine2 = kLow;
