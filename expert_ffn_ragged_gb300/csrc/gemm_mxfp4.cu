@@ -42,8 +42,8 @@ cudaError_t launch_impl(const Gemm4Maps& maps, const Gemm4Args& args, int grid, 
     }
     if (grid > 2 * clusters) grid = 2 * clusters;
   }
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), k4Threads, smem, PAIR ? 2 : 1, stream,
-                       maps, args);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), k4Threads, smem, PAIR ? 2 : 1, stream, maps,
+                    args);
 }
 
 template <bool PAIR>

@@ -246,6 +246,9 @@ __global__ void __launch_bounds__(k4Threads, 1)
       ptx::tmem_relinquish();
     }
   }
+  // everything above touches no memory of the stream's earlier work
+  pdl_trigger();
+  pdl_wait();
   if (warp == 2) build_schedule<kOpFwd, TM>(sh, args, lane);
   ptx::tc_fence_before();
   __syncthreads();

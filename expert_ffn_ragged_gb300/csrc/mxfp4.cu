@@ -53,6 +53,8 @@ constexpr int kQuantBatch = 4;  // pieces of 256 elements of a row that a warp h
 // A warp takes up to four pieces of 256 elements of a row: lane i eight of each, four lanes a block.
 template <bool SEND>
 __global__ void __launch_bounds__(kQuantThreads) mxfp4_quantize_kernel(const QuantArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.rows);
   const int vecs = a.k / 8, blocks = a.k / kMxBlock;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kQuantThreads) mxfp4_quantize_kernel(const Qua
 #pragma unroll
     for (int b = 0; b < kQuantBatch; ++b) {
       xv[b] = make_uint4(0, 0, 0, 0);
-      if (v0 + 32 * b < vecs) xv[b] = __ldg(x + r * vecs + v0 + 32 * b);
+      if (v0 + 32 * b < vecs) xv[b] = x[r * vecs + v0 + 32 * b];
     }
     const int32_t p_lane = SEND && lane < a.topk ? a.pos[r * a.topk + lane] : -1;
 #pragma unroll
@@ -117,7 +119,9 @@ __device__ __forceinline__ float2 code_pair(uint32_t byte) {
 
 // A warp takes up to four pieces of 256 elements of a row, as above.
 __global__ void __launch_bounds__(kQuantThreads)
-    mxfp4_dequantize_kernel(const QuantArgs a, uint4* __restrict__ out) {
+    mxfp4_dequantize_kernel(const QuantArgs a, uint4* out) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.rows);
   const int vecs = a.k / 8;
@@ -133,8 +137,8 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
     for (int b = 0; b < kQuantBatch; ++b) {
       const int v = v0 + 32 * b;
-      c[b] = v < vecs ? __ldg(q + v) : 0u;
-      sb[b] = v < vecs ? __ldg(s + (v >> 2)) : 0u;
+      c[b] = v < vecs ? q[v] : 0u;
+      sb[b] = v < vecs ? s[v >> 2] : 0u;
     }
 #pragma unroll
     for (int b = 0; b < kQuantBatch; ++b) {
@@ -154,8 +158,10 @@ __global__ void __launch_bounds__(kQuantThreads)
 // Weights [g, k, n] to rows along k: a thread owns one output column n and one block of 32 k.
 // Reads are coalesced over n; each thread writes its 16 bytes of codes.
 __global__ void __launch_bounds__(kQuantThreads)
-    mxfp4_weights_kernel(const __nv_bfloat16* __restrict__ rhs, uint8_t* __restrict__ q,
-                         uint8_t* __restrict__ scales, int32_t k, int32_t n, int32_t scale_width) {
+    mxfp4_weights_kernel(const __nv_bfloat16* rhs, uint8_t* q,
+                         uint8_t* scales, int32_t k, int32_t n, int32_t scale_width) {
+  pdl_trigger();
+  pdl_wait();
   const int col = blockIdx.x * kQuantThreads + threadIdx.x;
   const int block = blockIdx.y;
   const int64_t e = blockIdx.z;
@@ -200,22 +206,22 @@ int quant_grid(int64_t blocks, int sms) {
 cudaError_t launch_mxfp4_quantize(const QuantArgs& a, int sms, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
   const int grid = quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms);
-  return launch_kernel(a.pos != nullptr ? mxfp4_quantize_kernel<true> : mxfp4_quantize_kernel<false>,
-                       dim3(grid), kQuantThreads, 0, 1, stream, a);
+  return launch_pdl(a.pos != nullptr ? mxfp4_quantize_kernel<true> : mxfp4_quantize_kernel<false>,
+                    dim3(grid), kQuantThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_mxfp4_dequantize(const QuantArgs& a, void* out, int sms, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
-  return launch_kernel(mxfp4_dequantize_kernel, dim3(quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms)),
-                       kQuantThreads, 0, 1, stream, a, static_cast<uint4*>(out));
+  return launch_pdl(mxfp4_dequantize_kernel, dim3(quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms)),
+                    kQuantThreads, 0, 1, stream, a, static_cast<uint4*>(out));
 }
 
 cudaError_t launch_mxfp4_quantize_weights(const void* rhs, uint8_t* q, uint8_t* scales, int32_t g,
                                           int32_t k, int32_t n, int32_t scale_width,
                                           cudaStream_t stream) {
   const dim3 grid((n + kQuantThreads - 1) / kQuantThreads, scale_width, g);
-  return launch_kernel(mxfp4_weights_kernel, grid, kQuantThreads, 0, 1, stream,
-                       static_cast<const __nv_bfloat16*>(rhs), q, scales, k, n, scale_width);
+  return launch_pdl(mxfp4_weights_kernel, grid, kQuantThreads, 0, 1, stream,
+                    static_cast<const __nv_bfloat16*>(rhs), q, scales, k, n, scale_width);
 }
 
 }  // namespace rd

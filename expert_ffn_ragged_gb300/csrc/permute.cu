@@ -30,13 +30,15 @@ __device__ __forceinline__ int32_t rows_below(const int32_t* limit, int32_t rows
 
 __device__ __forceinline__ uint4 ld_row(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 
 __global__ void __launch_bounds__(kRowThreads) dispatch_rows_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
@@ -75,6 +77,8 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], uint4 y, float w) {
 // A warp owns B * 32 vectors of a token's row; the rows of S slots are in flight at once.
 template <int B, int S>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int pieces = (a.vecs + 32 * B - 1) / (32 * B);
@@ -137,6 +141,8 @@ __device__ __forceinline__ uint32_t scale_dot(uint32_t d, uint32_t y, float w, f
 }
 
 __global__ void __launch_bounds__(kRowThreads) combine_rows_bwd_kernel(const RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int32_t L = rows_below(a.limit, a.tokens);
   const int64_t slots = static_cast<int64_t>(L) * a.topk;
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_bwd_kernel(const Row
 #pragma unroll
         for (int b = 0; b < kRowBatch; ++b) {
           if (v0 + 32 * b < a.vecs) {
-            dv[b] = __ldg(dr + v0 + 32 * b);
+            dv[b] = dr[v0 + 32 * b];
             yv[b] = ld_row(yr + v0 + 32 * b);
           }
         }
@@ -194,7 +200,7 @@ int row_grid(int64_t units, int sms, int per_sm) {
 
 cudaError_t launch_dispatch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   const int64_t pieces = (a.vecs + 32 * kRowBatch - 1) / (32 * kRowBatch);
-  return launch_kernel(dispatch_rows_kernel, dim3(row_grid(a.tokens * pieces, sms, kDispatchBlocks)), kRowThreads, 0, 1, stream, a);
+  return launch_pdl(dispatch_rows_kernel, dim3(row_grid(a.tokens * pieces, sms, kDispatchBlocks)), kRowThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_combine_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
@@ -203,15 +209,15 @@ cudaError_t launch_combine_rows(const RowsArgs& a, int sms, cudaStream_t stream)
   // has little else to hide a load behind.
   const int64_t twos = static_cast<int64_t>(a.tokens) * ((a.vecs + 63) / 64);
   if (twos >= 64 * static_cast<int64_t>(sms))
-    return launch_kernel(combine_rows_kernel<2, 2>, dim3(row_grid(twos, sms, kCombineBlocks)), kRowThreads, 0, 1, stream, a);
+    return launch_pdl(combine_rows_kernel<2, 2>, dim3(row_grid(twos, sms, kCombineBlocks)), kRowThreads, 0, 1, stream, a);
   const int64_t ones = static_cast<int64_t>(a.tokens) * ((a.vecs + 31) / 32);
-  return launch_kernel(a.topk > 2 ? combine_rows_kernel<1, 4> : combine_rows_kernel<1, 2>,
-                       dim3(row_grid(ones, sms, kCombineBlocks)), kRowThreads, 0, 1, stream, a);
+  return launch_pdl(a.topk > 2 ? combine_rows_kernel<1, 4> : combine_rows_kernel<1, 2>,
+                    dim3(row_grid(ones, sms, kCombineBlocks)), kRowThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_combine_rows_bwd(const RowsArgs& a, int sms, cudaStream_t stream) {
-  return launch_kernel(combine_rows_bwd_kernel, dim3(row_grid(static_cast<int64_t>(a.tokens) * a.topk, sms, kCombineBwdBlocks)),
-                       kRowThreads, 0, 1, stream, a);
+  return launch_pdl(combine_rows_bwd_kernel, dim3(row_grid(static_cast<int64_t>(a.tokens) * a.topk, sms, kCombineBwdBlocks)),
+                    kRowThreads, 0, 1, stream, a);
 }
 
 }  // namespace rd

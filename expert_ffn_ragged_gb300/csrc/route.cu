@@ -95,7 +95,7 @@ __device__ __forceinline__ void load_row(const float* row, int e0, int experts, 
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
       float4 x = make_float4(kLow, kLow, kLow, kLow);
-      if (e0 + i < experts) x = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
+      if (e0 + i < experts) x = *reinterpret_cast<const float4*>(row + e0 + i);
       v[i] = x.x;
       v[i + 1] = x.y;
       v[i + 2] = x.z;
@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_row(const float* row, int e0, int experts, 
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = e0 + i < experts ? __ldg(row + e0 + i) : kLow;
+    for (int i = 0; i < EPL; ++i) v[i] = e0 + i < experts ? row[e0 + i] : kLow;
   }
 }
 
@@ -114,7 +114,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* row, int e0, int e
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
       uint2 x = make_uint2(0xFF80FF80u, 0xFF80FF80u);
-      if (e0 + i < experts) x = __ldg(reinterpret_cast<const uint2*>(row + e0 + i));
+      if (e0 + i < experts) x = *reinterpret_cast<const uint2*>(row + e0 + i);
       v[i] = __uint_as_float(x.x << 16);
       v[i + 1] = __uint_as_float(x.x & 0xFFFF0000u);
       v[i + 2] = __uint_as_float(x.y << 16);
@@ -172,7 +172,7 @@ __device__ __forceinline__ void slot_parts(const RouteArgs& a, bool there, float
 #pragma unroll
       for (int i = 0; i < EPL; ++i) top = fmaxf(top, logit[i]);  // a NaN logit loses
     }
-    top = warp_max(top);
+      top = warp_max(top);
     part = there ? expf(at - top) : 0.0f;
     float sum = part;
     if (!a.renormalize) {
@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
   int* cexp = reinterpret_cast<int*>(ckey + 32 * EPL + 4);
   int* chosen = cexp + 32 * EPL + 4;
   float* ranked = reinterpret_cast<float*>(chosen + 32);
+  pdl_trigger();
+  pdl_wait();
   if (a.bias != nullptr) {
     for (int e = threadIdx.x; e < 32 * EPL; e += kRouteWarps * 32) sbias[e] = e < a.experts ? a.bias[e] : 0.0f;
     __syncthreads();
@@ -417,6 +419,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
   extern __shared__ __align__(16) float smem_rows[];  // [warps][32 * EPL]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* srow = smem_rows + warp * 32 * EPL;
+  pdl_trigger();
+  pdl_wait();
   const int32_t L = tokens_below(a.limit, a.tokens);
   const bool dense = SCORE == RD_SCORE_SOFTMAX && !a.renormalize;
   const int e0 = lane * EPL;
@@ -503,8 +507,8 @@ cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
   a.vec = a.experts % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % unit == 0 &&
           reinterpret_cast<uintptr_t>(a.d_logits) % unit == 0;
   if (bwd) {
-    return launch_kernel(route_bwd_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32,
-                         sizeof(float) * kRouteWarps * 32 * EPL, 1, stream, a);
+    return launch_pdl(route_bwd_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32,
+                      sizeof(float) * kRouteWarps * 32 * EPL, 1, stream, a);
   }
   constexpr size_t smem = route_smem_bytes(EPL);
   if (smem > 48 * 1024) {
@@ -518,7 +522,7 @@ cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
       attr_set[dev].store(true, std::memory_order_release);
     }
   }
-  return launch_kernel(route_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32, smem, 1, stream, a);
+  return launch_pdl(route_kernel<EPL, T, SCORE>, dim3(grid), kRouteWarps * 32, smem, 1, stream, a);
 }
 
 template <int EPL, class T>

@@ -35,9 +35,9 @@ constexpr int kSortCluster = 16;  // most CTAs of a sort (one cluster; above 8 b
 
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32)
-    sort_rows_kernel(const int32_t* __restrict__ ids, int32_t tokens, int32_t topk, int32_t experts,
-                     const int32_t* limit, int32_t* __restrict__ group_sizes,
-                     int32_t* __restrict__ pos, int32_t* __restrict__ rows) {
+    sort_rows_kernel(const int32_t* ids, int32_t tokens, int32_t topk, int32_t experts,
+                     const int32_t* limit, int32_t* group_sizes,
+                     int32_t* pos, int32_t* rows) {
   // [warps][experts] counts, then first positions; [warps][experts] lane masks; [experts] the
   // CTA's sums; [experts] first rows
   extern __shared__ uint32_t smem[];
@@ -49,6 +49,8 @@ __global__ void __launch_bounds__(WARPS * 32)
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
   int32_t L = tokens;
   if (limit != nullptr) {
     const int32_t v = *limit;
@@ -188,8 +190,8 @@ cudaError_t launch_sort_rows(const int32_t* ids, int32_t tokens, int32_t topk, i
   const int64_t slots = static_cast<int64_t>(tokens) * topk;
   int ctas = 1;
   while (ctas < kSortCluster && slots > static_cast<int64_t>(ctas) * warps * 32 * kSortBatch) ctas *= 2;
-  return launch_kernel(kernel, dim3(ctas), warps * 32, sizeof(uint32_t) * (2 * warps + 2) * experts, ctas,
-                       stream, ids, tokens, topk, experts, limit, group_sizes, pos, rows);
+  return launch_pdl(kernel, dim3(ctas), warps * 32, sizeof(uint32_t) * (2 * warps + 2) * experts, ctas,
+                    stream, ids, tokens, topk, experts, limit, group_sizes, pos, rows);
 }
 
 }  // namespace rd
