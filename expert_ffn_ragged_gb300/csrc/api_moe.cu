@@ -388,13 +388,19 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   if ((st = current_device(&sms)) != RD_OK) return st;
   if (m == 0 || n == 0) return RD_OK;
 
+  // Tiles of 32 rows where the groups average at most 16 (most of them then hold a tile's rows or fewer):
+  // see gemm_mxfp4.cuh.
+  const bool pair = use_pair(sms, m, g_total);
+  const bool few = !pair && m <= 16 * static_cast<int64_t>(g_total);
+  const int tm = pair ? 2 * kBM : (few ? 32 : kBM);
   Gemm4Maps maps = {};
   if (k > 0) {
     // rows of k / 2 bytes as k / 4 two-byte elements, boxes of 128 bytes of a row; scale rows as
     // width / 2 such elements, boxes of 32 bytes
     const uint64_t da[2] = {static_cast<uint64_t>(k / 4), um};
     const uint64_t sa[1] = {static_cast<uint64_t>(k / 2)};
-    const uint32_t ba[2] = {64, kBM};
+    const uint32_t a_rows = few ? 32 : kBM;
+    const uint32_t ba[2] = {64, a_rows};
     if ((st = encode(&maps.a, a, 2, da, sa, ba)) != RD_OK) return st;
     const uint64_t db[3] = {static_cast<uint64_t>(k / 4), static_cast<uint64_t>(n), ug};
     const uint64_t sb[2] = {static_cast<uint64_t>(k / 2), static_cast<uint64_t>(n) * (k / 2)};
@@ -402,7 +408,7 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
     if ((st = encode(&maps.b, b, 3, db, sb, bb)) != RD_OK) return st;
     const uint64_t w = static_cast<uint64_t>(width);
     const uint64_t das[2] = {w / 2, um}, sas[1] = {w};
-    const uint32_t bas[2] = {16, kBM};
+    const uint32_t bas[2] = {16, a_rows};
     if ((st = encode(&maps.a_scales, a_scales, 2, das, sas, bas, CU_TENSOR_MAP_SWIZZLE_32B)) != RD_OK)
       return st;
     const uint64_t dbs[3] = {w / 2, static_cast<uint64_t>(n), ug}, sbs[2] = {w, static_cast<uint64_t>(n) * w};
@@ -410,7 +416,6 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
     if ((st = encode(&maps.b_scales, b_scales, 3, dbs, sbs, bbs, CU_TENSOR_MAP_SWIZZLE_32B)) != RD_OK)
       return st;
   }
-  const bool pair = use_pair(sms, m, g_total);
   const int tile_w = glu ? k4Half : k4BN;
   Gemm4Args g = {};
   g.group_sizes = group_sizes;
@@ -428,12 +433,11 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   g.n_tiles = static_cast<int32_t>((n_out + tile_w - 1) / tile_w);
   // a 4-bit row is a quarter of a bf16 row: bands of four times the rows keep as many bytes in L2
   // (32768 x 4096 x 14336: 623 -> 617 us, means of six)
-  g.band_tiles = band_tiles(pair, 4 * kBandRows);
+  g.band_tiles = band_tiles(pair, 4 * kBandRows) * (few ? kBM / 32 : 1);
   g.timeout_ns = wait_timeout_ns();
-  const int tm = pair ? 2 * kBM : kBM;
   const int64_t tiles = ((m + tm - 1) / tm + g_local) * g.n_tiles;
   if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
   const int grid = pair ? pair_grid(sms, tiles) : grid_for(sms, tiles);
   const int which = quant ? k4EpiGluQuant : (glu ? k4EpiGlu : k4EpiNone);
-  return done(launch_gemm_mxfp4(which, pair, maps, g, grid, cu(stream)));
+  return done(launch_gemm_mxfp4(which, pair ? k4Pair : (few ? k4Few : k4Single), maps, g, grid, cu(stream)));
 }

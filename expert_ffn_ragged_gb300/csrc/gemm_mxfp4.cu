@@ -4,11 +4,12 @@
 namespace rd {
 namespace {
 
-template <int EPI, bool PAIR>
+template <int EPI, int VAR>
 cudaError_t launch_impl(const Gemm4Maps& maps, const Gemm4Args& args, int grid, cudaStream_t stream) {
-  constexpr size_t smem = gemm4_smem_bytes<PAIR>();
+  constexpr bool PAIR = VAR == k4Pair;
+  constexpr size_t smem = gemm4_smem_bytes<VAR>();
   static_assert(smem <= 232448, "shared memory of one CTA");
-  const auto kernel = grouped_gemm_mxfp4_kernel<EPI, PAIR>;
+  const auto kernel = grouped_gemm_mxfp4_kernel<EPI, VAR>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -46,22 +47,25 @@ cudaError_t launch_impl(const Gemm4Maps& maps, const Gemm4Args& args, int grid, 
                     args);
 }
 
-template <bool PAIR>
+template <int VAR>
 cudaError_t launch_epi(int epi, const Gemm4Maps& maps, const Gemm4Args& args, int grid,
                        cudaStream_t stream) {
   switch (epi) {
-    case k4EpiNone: return launch_impl<k4EpiNone, PAIR>(maps, args, grid, stream);
-    case k4EpiGlu: return launch_impl<k4EpiGlu, PAIR>(maps, args, grid, stream);
-    default: return launch_impl<k4EpiGluQuant, PAIR>(maps, args, grid, stream);
+    case k4EpiNone: return launch_impl<k4EpiNone, VAR>(maps, args, grid, stream);
+    case k4EpiGlu: return launch_impl<k4EpiGlu, VAR>(maps, args, grid, stream);
+    default: return launch_impl<k4EpiGluQuant, VAR>(maps, args, grid, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_mxfp4(int epi, bool pair, const Gemm4Maps& maps, const Gemm4Args& args,
+cudaError_t launch_gemm_mxfp4(int epi, int variant, const Gemm4Maps& maps, const Gemm4Args& args,
                               int grid, cudaStream_t stream) {
-  return pair ? launch_epi<true>(epi, maps, args, grid, stream)
-              : launch_epi<false>(epi, maps, args, grid, stream);
+  switch (variant) {
+    case k4Pair: return launch_epi<k4Pair>(epi, maps, args, grid, stream);
+    case k4Single: return launch_epi<k4Single>(epi, maps, args, grid, stream);
+    default: return launch_epi<k4Few>(epi, maps, args, grid, stream);
+  }
 }
 
 }  // namespace rd

@@ -29,10 +29,10 @@
 //
 // Bound and measured: large groups by the tensor cores (one pair MMA of 256 x 192 x 64 takes 96 cycles:
 // 10.3 PFLOP/s at 2.07 GHz) and, back to back, by the power limit: 32768 x 4096 x 14336 over 8 experts
-// 601 us alone (6.4 PFLOP/s), 678 in a loop at the power cap.  Few rows an expert by the weights' bytes:
-// 256 tokens top-8 of 128 experts, up 69 us (419 MB: 6.1 TB/s), down 41 us (214 MB: 5.2 TB/s, with every
-// tile fetching 128 rows of A of which 16 are used).  One token: 14 and 9 us, the chain of a few stages on
-// 64 SMs.
+// 600 us alone (6.4 PFLOP/s), 680 in a loop at the power cap.  Few rows an expert by the weights' bytes:
+// 256 tokens top-8 of 128 experts, up 67 us (419 MB: 6.3 TB/s), down 39 us (214 MB: 5.5 TB/s; start and
+// end of a launch, about 6 us, weigh more there).  One token: 11 and 7.5 us, a chain of a few stages on 64
+// SMs.
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -49,8 +49,6 @@ constexpr int k4Threads = 480;
 constexpr int k4ScaleWarps = 4;
 constexpr int k4RawK = 1024;    // elements of k of a shared-memory scale slot (32 scale bytes a row)
 constexpr int k4RawSlots = 3;
-constexpr int k4RawA = kBM * 32;
-constexpr int k4RawBytes = (kBM + k4BN) * 32;
 // Tensor memory: two accumulators, then the scale columns of each stage: per word (128 elements of
 // k) 4 columns for A's 128 rows, then per word 6 for B's 192.
 constexpr int k4ScaleCol = 2 * k4BN;
@@ -58,6 +56,14 @@ constexpr int k4WordColsA = kBM / 32;
 constexpr int k4WordColsB = k4BN / 32;
 
 enum Gemm4Epi : int { k4EpiNone = 0, k4EpiGlu = 1, k4EpiGluQuant = 2 };
+
+// Tiles: of 256 rows on a CTA pair, of 128 rows on one CTA, or of 32 rows on one CTA for groups of few
+// rows.  The last is the 128-row MMA with rows of its own in the last lane quarter only: its A copies are
+// a quarter as large, which makes room for six stages of B in place of four, and what the MMA reads as
+// the other 96 rows is whatever lies before them in shared memory (any bits are E2M1 numbers, and no warp
+// looks at those accumulator rows).  Against 128-row tiles: one token 28.4 -> 26.1 us, 256 tokens 122.1 ->
+// 120.7.
+enum Gemm4Variant : int { k4Pair = 0, k4Single = 1, k4Few = 2 };
 
 struct Gemm4Args {
   const int32_t* group_sizes;
@@ -83,27 +89,37 @@ struct Gemm4Maps {
   CUtensorMap a, b, a_scales, b_scales;
 };
 
-template <bool PAIR>
+template <int VAR>
 struct Tile4Cfg {
-  static constexpr int kStagesN = PAIR ? 3 : 4;
-  static constexpr int kSub = PAIR ? 2 : 1;            // 256-element blocks of a stage
-  static constexpr int kTileM = PAIR ? 2 * kBM : kBM;
-  static constexpr int kBRows = PAIR ? k4Half : k4BN;  // B rows held by one CTA
-  static constexpr int kSubA = kBM * 128;              // 16 KB
-  static constexpr int kSubB = kBRows * 128;           // 12 KB (pair) or 24 KB
+  static constexpr bool kPair = VAR == k4Pair;
+  static constexpr bool kFew = VAR == k4Few;
+  static constexpr int kStagesN = kPair ? 3 : (kFew ? 6 : 4);
+  static constexpr int kSub = kPair ? 2 : 1;            // 256-element blocks of a stage
+  static constexpr int kMmaM = kPair ? 2 * kBM : kBM;
+  static constexpr int kARows = kFew ? 32 : kBM;        // A rows held by one CTA
+  static constexpr int kTileM = kPair ? 2 * kBM : kARows;
+  static constexpr int kBRows = kPair ? k4Half : k4BN;  // B rows held by one CTA
+  static constexpr int kSubA = kARows * 128;            // 16 KB, or 4 KB
+  static constexpr int kSubB = kBRows * 128;            // 12 KB (pair) or 24 KB
   static constexpr int kStageA = kSub * kSubA;
   static constexpr int kStageB = kSub * kSubB;
   static constexpr int kStageBytes = kStageA + kStageB;
+  // A after B where the MMA's first rows lie before it, else before
+  static constexpr int kOffA = kFew ? kStagesN * kStageB : 0;
+  static constexpr int kOffB = kFew ? 0 : kStagesN * kStageA;
+  static constexpr int kRowsBefore = kBM - kARows;      // MMA rows that are not the tile's
+  static constexpr int kRawA = kARows * 32;             // scales of A's rows in a slot, then B's
+  static constexpr int kRawBytes = kRawA + k4BN * 32;
   static constexpr int kWords = 2 * kSub;              // scale words of a row per stage
   static constexpr int kColsA = kWords * k4WordColsA;  // scale columns of a stage: A's, then B's
   static constexpr int kCols = kColsA + kWords * k4WordColsB;
   static_assert(k4ScaleCol + kStagesN * kCols <= kTmemCols, "tensor memory");
 };
 
-template <bool PAIR>
+template <int VAR>
 struct alignas(128) Gemm4Shared {
-  static constexpr int S = Tile4Cfg<PAIR>::kStagesN;
-  uint8_t raw[k4RawSlots][k4RawBytes];  // first: TMA destinations (128-byte aligned)
+  static constexpr int S = Tile4Cfg<VAR>::kStagesN;
+  uint8_t raw[k4RawSlots][Tile4Cfg<VAR>::kRawBytes];  // first: TMA destinations (128-byte aligned)
   uint64_t full[S];
   uint64_t empty[S];
   uint64_t rfull[k4RawSlots];
@@ -122,20 +138,20 @@ struct alignas(128) Gemm4Shared {
   uint4 epi[kEpiWarps][32 * 4];
 };
 
-template <bool PAIR>
+template <int VAR>
 constexpr size_t gemm4_smem_bytes() {
-  return 1024 + static_cast<size_t>(Tile4Cfg<PAIR>::kStagesN) * Tile4Cfg<PAIR>::kStageBytes +
-         sizeof(Gemm4Shared<PAIR>);
+  return 1024 + static_cast<size_t>(Tile4Cfg<VAR>::kStagesN) * Tile4Cfg<VAR>::kStageBytes +
+         sizeof(Gemm4Shared<VAR>);
 }
 
 // Tile t, as decode_tile_view has it.  A role's tiles only ever move forward, so the group is searched
 // from that of its last tile on (`hint`); the divisions are left out where a group is one m-tile
 // high, as in decoding, or one band.
-template <bool PAIR>
-__device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<PAIR>& sh, const Gemm4Args& a, int t,
+template <int VAR>
+__device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<VAR>& sh, const Gemm4Args& a, int t,
                                              int& hint) {
-  constexpr int TM = Tile4Cfg<PAIR>::kTileM;
-  constexpr int kStageK = Tile4Cfg<PAIR>::kSub * k4BK;
+  constexpr int TM = Tile4Cfg<VAR>::kTileM;
+  constexpr int kStageK = Tile4Cfg<VAR>::kSub * k4BK;
   int j = hint;
   if (sh.tile_start[j + 1] <= t) {
     int hi = a.g_local;  // tile_start[j] <= t < tile_start[hi]
@@ -188,20 +204,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
-template <int EPI, bool PAIR>
+template <int EPI, int VAR>
 __global__ void __launch_bounds__(k4Threads, 1)
     grouped_gemm_mxfp4_kernel(const __grid_constant__ Gemm4Maps maps, const Gemm4Args args) {
   constexpr bool GLU = EPI != k4EpiNone;
-  using Cfg = Tile4Cfg<PAIR>;
+  using Cfg = Tile4Cfg<VAR>;
+  constexpr bool PAIR = Cfg::kPair;
   constexpr int S = Cfg::kStagesN;
   constexpr int TM = Cfg::kTileM;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + S * Cfg::kStageA;
-  Gemm4Shared<PAIR>& sh = *reinterpret_cast<Gemm4Shared<PAIR>*>(smem + S * Cfg::kStageBytes);
+  uint8_t* sA = smem + Cfg::kOffA;
+  uint8_t* sB = smem + Cfg::kOffB;
+  Gemm4Shared<VAR>& sh = *reinterpret_cast<Gemm4Shared<VAR>*>(smem + S * Cfg::kStageBytes);
 
   // the same in every lane of a warp, which the compiler cannot see of threadIdx.x >> 5
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       uint32_t pend_mask = 0, pend_par = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
+        const Tile tl = decode_tile4<VAR>(sh, args, t, group);
         const int arow = tl.row_load + static_cast<int>(rank) * kBM;
         // the 96-row boxes of b: one per CTA of a pair, two on a single CTA
         const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
@@ -329,10 +346,10 @@ __global__ void __launch_bounds__(k4Threads, 1)
     // lane issues.  A wait that gives up only raises the abort flag: the MMAs after it compute on
     // whatever is there, and the loop is left at the next tile.
     if (leader) {
-      constexpr uint32_t idesc0 = ptx::idesc_mxfp4_f32(TM, k4BN, 0);
-      constexpr uint32_t idesc2 = ptx::idesc_mxfp4_f32(TM, k4BN, 2);
+      constexpr uint32_t idesc0 = ptx::idesc_mxfp4_f32(Cfg::kMmaM, k4BN, 0);
+      constexpr uint32_t idesc2 = ptx::idesc_mxfp4_f32(Cfg::kMmaM, k4BN, 2);
       // operand descriptors of stage 0; a stage, and a K step of 32 bytes, move the address field
-      const uint64_t a_desc0 = ptx::sw128_desc(ptx::smem_addr(sA), 16, 1024);
+      const uint64_t a_desc0 = ptx::sw128_desc(ptx::smem_addr(sA) - Cfg::kRowsBefore * 128, 16, 1024);
       const uint64_t b_desc0 = ptx::sw128_desc(ptx::smem_addr(sB), 16, 1024);
       const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
       const int tiles = __shfl_sync(0xFFFFFFFFu, total, 0);
@@ -419,8 +436,8 @@ __global__ void __launch_bounds__(k4Threads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = unit; t < total; t += units) {
-      const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
-      const int wrow0 = tl.row_load + static_cast<int>(rank) * kBM + q * 32;
+      const Tile tl = decode_tile4<VAR>(sh, args, t, group);
+      const int wrow0 = tl.row_load + static_cast<int>(rank) * kBM + q * 32 - Cfg::kRowsBefore;
       const int lo = tile_store_lo(tl, TM), hi = tile_store_hi(tl);
       const int col0 = tl.n_idx * tile_w;
       // this lane's 32 columns of its row to global memory, through a transpose (8 rows x 64
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       uint32_t phase = 0, pend_mask = 0, pend_par = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
+        const Tile tl = decode_tile4<VAR>(sh, args, t, group);
         const int arow = tl.row_load + static_cast<int>(rank) * kBM;
         const int brow0 = b_row_of<GLU>(tl.n_idx, 0, args.n_out);
         const int brow1 = b_row_of<GLU>(tl.n_idx, k4Half, args.n_out);
@@ -560,11 +577,11 @@ __global__ void __launch_bounds__(k4Threads, 1)
           if (!ok) break;
           const uint32_t rb = ptx::smem_addr(&sh.rfull[slot]);
           const uint32_t dst = ptx::smem_addr(sh.raw[slot]);
-          ptx::mbar_arrive_expect_tx(rb, k4RawBytes);
+          ptx::mbar_arrive_expect_tx(rb, Cfg::kRawBytes);
           const int x = k0 / (2 * kMxBlock);  // two scale bytes a map element
           ptx::tma_load_2d(dst, &maps.a_scales, rb, x, arow);
-          ptx::tma_load_3d(dst + k4RawA, &maps.b_scales, rb, x, brow0, tl.j);
-          ptx::tma_load_3d(dst + k4RawA + k4Half * 32, &maps.b_scales, rb, x, brow1, tl.j);
+          ptx::tma_load_3d(dst + Cfg::kRawA, &maps.b_scales, rb, x, brow0, tl.j);
+          ptx::tma_load_3d(dst + Cfg::kRawA + k4Half * 32, &maps.b_scales, rb, x, brow1, tl.j);
           pend_mask |= 1u << slot;
           pend_par = (pend_par & ~(1u << slot)) | (phase << slot);
           if (++slot == k4RawSlots) {
@@ -595,7 +612,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
     uint32_t raw_phase = 0, phase = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      const Tile tl = decode_tile4<PAIR>(sh, args, t, group);
+      const Tile tl = decode_tile4<VAR>(sh, args, t, group);
       for (int kb = 0; kb < tl.nkb; ++kb) {
         const int k0 = kb * kStageK;
         if (k0 % k4RawK == 0) {
@@ -607,14 +624,17 @@ __global__ void __launch_bounds__(k4Threads, 1)
         uint32_t v[kRowsL][kW];
 #pragma unroll
         for (int i = 0; i < kRowsL; ++i) {
-          if constexpr (kW == 4) {
+          if (i < Cfg::kRowsBefore / 32) {
+#pragma unroll
+            for (int w = 0; w < kW; ++w) v[i][w] = 0;
+          } else if constexpr (kW == 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(src + i * 32 * 32);
             v[i][0] = x.x;
             v[i][1] = x.y;
             v[i][2] = x.z;
             v[i][3] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(src + i * 32 * 32);
+            const uint2 x = *reinterpret_cast<const uint2*>(src + (i - Cfg::kRowsBefore / 32) * 32 * 32);
             v[i][0] = x.x;
             v[i][1] = x.y;
           }

@@ -76,7 +76,7 @@ cudaError_t launch_mxfp4_quantize_weights(const void* rhs, uint8_t* q, uint8_t* 
 
 struct Gemm4Maps;
 struct Gemm4Args;
-cudaError_t launch_gemm_mxfp4(int epi, bool pair, const Gemm4Maps& maps, const Gemm4Args& args,
+cudaError_t launch_gemm_mxfp4(int epi, int variant, const Gemm4Maps& maps, const Gemm4Args& args,
                               int grid, cudaStream_t stream);
 
 }  // namespace rd

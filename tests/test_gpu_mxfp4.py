@@ -241,6 +241,19 @@ def test_product_group_shapes(rd_lib, variant, m, sizes):
         _run(rd_lib, epi, m, 288, 384, sizes, seed=m)
 
 
+@pytest.mark.parametrize("epi", [0, 1, 2])
+@pytest.mark.parametrize("k,n,band_rows,limit", [(32, 64, 0, None), (1184, 192, 128, None), (2080, 448, 0, 801),
+                                                 (288, 832, 256, 500)])
+def test_product_few_rows_a_group(rd_lib, epi, k, n, band_rows, limit):
+    """At most 16 rows a group on average: tiles of 32 rows, with groups of several tiles (and bands of
+    four or eight tiles) among them."""
+    sizes = [0, 1, 31, 32, 33, 64, 65, 200, 2, 250, 0] + [5, 0, 17, 1] * 13
+    m = sum(sizes) + 11
+    assert m <= 16 * len(sizes)
+    with rd_lib.tuning(band_rows=band_rows):
+        _run(rd_lib, epi, m, k, n, sizes, off=1, gl=len(sizes) - 3, limit=limit, seed=k + n + epi)
+
+
 def test_product_of_nothing(rd_lib, variant):
     u8 = dict(dtype=torch.uint8, device=DEV)
     none = rd_lib.ragged_dot_mxfp4(torch.empty((0, 16), **u8), torch.empty((0, 16), **u8), torch.zeros((2, 8, 16), **u8),
