@@ -106,17 +106,21 @@ def _word(t, name, idx):
     return t.data_ptr()
 
 
-_current_device = None
+_current_device = _raw_stream = None
 
 
 def _launch(fn, name, idx, device, stream, *args):
     """Call an entry point on the tensors' device, on its current stream or ``stream``."""
-    global _current_device
+    global _current_device, _raw_stream
     if _current_device is None:
         torch = _rd._torch()
         # without the lazy-initialisation check of the public function, where it exists
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    handle = _rd._stream(stream, device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(idx)
+    else:
+        handle = _rd._stream(stream, device)
     if _current_device() == idx:
         code = fn(*args, handle)
     else:
