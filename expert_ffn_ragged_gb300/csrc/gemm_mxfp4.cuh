@@ -20,16 +20,17 @@
 //     core wants, for 128 elements of k, row r's four scale bytes in lane r % 32 of column r / 32,
 //     repeated in every lane quarter.  Every ring stage has scale columns of its own, so the scales
 //     run as far ahead as the operands (with two slots of 512 elements for three such stages the
-//     MMAs waited for them: 710 cycles per 256 elements).  No padding of groups and no packing of the scales is needed,
-//     and the row shift of a group's last tile is free.  (Loaded straight from global memory into
-//     registers and passed on through shared memory, the scales held the MMAs to 1350 cycles per
-//     256 elements of k.)
+//     MMAs waited for them: 710 cycles per 256 elements).  No padding of groups and no packing of the
+//     scales is needed, and the row shift of a group's last tile is free.  (Loaded straight from
+//     global memory into registers and passed on through shared memory, the scales held the MMAs to
+//     1350 cycles per 256 elements of k.)
 // Warps: 0 operand producer, 1 MMA issuer, 2-9 epilogue, 10-13 scales, 14 scale producer.  Zero rows
 // are written by the epilogue warps when their tiles are done.
 //
 // Bound and measured: large groups by the tensor cores (one pair MMA of 256 x 192 x 64 takes 96 cycles:
 // 10.3 PFLOP/s at 2.07 GHz) and, back to back, by the power limit: 32768 x 4096 x 14336 over 8 experts
-// 600 us alone (6.4 PFLOP/s), 680 in a loop at the power cap.  Few rows an expert by the weights' bytes:
+// 600 us alone (6.4 PFLOP/s), 680 in a loop at the power cap; of the 600, left out one after another,
+// 100 go with the operands' copies, 65 with the output's stores, 400 are MMAs and tile padding.  Few rows an expert by the weights' bytes:
 // 256 tokens top-8 of 128 experts, up 67 us (419 MB: 6.3 TB/s), down 39 us (214 MB: 5.5 TB/s; start and
 // end of a launch, about 6 us, weigh more there).  One token: 11 and 7.5 us, a chain of a few stages on 64
 // SMs.
@@ -521,8 +522,8 @@ __global__ void __launch_bounds__(k4Threads, 1)
         } else {
           // Chunk by chunk.  All three read at once and the accumulator given back before the stores
           // was slower where the outputs dominate (131072 x 768 x 4096: 297 -> 334 us), as were stores
-          // of 32 bytes a lane without the transpose (32768 x 4096 x 14336: 620 -> 680); stores of
-          // whole 128-byte lines made no difference.
+          // of 32 bytes a lane without the transpose (32768 x 4096 x 14336: 620 -> 680); whole 128-byte
+          // lines (604 -> 613) and bulk tensor stores (603 -> 599, one token 26.4 -> 27.0) were no better.
           uint32_t v[32], p[16];
           ptx::tmem_load_32cols(tbase + c * 32, v);
 #pragma unroll

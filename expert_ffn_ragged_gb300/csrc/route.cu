@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     // a softmax sum is 1 .. experts (0 without an expert, NaN with a +inf logit)
     const float inv = total <= 0.0f ? 0.0f
                                     : (SCORE == RD_SCORE_SOFTMAX ? reciprocal_fast(total) : __fdiv_rn(1.0f, total));
-    const float q = part * inv;
+    // a quotient, so that a slot that is all of the sum has weight one and a gradient of exactly zero
+    const float q = SCORE == RD_SCORE_SOFTMAX || total <= 0.0f ? part * inv : __fdiv_rn(part, total);
     const float mean = warp_sum(there ? q * d : 0.0f);
     float v[EPL];
 #pragma unroll

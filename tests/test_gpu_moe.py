@@ -231,6 +231,18 @@ def test_token_limit(rd_lib):
         assert bool((g[L:] == 6.0).all()) and bool(g[:L].isfinite().all())
 
 
+@pytest.mark.parametrize("score", [moe.SOFTMAX, moe.SIGMOID])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_of_a_constant_weight(rd_lib, score, dtype):
+    """One expert a token, renormalised: its weight is the scale whatever the logits are, so the gradient is zero."""
+    rng = np.random.default_rng(21)
+    logits = torch.from_numpy(4 * rng.normal(size=(777, 24)).astype(np.float32)).to(dtype).to(DEV)
+    r = rd_lib.route(logits, 1, score=score, scale=2.5)
+    assert bool((r.weights == 2.5).all())
+    d_w = torch.from_numpy(rng.normal(size=(777, 1)).astype(np.float32)).to(DEV)
+    assert not rd_lib.route_bwd(logits, r.ids, d_w, score=score, scale=2.5).any()
+
+
 def _slots(rng, tokens, topk, rows):
     """Positions of some slots, without repeats; others have no row (-1 or far outside)."""
     pos = np.full(tokens * topk, -1)
