@@ -197,7 +197,7 @@ constexpr size_t route_smem_bytes(int epl) {
   return sizeof(float) * (32 * epl + kRouteWarps * route_warp_words(epl));
 }
 
-// How many of the n values (a multiple of four, in shared memory) are larger than v.
+// How many of the n values (a multiple of four, in shared memory) are larger than v; none of them is -0.
 __device__ __forceinline__ int count_larger(const float* values, int n, float v) {
   int c = 0;
 #pragma unroll 8
@@ -265,8 +265,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
     if (SCORE == RD_SCORE_SIGMOID) {
       sigmoids_f32<EPL>(logit, key);
     } else {
+      // -0 + 0 is 0: the ranking below takes the sign of a difference, which tells zeros of unlike signs
+      // apart.  A sum with a bias is no -0 then either, and a sigmoid never is.
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) key[i] = logit[i];
+      for (int i = 0; i < EPL; ++i) key[i] = __fadd_rn(logit[i], 0.0f);
     }
     if (a.bias != nullptr) {
       float b[EPL];
