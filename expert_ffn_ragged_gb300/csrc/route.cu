@@ -454,11 +454,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     if (t + stride < L) fetch(t + stride);
     float part, total, ex[EPL];
     slot_parts<EPL, SCORE>(a, there, at, logit, ex, part, total);
-    // a softmax sum is 1 .. experts (0 without an expert, NaN with a +inf logit)
-    const float inv = total <= 0.0f ? 0.0f
-                                    : (SCORE == RD_SCORE_SOFTMAX ? reciprocal_fast(total) : __fdiv_rn(1.0f, total));
+    // A softmax sum is 1 .. experts (0 without an expert, NaN with a +inf logit).  One of sigmoids may be a
+    // subnormal number: its reciprocal, and d / sum, would be infinite where the share and the gradient are not.
+    const float inv = SCORE == RD_SCORE_SOFTMAX && !(total <= 0.0f) ? reciprocal_fast(total) : 0.0f;
     // a quotient, so that a slot that is all of the sum has weight one and a gradient of exactly zero
-    const float q = SCORE == RD_SCORE_SOFTMAX || total <= 0.0f ? part * inv : __fdiv_rn(part, total);
+    const float q = SCORE == RD_SCORE_SOFTMAX ? part * inv : (total <= 0.0f ? 0.0f : __fdiv_rn(part, total));
     const float mean = warp_sum(there ? q * d : 0.0f);
     float v[EPL];
 #pragma unroll
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     if (there) {
       float g;
       if (SCORE == RD_SCORE_SOFTMAX) g = a.scale * q * (d - mean);
-      else g = a.scale * (a.renormalize ? (d - mean) * inv : d) * part * (1.0f - part);
+      else g = a.scale * (a.renormalize ? q * (d - mean) : d * part) * (1.0f - part);
       srow[id] = g;
     }
     __syncwarp();

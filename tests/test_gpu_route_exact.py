@@ -1,4 +1,11 @@
-"""The router's choice held to its definition exactly, and its gradient at the ends of the range."""
+"""The router's choice held to its definition exactly, and its gradient at the ends of the range.
+
+Tolerance of the sigmoid gradient at very negative logits: the relative error of a score is a few units of
+2^-23 (two ulps of exp, one each of the sum and the reciprocal; the scores stay above 2^18 units of the
+smallest subnormal, so their spacing adds less), of a share twice that and one division, of the sums of
+at most 32 slots 5 units: 2^-23 * 64 of scale * share * (|d| + sum |q d|) holds them all; bf16 output
+adds half an ulp, 2^-8 relative.
+"""
 import numpy as np
 import pytest
 
@@ -34,3 +41,31 @@ def test_zeros_of_either_sign_tie(rd_lib, experts, topk, groups, topk_groups, dt
         for t in range(tokens):
             ref = moe.route_weights(l[t].double().numpy(), want[t], moe.SOFTMAX, True)
             assert np.all(np.abs(r.weights[t].double().cpu().numpy() - ref) <= 2.0 ** -23 * 64 * ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_of_tiny_scores(rd_lib, renorm, dtype):
+    """All logits far below zero: the scores and their sum are near the smallest normal number, the gradient
+    of the renormalised weights is of the order of d all the same."""
+    rng = np.random.default_rng(5)
+    tokens, experts, topk, scale = 200, 24, 4, 1.5
+    l = torch.from_numpy(rng.uniform(-88.0, -80.0, size=(tokens, experts)).astype(np.float32))
+    l = l.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    ids = np.array([rng.permutation(experts)[:topk] for _ in range(tokens)])
+    d = (rng.normal(size=(tokens, topk)) * 10.0 ** rng.uniform(0, 5, size=(tokens, 1))).astype(np.float32)
+    out = rd_lib.route_bwd(l.to(DEV), torch.tensor(ids, dtype=torch.int32, device=DEV), torch.from_numpy(d).to(DEV),
+                           score=rd_lib.SCORE_SIGMOID, renormalize=renorm, scale=scale)
+    got, l64 = out.double().cpu().numpy(), l.double().numpy()
+    for t in range(tokens):
+        ref = moe.route_loss_grad(l64[t], ids[t], d[t], moe.SIGMOID, renorm, scale)
+        s = moe.sigmoid(l64[t][ids[t]])
+        q = s / s.sum()
+        spread = np.abs(d[t]).max() + np.abs(q * d[t]).sum()
+        tol = np.zeros(experts)
+        tol[ids[t]] = 2.0 ** -23 * 64 * scale * (q if renorm else s) * spread
+        if dtype == "bf16":
+            tol += 2.0 ** -8 * np.abs(ref)
+        # a subnormal result is within half a unit of the format's smallest number
+        tol += 2.0 ** -149 if dtype == "f32" else 2.0 ** -133
+        assert np.all(np.abs(got[t] - ref) <= tol), t
