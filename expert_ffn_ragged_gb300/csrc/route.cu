@@ -251,16 +251,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
   const int lpg = gsize / EPL;
   const bool lane_groups = gsize % EPL == 0 && (lpg & (lpg - 1)) == 0;
   const int my_group = lane_groups ? lane / lpg : 0;
-  const int stride = gridDim.x * kRouteWarps;
+  // Near 2^31 tokens t + stride leaves 32 bits: `last` decides whether there is a next token, and the step
+  // after the last one is unsigned.
+  const int stride = gridDim.x * kRouteWarps, last = L - stride;
   int t = blockIdx.x * kRouteWarps + warp;
   float next[EPL];
   if (t < L) load_row<EPL>(logits + static_cast<int64_t>(t) * a.experts, e0, a.experts, a.vec, next);
-  for (; t < L; t += stride) {
+  for (bool more = t < L; more; t += static_cast<uint32_t>(stride)) {
     const T* row = logits + static_cast<int64_t>(t) * a.experts;
     float logit[EPL], key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) logit[i] = next[i];
-    if (t + stride < L)  // the next token's row, under this one's work
+    more = t < last;
+    if (more)  // the next token's row, under this one's work
       load_row<EPL>(row + static_cast<int64_t>(stride) * a.experts, e0, a.experts, a.vec, next);
     if (SCORE == RD_SCORE_SIGMOID) {
       sigmoids_f32<EPL>(logit, key);
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
   const int32_t L = tokens_below(a.limit, a.tokens);
   const bool dense = SCORE == RD_SCORE_SOFTMAX && !a.renormalize;
   const int e0 = lane * EPL;
-  const int stride = gridDim.x * kRouteWarps;
+  const int stride = gridDim.x * kRouteWarps, last = L - stride;  // as above
   const T* logits = static_cast<const T*>(a.logits);
   int t = blockIdx.x * kRouteWarps + warp;
   float next[EPL];
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     }
   };
   if (t < L) fetch(t);
-  for (; t < L; t += stride) {
+  for (bool more = t < L; more; t += static_cast<uint32_t>(stride)) {
     const T* row = logits + static_cast<int64_t>(t) * a.experts;
     T* out = static_cast<T*>(a.d_logits) + static_cast<int64_t>(t) * a.experts;
     float logit[EPL];
@@ -451,7 +454,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
     const bool there = lane < a.topk && id >= 0 && id < a.experts;
     const float d = there ? next_d : 0.0f;
     const float at = there ? load_logit(row + id) : 0.0f;
-    if (t + stride < L) fetch(t + stride);
+    more = t < last;
+    if (more) fetch(t + stride);
     float part, total, ex[EPL];
     slot_parts<EPL, SCORE>(a, there, at, logit, ex, part, total);
     // A softmax sum is 1 .. experts (0 without an expert, NaN with a +inf logit).  One of sigmoids may be a
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
 
 template <int EPL, class T, int SCORE>
 cudaError_t launch_score(RouteArgs a, bool bwd, int sms, cudaStream_t stream) {
-  const int64_t blocks = (a.tokens + kRouteWarps - 1) / kRouteWarps;
+  const int64_t blocks = (static_cast<int64_t>(a.tokens) + kRouteWarps - 1) / kRouteWarps;
   // blocks an SM: two rounds of the four that fit (route), two of the six that fit (its gradient; with
   // 8 the second round is a third full: 65536 x 128 17.7 us against 16.9)
   const int most = sms * (bwd ? 12 : 8);

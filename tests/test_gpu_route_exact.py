@@ -69,3 +69,42 @@ def test_sigmoid_gradient_of_tiny_scores(rd_lib, renorm, dtype):
         # a subnormal result is within half a unit of the format's smallest number
         tol += 2.0 ** -149 if dtype == "f32" else 2.0 ** -133
         assert np.all(np.abs(got[t] - ref) <= tol), t
+
+
+def test_largest_token_count(rd_lib):
+    """2^31 - 1 tokens of one expert, the most that a call takes: every token is visited once, the last ones
+    too, and nothing outside the outputs is written."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of free device memory")
+    tokens, pad = 2 ** 31 - 1, 64
+    masked = [0, 1, 9727, 2 ** 30, tokens - 14593, tokens - 9729, tokens - 8, tokens - 1]
+    logits = torch.zeros((tokens, 1), dtype=torch.bfloat16, device=DEV)
+    logits[masked] = float("-inf")
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 2 * pad,), 77, dtype=dtype, device=DEV)
+        return buf, buf[pad:pad + n].view(shape)
+
+    def intact(buf):
+        return bool((buf[:pad] == 77).all()) and bool((buf[-pad:] == 77).all())
+
+    bufs = [guarded(s, d) for s, d in (((tokens, 1), torch.int32), ((tokens, 1), torch.float32), ((1,), torch.int32),
+                                       ((tokens, 1), torch.int32), ((1,), torch.int32))]
+    r = rd_lib.route(logits, 1, out=rd_lib.Routing(*[v for _, v in bufs]))
+    live = tokens - len(masked)
+    assert int(r.rows) == live and r.group_sizes.tolist() == [live]
+    assert all(intact(b) for b, _ in bufs)
+    assert r.ids[masked].flatten().tolist() == [-1] * len(masked) and int((r.ids == 0).sum()) == live
+    assert not r.weights[masked].any() and int((r.weights == 1).sum()) == live
+    assert r.pos[masked].flatten().tolist() == [-1] * len(masked)
+    assert r.pos[[2, 9728, tokens - 2]].flatten().tolist() == [0, 9725, live - 1]
+    ids = r.ids
+    del bufs, r
+    d = torch.full((tokens, 1), 2.0, device=DEV)
+    buf, out = guarded((tokens, 1), torch.bfloat16)
+    rd_lib.route_bwd(logits, ids, d, score=rd_lib.SCORE_SIGMOID, renormalize=False, out=out)
+    assert intact(buf)
+    assert not out[masked].any() and int((out == 0.5).sum()) == live
+    del logits, ids, d, buf, out
+    torch.cuda.empty_cache()
