@@ -1,4 +1,6 @@
-"""The router's choice held to its definition exactly, and its gradient at the ends of the range.
+"""The router's choice held to its definition exactly: the keys are f32, so the ids, their order and every
+tie follow from the bits of elementwise f32 arithmetic, which torch computes here on the same device.
+And its gradient at the ends of the range.
 
 Tolerance of the sigmoid gradient at very negative logits: the relative error of a score is a few units of
 2^-23 (two ulps of exp, one each of the sum and the reciprocal; the scores stay above 2^18 units of the
@@ -15,6 +17,29 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+LOW = float("-inf")
+
+
+def _choose_f32(logits, bias, topk, score, groups, topk_groups):
+    """Expert ids from keys in elementwise f32, best first, ties to the lower index, -1 where none is left."""
+    l = logits.float()
+    t, e = l.shape
+    masked = torch.isnan(l) | (l == LOW)
+    key = l if score == moe.SOFTMAX else 1.0 / (1.0 + torch.exp(-l))
+    if bias is not None:
+        key = key + bias
+    key = torch.where(masked, torch.full_like(key, LOW), key).cpu()
+    if groups > 1:
+        best = torch.topk(key.view(t, groups, e // groups), min(2, e // groups), dim=2).values
+        first = best[:, :, 0]
+        if score == moe.SIGMOID and best.shape[2] == 2:
+            first = torch.where(best[:, :, 1] == LOW, first, first + best[:, :, 1])
+        order = torch.sort(first, dim=1, descending=True, stable=True).indices[:, :topk_groups]
+        kept = torch.zeros(t, groups, dtype=torch.bool).scatter(1, order, True)
+        key = torch.where(kept.repeat_interleave(e // groups, 1), key, torch.full_like(key, LOW))
+    # on the host -0.0 and 0.0 compare equal and a stable sort keeps their order
+    key, ids = torch.sort(key, dim=1, descending=True, stable=True)
+    return torch.where(key[:, :topk] == LOW, -1, ids[:, :topk]).to(torch.int32)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -41,6 +66,37 @@ def test_zeros_of_either_sign_tie(rd_lib, experts, topk, groups, topk_groups, dt
         for t in range(tokens):
             ref = moe.route_weights(l[t].double().numpy(), want[t], moe.SOFTMAX, True)
             assert np.all(np.abs(r.weights[t].double().cpu().numpy() - ref) <= 2.0 ** -23 * 64 * ref)
+
+
+@pytest.mark.parametrize("kind", ["grid", "free"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", [moe.SOFTMAX, moe.SIGMOID])
+@pytest.mark.parametrize("experts,topk,groups,topk_groups", [
+    (256, 8, 8, 4), (256, 8, 8, 8), (64, 6, 8, 3), (128, 4, 4, 2), (512, 2, 2, 1), (1024, 16, 4, 1), (1024, 32, 32, 7),
+    (32, 4, 32, 5), (24, 3, 3, 2), (8, 2, 4, 1), (96, 8, 8, 2), (160, 8, 32, 5), (1000, 32, 10, 3), (256, 8, 1, 1),
+    (31, 7, 1, 1)])
+def test_choice_equals_elementwise_f32(rd_lib, experts, topk, groups, topk_groups, score, dtype, kind):
+    """Ids and their order, bit for bit: groups of a power of two of whole lanes, of other sizes, and none; on a
+    coarse grid, where most keys and group scores tie, and on free values; with masked experts and tokens."""
+    rng = np.random.default_rng(experts + 7 * groups + score)
+    tokens = 300
+    l = rng.normal(size=(tokens, experts)) * 1.5
+    bias = rng.normal(size=experts) * 0.05
+    if kind == "grid":
+        l, bias = np.round(2 * l) / 2, np.round(bias * 20) / 8
+    l[rng.random(l.shape) < 0.03] = -np.inf
+    l[rng.random(l.shape) < 0.01] = np.nan
+    l[rng.random(l.shape) < 0.002] = np.inf
+    l[rng.random(tokens) < 0.03] = -np.inf
+    few = rng.random(tokens) < 0.1                      # tokens with hardly an expert
+    l[few] = np.where(rng.random((few.sum(), experts)) < 0.03, l[few], -np.inf)
+    l[:4] -= 60.0
+    l[4:8] -= 95.0                                      # sigmoids of zero and of subnormal numbers
+    l = torch.from_numpy(l.astype(np.float32)).to(torch.float32 if dtype == "f32" else torch.bfloat16).to(DEV)
+    for b in (None, torch.from_numpy(bias.astype(np.float32)).to(DEV)):
+        r = rd_lib.route(l, topk, score=score, bias=b, groups=groups, topk_groups=topk_groups)
+        want = _choose_f32(l, b, topk, score, groups, topk_groups)
+        assert torch.equal(r.ids.cpu(), want)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
