@@ -23,6 +23,7 @@
 
 #include "launch.h"
 #include "moe_args.h"
+#include "route_math.cuh"
 
 namespace rd {
 namespace {
@@ -38,17 +39,6 @@ __device__ __forceinline__ int32_t tokens_below(const int32_t* limit, int32_t to
   if (limit == nullptr) return tokens;
   const int32_t v = *limit;
   return v < 0 ? 0 : (v > tokens ? tokens : v);
-}
-
-// The correctly rounded 1 / d for d in [1, kFastRcp): the hardware approximation and one Newton step
-// with fused multiply-adds, r + r (1 - d r), which rounds correctly when r is within an ulp
-// (P. Markstein, IA-64 and Elementary Functions, 2000, for all mantissas but the one of all ones);
-// checked against the correctly rounded reciprocal for every float in the range.
-constexpr float kFastRcp = 1.0e37f;
-__device__ __forceinline__ float reciprocal_fast(float d) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
 }
 
 // the logistic in the elementwise f32 arithmetic that the keys are defined by

@@ -8,6 +8,11 @@ smallest subnormal, so their spacing adds less), of a share twice that and one d
 at most 32 slots 5 units: 2^-23 * 64 of scale * share * (|d| + sum |q d|) holds them all; bf16 output
 adds half an ulp, 2^-8 relative.
 """
+import ctypes
+import os
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 
@@ -17,6 +22,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "expert_ffn_ragged_gb300", "csrc")
 LOW = float("-inf")
 
 
@@ -164,3 +171,18 @@ def test_largest_token_count(rd_lib):
     assert not out[masked].any() and int((out == 0.5).sum()) == live
     del logits, ids, d, buf, out
     torch.cuda.empty_cache()
+
+
+def test_reciprocal_of_every_float(rd_lib, tmp_path):
+    """The keys' reciprocal (approximation and one Newton step) is the correctly rounded one for every float of
+    the range it is used in, 1.03e9 of them."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    lib = str(tmp_path / "libsweep.so")
+    subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-shared",
+                    "-Xcompiler", "-fPIC", "-I" + CSRC, os.path.join(HERE, "reciprocal_sweep.cu"), "-o", lib], check=True)
+    torch.cuda.synchronize()
+    count, wrong, lowest = ctypes.c_uint(), ctypes.c_ulonglong(), ctypes.c_uint()
+    code = ctypes.CDLL(lib).reciprocal_sweep(ctypes.byref(count), ctypes.byref(wrong), ctypes.byref(lowest))
+    assert code == 0
+    assert count.value > 1_000_000_000
+    assert wrong.value == 0, hex(lowest.value)
