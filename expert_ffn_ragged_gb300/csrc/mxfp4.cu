@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(kQuantThreads)
                          uint8_t* scales, int32_t k, int32_t n, int32_t scale_width) {
   pdl_trigger();
   pdl_wait();
-  const int col = blockIdx.x * kQuantThreads + threadIdx.x;
+  const uint32_t col = blockIdx.x * kQuantThreads + threadIdx.x;  // up to a block past n: not in 31 bits
   const int block = blockIdx.y;
   const int64_t e = blockIdx.z;
-  if (col >= n) return;
+  if (col >= static_cast<uint32_t>(n)) return;
   uint8_t* s = scales + (e * n + col) * scale_width + block;
   if (block >= k / kMxBlock) {
     *s = 0;
@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(kQuantThreads)
   *s = static_cast<uint8_t>(sb);
 }
 
+// in 64 bits: the largest extents and a tile together leave 32
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // at most 24 blocks an SM (16381 rows of 4096, there and back: 8 an SM 57.9 us, 12 55.6, 24 53.9,
 // 64 55.3: enough for an even end, few enough that the starts do not count)
 int quant_grid(int64_t blocks, int sms) {
@@ -204,22 +207,22 @@ int quant_grid(int64_t blocks, int sms) {
 }  // namespace
 
 cudaError_t launch_mxfp4_quantize(const QuantArgs& a, int sms, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
-  const int grid = quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms);
+  const int64_t units = a.rows * ceil_div(a.k, 256 * kQuantBatch);
+  const int grid = quant_grid(ceil_div(units, kQuantWarps), sms);
   return launch_pdl(a.pos != nullptr ? mxfp4_quantize_kernel<true> : mxfp4_quantize_kernel<false>,
                     dim3(grid), kQuantThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_mxfp4_dequantize(const QuantArgs& a, void* out, int sms, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(a.rows) * ((a.k + 256 * kQuantBatch - 1) / (256 * kQuantBatch));
-  return launch_pdl(mxfp4_dequantize_kernel, dim3(quant_grid((units + kQuantWarps - 1) / kQuantWarps, sms)),
+  const int64_t units = a.rows * ceil_div(a.k, 256 * kQuantBatch);
+  return launch_pdl(mxfp4_dequantize_kernel, dim3(quant_grid(ceil_div(units, kQuantWarps), sms)),
                     kQuantThreads, 0, 1, stream, a, static_cast<uint4*>(out));
 }
 
 cudaError_t launch_mxfp4_quantize_weights(const void* rhs, uint8_t* q, uint8_t* scales, int32_t g,
                                           int32_t k, int32_t n, int32_t scale_width,
                                           cudaStream_t stream) {
-  const dim3 grid((n + kQuantThreads - 1) / kQuantThreads, scale_width, g);
+  const dim3 grid(static_cast<unsigned>(ceil_div(n, kQuantThreads)), scale_width, g);
   return launch_pdl(mxfp4_weights_kernel, grid, kQuantThreads, 0, 1, stream,
                     static_cast<const __nv_bfloat16*>(rhs), q, scales, k, n, scale_width);
 }

@@ -1,4 +1,4 @@
-"""4-bit rows at the ends of the exponent range, bit for bit against the float64 oracle."""
+"""4-bit rows at the ends of the exponent range and of the extents, bit for bit."""
 import numpy as np
 import pytest
 
@@ -44,3 +44,52 @@ def test_blocks_of_the_largest_values(rd_lib):
     bits = np.concatenate([rng.integers(0x7F80 - span, 0x7F80, (4, 32)) for span in (1, 0x20, 0x80, 0x100, 0x400, 0x7F80)])
     bits |= rng.integers(0, 2, bits.shape) << 15
     _check(rd_lib, torch.from_numpy(bits.astype(np.uint16).view(np.int16)).view(torch.bfloat16))
+
+
+def _free(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
+        pytest.skip(f"needs {gigabytes} GB of free device memory")
+
+
+def test_longest_row(rd_lib):
+    """One row of 2^31 - 32 elements, the longest that a call takes, there and back."""
+    _free(24)
+    k, n = 2 ** 31 - 32, 4096
+    x = torch.zeros((1, k), dtype=torch.bfloat16, device=DEV)
+    part = torch.randn(1, n, device=DEV).to(torch.bfloat16)
+    at = (0, 2 ** 30 + 512, k - n)
+    for c in at:
+        x[:, c:c + n] = part
+    q, s = rd_lib.mxfp4_quantize(x)
+    back = rd_lib.mxfp4_dequantize(q, s)
+    want = rd_lib.mxfp4_quantize(part)
+    values = rd_lib.mxfp4_dequantize(*want)
+    for c in at:
+        assert torch.equal(q[:, c // 2:(c + n) // 2], want.q)
+        assert torch.equal(s[:, c // 32:(c + n) // 32], want.scales)
+        assert torch.equal(back[:, c:c + n], values)
+    assert not s[:, k // 32:].any()
+    assert int(back.count_nonzero()) == len(at) * int(values.count_nonzero())
+
+
+def test_most_columns_of_a_weight(rd_lib):
+    """[1, 32, 2^31 - 8] to 4 bits: the last block of columns is half outside, and is not written."""
+    _free(215)
+    n, pad = 2 ** 31 - 8, 256
+    rhs = torch.empty((1, 32, n), dtype=torch.bfloat16, device=DEV)
+    part = torch.randn(1, 32, 512, device=DEV).to(torch.bfloat16)
+    at = (0, 2 ** 30 + 8, n - 512)
+    for c in at:
+        rhs[:, :, c:c + 512] = part
+    bufs = [torch.empty((n + pad) * 16, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for b in bufs:
+        b[-16 * pad:] = 0xA5
+    out = rd_lib.Mxfp4(*[b[:16 * n].view(1, n, 16) for b in bufs])
+    rd_lib.mxfp4_quantize_weights(rhs, out=out)
+    want = rd_lib.mxfp4_quantize_weights(part)
+    for c in at:
+        assert torch.equal(out.q[:, c:c + 512], want.q) and torch.equal(out.scales[:, c:c + 512], want.scales)
+    assert all(bool((b[-16 * pad:] == 0xA5).all()) for b in bufs)
+    del rhs, bufs, out
+    torch.cuda.empty_cache()
