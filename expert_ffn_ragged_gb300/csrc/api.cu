@@ -214,6 +214,7 @@ extern "C" rd_status rd_ragged_dot(const void* lhs, const void* rhs, void* out, 
   if (st != RD_OK) return st;
   if (glu && n % 16 != 0) return n % 2 ? RD_ERR_INVALID_ARG : RD_ERR_UNSUPPORTED;
   const int64_t n_out = glu ? n / 2 : n;
+  if (n_out > kMaxWidth) return RD_ERR_UNSUPPORTED;
   if ((m > 0 && k > 0 && lhs == nullptr) || (k > 0 && n > 0 && rhs == nullptr) ||
       (m > 0 && n_out > 0 && out == nullptr))
     return RD_ERR_INVALID_ARG;
@@ -278,6 +279,7 @@ rd_status trans_rhs_impl(const void* lhs, const void* rhs, const void* fused, vo
                          int32_t* status, rd_stream_t stream) {
   rd_status st = check_groups(m, k, n, group_sizes, g_total, group_offset, g_local, limit, status);
   if (st != RD_OK) return st;
+  if (k > kMaxWidth) return RD_ERR_UNSUPPORTED;
   const bool glu_bwd = fused != nullptr;
   const int64_t out_w = glu_bwd ? 2 * k : k;
   if ((m > 0 && n > 0 && lhs == nullptr) || (k > 0 && n > 0 && rhs == nullptr) ||
@@ -370,6 +372,7 @@ rd_status trans_ragged_impl(const void* x, const void* y, void* out, int64_t m, 
   const uint64_t out_elem = epi == kEpiNone ? 2 : 4;
   rd_status st = check_groups(m, k, n, group_sizes, g_total, group_offset, g_local, limit, status);
   if (st != RD_OK) return st;
+  if (k > kMaxWidth || n > kMaxWidth) return RD_ERR_UNSUPPORTED;
   if (workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 127u))
     return RD_ERR_UNSUPPORTED;
   if ((m > 0 && k > 0 && x == nullptr) || (m > 0 && n > 0 && y == nullptr) ||

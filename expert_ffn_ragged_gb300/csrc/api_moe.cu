@@ -366,6 +366,8 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   if (k % 32 != 0) return RD_ERR_UNSUPPORTED;
   if (glu && n % (quant ? 64 : 16) != 0) return RD_ERR_UNSUPPORTED;
   const int64_t n_out = glu ? n / 2 : n;
+  // the kernel counts k in 32 bits, up to a shared-memory slot of scales past its end
+  if (n_out > kMaxWidth || k > kMaxDim + 1 - k4RawK) return RD_ERR_UNSUPPORTED;
   if ((m > 0 && k > 0 && (a == nullptr || a_scales == nullptr)) ||
       (k > 0 && n > 0 && (b == nullptr || b_scales == nullptr)) ||
       (m > 0 && n > 0 && (out == nullptr || quant != (out_scales != nullptr))))

@@ -168,7 +168,7 @@ __device__ __forceinline__ Tile decode_tile4(const Gemm4Shared<VAR>& sh, const G
   tl.rs = sh.bound[a.group_offset + j];
   tl.re = sh.bound[a.group_offset + j + 1];
   int u = t - sh.tile_start[j];
-  const int mt = (tl.re - tl.rs + TM - 1) / TM;
+  const int mt = ceil_div(tl.re - tl.rs, TM);
   if (mt == 1) {
     tl.m_idx = 0;
     tl.n_idx = u;

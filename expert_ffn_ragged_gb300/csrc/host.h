@@ -10,6 +10,8 @@
 namespace rd {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFF;
+// widest output of a grouped product: the last tile (at most 256 columns or, of dw, rows) ends within 32 bits
+constexpr int64_t kMaxWidth = kMaxDim - 255;
 
 // bound of every wait inside the kernels (rd_set_tuning, or the default)
 uint64_t wait_timeout_ns();

@@ -72,6 +72,11 @@ RD_HD bool group_is_empty(const int32_t* bound, int group_offset, int j) {
   return bound[group_offset + j + 1] == bound[group_offset + j];
 }
 
+// ceil(n / d) for n >= 0; unsigned, since n + d - 1 may pass 2^31
+RD_HD int32_t ceil_div(int32_t n, int32_t d) {
+  return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(d) - 1) / static_cast<uint32_t>(d));
+}
+
 RD_HD int32_t clamp_boundary(long long run, int32_t L) {
   return static_cast<int32_t>(run < L ? run : L);
 }
@@ -80,8 +85,7 @@ RD_HD int32_t clamp_boundary(long long run, int32_t L) {
 RD_HD long long tiles_of_group(int op, int32_t lo, int32_t hi, int tm, int32_t n_tiles,
                                int32_t dw_m_tiles) {
   if (op == kOpDw) return static_cast<long long>(dw_m_tiles) * n_tiles;
-  const int32_t cnt = hi - lo;
-  return static_cast<long long>((cnt + tm - 1) / tm) * n_tiles;
+  return static_cast<long long>(ceil_div(hi - lo, tm)) * n_tiles;
 }
 
 template <int OP, int TM>
@@ -97,7 +101,7 @@ RD_HD Tile decode_tile_view(const SchedView& v, int t) {
     tl.rs = v.bound[v.group_offset + tl.j];
     tl.re = v.bound[v.group_offset + tl.j + 1];
     tl.row_load = 0;
-    tl.nkb = (tl.re - tl.rs + kBK - 1) / kBK;
+    tl.nkb = ceil_div(tl.re - tl.rs, kBK);
   } else {
     int lo = 0, hi = v.g_local;  // tile_start[lo] <= t < tile_start[hi]
     while (hi - lo > 1) {
@@ -112,7 +116,7 @@ RD_HD Tile decode_tile_view(const SchedView& v, int t) {
     // band sweeps every n-tile before the next band starts, so the band's lhs
     // rows stay in L2 while each rhs column panel is read once per band.
     const int kBand = v.band_tiles;
-    const int mt = (tl.re - tl.rs + TM - 1) / TM;
+    const int mt = ceil_div(tl.re - tl.rs, TM);
     const int band = u / (kBand * v.n_tiles);
     const int rem = u - band * kBand * v.n_tiles;
     const int left = mt - band * kBand;
@@ -121,7 +125,7 @@ RD_HD Tile decode_tile_view(const SchedView& v, int t) {
     tl.n_idx = rem / bw;
     const int first = tl.rs + tl.m_idx * TM;
     tl.row_load = (tl.m_idx == mt - 1) ? tl.re - TM : first;
-    tl.nkb = (v.kc + kBK - 1) / kBK;
+    tl.nkb = ceil_div(v.kc, kBK);
   }
   return tl;
 }

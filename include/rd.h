@@ -15,6 +15,11 @@
  * after the call returns (the work it enqueued still reads and writes the
  * buffers until it completes on the stream).
  *
+ * Extents: at most 2^31 - 1; the width of a grouped call's output (n of
+ * rd_ragged_dot, n / 2 with the GLU; k of rd_ragged_dot_trans_rhs, f of its
+ * GLU form; k and n of the dw calls) at most 2^31 - 256, so that its last
+ * tile ends within 32 bits.  RD_ERR_UNSUPPORTED beyond.
+ *
  * Group semantics (all grouped calls):
  *   L      = min(max(*limit, 0), m), or m when limit is NULL.
  *   s[i]   = min(sum_{j<i} max(group_sizes[j], 0), L), i = 0..g_total.

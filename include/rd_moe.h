@@ -196,7 +196,8 @@ rd_status rd_mxfp4_dequantize(const void* q, const void* scales, void* out, int6
  *                         bytes past n / 64 are not written); zero rows are zero bytes in both
  *   out_scales is NULL for the other two.
  * Requires k % 32 == 0, n % 8 == 0 (n / 2 % 8 == 0 with the GLU, n / 2 % 32 == 0 with the 4-bit
- * output), 16-byte aligned matrices, no overlap of the outputs with anything.
+ * output), 16-byte aligned matrices, no overlap of the outputs with anything; k at most 2^31 - 1024 and
+ * the output's width (n, n / 2 with the GLU) at most 2^31 - 256.
  */
 rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, const void* b,
                               const void* b_scales, void* out, void* out_scales, int64_t m,
