@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = c_begin; c < c_end; ++c) {
           const int col = col0 + c * 32;
           uint4 G[4], U[4];
-          const __nv_bfloat16* src = fused + static_cast<size_t>(row) * (2 * args.n_out) + col;
+          const __nv_bfloat16* src = fused + static_cast<size_t>(row) * (2 * static_cast<size_t>(args.n_out)) + col;
 #pragma unroll
           for (int w4 = 0; w4 < 4; ++w4) {
             if (row_ok && col + 8 * w4 + 8 <= args.n_out) {

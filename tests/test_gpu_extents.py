@@ -1,4 +1,4 @@
-"""Grouped products of the most rows that a call takes: 2^31 - 1, all in one group."""
+"""Grouped products at the largest extents: 2^31 - 1 rows in one group, rows of more than 2^31 elements."""
 import numpy as np
 import pytest
 
@@ -62,4 +62,33 @@ def test_product_rows(rd_lib, variant):
     assert int(status) == 0
     _check(out, want)
     del lhs, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("variant", ["pair", "single"])
+def test_glu_gradient_of_a_wide_layer(rd_lib, variant):
+    """f above 2^30: a row of the fused buffer is more than 2^31 elements long."""
+    _free(60)
+    rng = np.random.default_rng(3)
+    m, f, n, part = 3, 2 ** 30 + 8, 8, 264
+
+    def some(*shape):
+        return torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(torch.bfloat16).to(DEV)
+
+    d_out, w, gate, up = some(m, n), some(1, part, n), some(m, part), some(m, part)
+    want = rd_lib.ragged_dot_trans_rhs_glu_bwd(d_out, w, torch.cat((gate, up), 1), _i32([m]))
+    rhs = torch.zeros((1, f, n), dtype=torch.bfloat16, device=DEV)
+    fused = torch.zeros((m, 2 * f), dtype=torch.bfloat16, device=DEV)
+    for at in (0, 2 ** 29 + 8, f - part):
+        rhs[:, at:at + part] = w
+        fused[:, at:at + part] = gate
+        fused[:, f + at:f + at + part] = up
+    status = _i32([0])
+    with rd_lib.tuning(variant=rd_lib.VARIANT_PAIR if variant == "pair" else rd_lib.VARIANT_SINGLE):
+        out = rd_lib.ragged_dot_trans_rhs_glu_bwd(d_out, rhs, fused, _i32([m]), status=status)
+    assert int(status) == 0
+    for at in (0, 2 ** 29 + 8, f - part):
+        assert torch.equal(out[:, at:at + part], want[:, :part])
+        assert torch.equal(out[:, f + at:f + at + part], want[:, part:])
+    del rhs, fused, out
     torch.cuda.empty_cache()
