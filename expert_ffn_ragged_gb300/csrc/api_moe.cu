@@ -256,11 +256,13 @@ extern "C" int64_t rd_mxfp4_scale_width(int64_t k) { return k <= 0 ? 0 : (k / 32
 
 namespace {
 
-rd_status check_mx(const void* x, const void* q, const void* scales, int64_t rows, int64_t k,
-                   const int32_t* limit) {
-  if (rows < 0 || k < 0) return RD_ERR_INVALID_ARG;
-  if (rows > kMaxDim || k > kMaxDim || k % 32 != 0) return RD_ERR_UNSUPPORTED;
-  if (rows > 0 && k > 0 && (x == nullptr || q == nullptr || scales == nullptr)) return RD_ERR_INVALID_ARG;
+// x [rows, k], q and scales of q_rows rows
+rd_status check_mx(const void* x, const void* q, const void* scales, int64_t rows, int64_t q_rows,
+                   int64_t k, const int32_t* limit) {
+  if (rows < 0 || q_rows < 0 || k < 0) return RD_ERR_INVALID_ARG;
+  if (rows > kMaxDim || q_rows > kMaxDim || k > kMaxDim || k % 32 != 0) return RD_ERR_UNSUPPORTED;
+  if (rows > 0 && k > 0 && (x == nullptr || (q_rows > 0 && (q == nullptr || scales == nullptr))))
+    return RD_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned4(limit)) return RD_ERR_UNSUPPORTED;
   return RD_OK;
 }
@@ -270,10 +272,8 @@ rd_status check_mx(const void* x, const void* q, const void* scales, int64_t row
 extern "C" rd_status rd_mxfp4_quantize(const void* x, const int32_t* pos, void* q, void* scales,
                                        int64_t rows, int64_t topk, int64_t k, int64_t out_rows,
                                        const int32_t* limit, rd_stream_t stream) {
-  rd_status st = check_mx(x, q, scales, rows, k, limit);
+  rd_status st = check_mx(x, q, scales, rows, out_rows, k, limit);
   if (st != RD_OK) return st;
-  if (out_rows < 0) return RD_ERR_INVALID_ARG;
-  if (out_rows > kMaxDim) return RD_ERR_UNSUPPORTED;
   if (pos == nullptr) {
     if (out_rows < rows) return RD_ERR_INVALID_ARG;
     topk = 1;
@@ -307,7 +307,7 @@ extern "C" rd_status rd_mxfp4_quantize(const void* x, const int32_t* pos, void* 
 
 extern "C" rd_status rd_mxfp4_dequantize(const void* q, const void* scales, void* out, int64_t rows,
                                          int64_t k, const int32_t* limit, rd_stream_t stream) {
-  rd_status st = check_mx(out, q, scales, rows, k, limit);
+  rd_status st = check_mx(out, q, scales, rows, rows, k, limit);
   if (st != RD_OK) return st;
   const int64_t width = rd_mxfp4_scale_width(k);
   if (any_overlap<1, 3>({{out, static_cast<uint64_t>(rows) * k * 2}},
