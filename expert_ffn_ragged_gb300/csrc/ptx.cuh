@@ -144,12 +144,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
                : "memory");
 }
 
-// The same without the release at cluster scope, which holds the warp until its earlier accesses
-// are visible to the cluster (~1600 cycles next to busy tensor cores).  Enough to hand over tensor
-// memory: tcgen05.wait and the fence before thread synchronisation have ordered those accesses,
-// and nothing that the peer reads through generic memory is published with it.
+// The same arrival, at cluster scope too, without the release, which holds the warp until its earlier accesses
+// are visible to the cluster (~1600 cycles next to busy tensor cores).  For handing over tensor memory: the
+// tcgen05 accesses before it are complete (tcgen05.wait) and ordered before the arrival (the fence before
+// thread synchronisation), those of the waiting thread after it by its own fence, and nothing that the peer
+// reads through generic memory is published with it.
 __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA

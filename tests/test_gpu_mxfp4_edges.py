@@ -1,4 +1,4 @@
-"""4-bit rows at the ends of the exponent range and of the extents, bit for bit."""
+"""4-bit rows at the ends of the exponent range and of the extents, bit for bit; a product of many tiles."""
 import numpy as np
 import pytest
 
@@ -93,3 +93,33 @@ def test_most_columns_of_a_weight(rd_lib):
     assert all(bool((b[-16 * pad:] == 0xA5).all()) for b in bufs)
     del rhs, bufs, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("k", [4096, 1184])
+def test_pair_product_of_many_tiles(rd_lib, k):
+    """Hundreds of tiles of many stages on CTA pairs, every element against the float64 product of the same 4-bit
+    values within the products' tolerance (two bf16 ulps and 1e-3 sqrt(k) max|a| max|b|), the same bits every time."""
+    gen = torch.Generator(device=DEV).manual_seed(k)
+    sizes, n = [2600, 0, 1, 3000, 2047, 544], 1536
+    m = sum(sizes)
+    a = rd_lib.mxfp4_quantize(torch.randn(m, k, generator=gen, device=DEV).to(torch.bfloat16))
+    b = rd_lib.mxfp4_quantize_weights(
+        (torch.randn(len(sizes), k, n, generator=gen, device=DEV) * k ** -0.5).to(torch.bfloat16))
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    with rd_lib.tuning(variant=rd_lib.VARIANT_PAIR):
+        first = rd_lib.ragged_dot_mxfp4(*a, *b, gs, status=status)
+        for i in range(30):
+            if i % 3 == 0:                       # another kernel's tiles in tensor memory in between
+                rd_lib.ragged_dot_mxfp4(*a, *b, gs, epilogue=rd_lib.EPI_SILU_GLU_MXFP4)
+            again = rd_lib.ragged_dot_mxfp4(*a, *b, gs, status=status)
+            assert torch.equal(again.view(torch.int16), first.view(torch.int16)), i
+    assert int(status) == 0
+    a64, row = rd_lib.mxfp4_dequantize(*a).double(), 0
+    for j, cnt in enumerate(sizes):
+        b64 = rd_lib.mxfp4_dequantize(b.q[j], b.scales[j]).double()
+        ref = a64[row:row + cnt] @ b64.t()
+        ulp = torch.exp2(torch.floor(torch.log2(ref.abs().clamp(min=2.0 ** -126))) - 7)
+        tol = 2 * ulp + 1e-3 * k ** 0.5 * a64.abs().max() * b64.abs().max()
+        assert bool(((first[row:row + cnt].double() - ref).abs() <= tol).all()), j
+        row += cnt
