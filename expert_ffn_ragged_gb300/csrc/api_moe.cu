@@ -390,8 +390,21 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   if ((st = current_device(&sms)) != RD_OK) return st;
   if (m == 0 || n == 0) return RD_OK;
 
-  // Tiles of 32 rows where the groups average at most 16 (most of them then hold a tile's rows or fewer):
-  // see gemm_mxfp4.cuh.
+  // Tiles of 32 rows where the groups average at most 16 (most of them then hold a tile's rows or fewer; see
+  // gemm_mxfp4.cuh), of 256 on CTA pairs from 512 on (use_pair), of 128 between.  By rows a group, us:
+  //                                        1     16     24     32     48    192    256    512   1024
+  //   4096 -> 1536, 128 experts    32    47.0   69.3   69.7   72.0   88.9
+  //                               128    48.4   70.2   70.8   71.3   72.3  103.7  120.1  202.5  379.7
+  //                               256    54.0   81.6   82.2   82.8   83.5   90.7  119.7  182.4  327.6
+  //   768 -> 4096, 128 experts     32    29.8   41.5   42.9   47.8   63.3
+  //                               128    37.7   42.3   43.1   43.8   46.0   81.9   95.2  162.4  299.8
+  //                               256    53.1   65.1   65.5   59.8   61.7   80.7  111.0  168.4  298.4
+  //   4096 -> 14336, 8 experts     32    33.7   42.6   42.9   47.6   49.9
+  //                               128    38.6   43.7   44.2   44.2   44.6   63.5   72.5  116.2  208.4
+  //                               256    61.1   50.4   51.1   51.1   51.8   55.4   70.9  106.6  181.1
+  // 32 against 128: the sides meet between 24 and 32.  128 against 256: at k = 4096 pairs are ahead from 192
+  // rows on (by up to 14 %; even at 256), at k = 768 they are behind at 256 and 512 and even at 1024.  The bf16
+  // products' 512 lies between the two.
   const bool pair = use_pair(sms, m, g_total);
   const bool few = !pair && m <= 16 * static_cast<int64_t>(g_total);
   const int tm = pair ? 2 * kBM : (few ? 32 : kBM);

