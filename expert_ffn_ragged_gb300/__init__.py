@@ -21,6 +21,8 @@ Functions (same names as the C ABI, without the ``rd_`` prefix):
 * ``status_bits(status)``, ``check_status(status)``       -> read a status word (names, or raise)
 * routing, sorting, dispatch / combine and the 4-bit products (``include/rd_moe.h``): the functions
   of ``expert_ffn_ragged_gb300.moe``, importable from here
+* layer norm, products with bias / activation / residual, dropout (``include/rd_block.h``): the functions
+  of ``expert_ffn_ragged_gb300.block``, importable from here
 
 Every tensor of a call must sit on one CUDA device; the call runs on that
 device's current stream (or ``stream``).  A ``status`` word (a one-element
@@ -44,6 +46,9 @@ __all__ = [
     "mxfp4_scale_width", "mxfp4_quantize", "mxfp4_quantize_weights", "mxfp4_dequantize",
     "ragged_dot_mxfp4", "Routing", "Mxfp4", "SCORE_SOFTMAX", "SCORE_SIGMOID", "MAX_TOPK",
     "MAX_EXPERT_GROUPS", "EPI_SILU_GLU_MXFP4",
+    "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "linear", "linear_act_bwd",
+    "linear_act_bwd_workspace_bytes", "dropout_rows", "LayerNorm", "ACT_NONE", "ACT_RELU", "ACT_GELU",
+    "ACT_GELU_TANH", "ACT_SILU",
 ]
 
 EPI_NONE = 0
@@ -113,6 +118,7 @@ def load():
     lib.rd_status_string.argtypes = [ctypes.c_int]
     lib.rd_status_string.restype = ctypes.c_char_p
     moe.declare(lib)
+    block.declare(lib)
     _lib = lib
     return lib
 
@@ -590,3 +596,7 @@ from .moe import (  # noqa: E402
     EPI_SILU_GLU_MXFP4, MAX_EXPERT_GROUPS, MAX_TOPK, SCORE_SIGMOID, SCORE_SOFTMAX, Mxfp4, Routing,
     combine_rows, combine_rows_bwd, dispatch_rows, mxfp4_dequantize, mxfp4_quantize,
     mxfp4_quantize_weights, mxfp4_scale_width, ragged_dot_mxfp4, route, route_bwd, sort_rows)
+from . import block  # noqa: E402
+from .block import (  # noqa: E402
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, LayerNorm, dropout_rows, layer_norm_bwd,
+    layer_norm_bwd_workspace_bytes, layer_norm_fwd, linear, linear_act_bwd, linear_act_bwd_workspace_bytes)

@@ -21,7 +21,8 @@ OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "librd.so")
 
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_dx.cu", "gemm_dw.cu", "glu.cu", "unsort.cu",
-           "api_moe.cu", "route.cu", "sort_rows.cu", "permute.cu", "mxfp4.cu", "gemm_mxfp4.cu"]
+           "api_moe.cu", "route.cu", "sort_rows.cu", "permute.cu", "mxfp4.cu", "gemm_mxfp4.cu",
+           "api_block.cu", "layer_norm.cu", "dropout.cu", "act_bwd.cu", "gemm_linear.cu", "gemm_split.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",
                  "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
@@ -35,7 +36,7 @@ def _nvcc() -> str:
 
 
 def _headers():
-    out = [os.path.join(ROOT, "include", h) for h in ("rd.h", "rd_moe.h")]
+    out = [os.path.join(ROOT, "include", h) for h in ("rd.h", "rd_moe.h", "rd_block.h")]
     for f in os.listdir(CSRC):
         if f.endswith((".h", ".cuh")):
             out.append(os.path.join(CSRC, f))

@@ -1,0 +1,362 @@
+// api_block.cu -- the C entry points of include/rd_block.h: argument checks (all of those that the
+// host can make come before any CUDA call), tensor maps, launch shapes.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/rd_block.h"
+#include "block_args.h"
+#include "gemm_args.h"
+#include "gemm_split.h"
+#include "host.h"
+
+using namespace rd;
+
+namespace {
+
+rd_status done(cudaError_t e) { return e == cudaSuccess ? RD_OK : RD_ERR_CUDA; }
+
+cudaStream_t cu(rd_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+struct Span {
+  const void* p;
+  uint64_t bytes;
+};
+
+// whether an output overlaps an input or another output
+template <int O, int I>
+bool any_overlap(const Span (&outs)[O], const Span (&ins)[I]) {
+  for (int o = 0; o < O; ++o) {
+    for (int i = 0; i < I; ++i)
+      if (overlap(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes)) return true;
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].bytes, outs[i].p, outs[i].bytes)) return true;
+  }
+  return false;
+}
+
+bool known(int32_t dtype) { return dtype == RD_F32 || dtype == RD_BF16; }
+uint64_t size_of(int32_t dtype) { return dtype == RD_F32 ? 4 : 2; }
+// matrices: 16 bytes, f32 ones 32 (eight elements are one access)
+bool matrix_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == RD_F32 ? 31u : 15u)) == 0;
+}
+
+rd_status check_matrix(int64_t rows, int64_t hidden, int32_t dtype, int32_t out_dtype) {
+  if (rows < 0 || hidden < 0 || !known(dtype) || !known(out_dtype)) return RD_ERR_INVALID_ARG;
+  if (rows > kMaxDim || hidden > kMaxDim || hidden % 8 != 0) return RD_ERR_UNSUPPORTED;
+  return RD_OK;
+}
+
+}  // namespace
+
+extern "C" rd_status rd_layer_norm_fwd(const void* x, int32_t dtype, const float* weight,
+                                       const float* bias, float eps, void* out, int32_t out_dtype,
+                                       float* mean, float* rstd, int64_t rows, int64_t hidden,
+                                       const int32_t* limit, rd_stream_t stream) {
+  rd_status st = check_matrix(rows, hidden, dtype, out_dtype);
+  if (st == RD_ERR_INVALID_ARG) return st;
+  if (!(eps >= 0.0f) || isinf(eps) || (mean == nullptr) != (rstd == nullptr)) return RD_ERR_INVALID_ARG;
+  if (rows > 0 && hidden > 0 && (x == nullptr || out == nullptr)) return RD_ERR_INVALID_ARG;
+  if (st != RD_OK) return st;
+  if (!matrix_aligned(x, dtype) || !matrix_aligned(out, out_dtype) || !aligned16(weight) || !aligned16(bias) ||
+      !aligned4(mean) || !aligned4(rstd) || !aligned4(limit))
+    return RD_ERR_UNSUPPORTED;
+  const uint64_t n = static_cast<uint64_t>(rows) * hidden, rb = static_cast<uint64_t>(rows) * 4,
+                 hb = static_cast<uint64_t>(hidden) * 4;
+  if (any_overlap<3, 4>({{out, n * size_of(out_dtype)}, {mean, rb}, {rstd, rb}},
+                        {{x, n * size_of(dtype)}, {weight, hb}, {bias, hb}, {limit, 4}}))
+    return RD_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  if (rows == 0 || hidden == 0) return RD_OK;
+  NormArgs a = {};
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.limit = limit;
+  a.rows = static_cast<int32_t>(rows);
+  a.hidden = static_cast<int32_t>(hidden);
+  a.eps = eps;
+  return done(launch_layer_norm_fwd(a, dtype, out_dtype, sms, cu(stream)));
+}
+
+namespace {
+uint64_t norm_bwd_bytes(int64_t rows, int64_t hidden, int sms) {
+  return static_cast<uint64_t>(layer_norm_bwd_parts(rows, hidden, sms)) * 2 * static_cast<uint64_t>(hidden) * 4;
+}
+}  // namespace
+
+extern "C" rd_status rd_layer_norm_bwd_workspace_size(int64_t rows, int64_t hidden, size_t* bytes) {
+  if (bytes == nullptr) return RD_ERR_INVALID_ARG;
+  rd_status st = check_matrix(rows, hidden, RD_F32, RD_F32);
+  if (st != RD_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  *bytes = norm_bwd_bytes(rows, hidden, sms);
+  return RD_OK;
+}
+
+extern "C" rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, const void* x,
+                                       int32_t dtype, const float* weight, const float* mean,
+                                       const float* rstd, void* d_x, float* d_weight, float* d_bias,
+                                       int64_t rows, int64_t hidden, const int32_t* limit,
+                                       void* workspace, size_t workspace_bytes, rd_stream_t stream) {
+  rd_status st = check_matrix(rows, hidden, dtype, out_dtype);
+  if (st == RD_ERR_INVALID_ARG) return st;
+  const bool sums = d_weight != nullptr || d_bias != nullptr;
+  if (rows > 0 && hidden > 0 &&
+      (x == nullptr || d_out == nullptr || d_x == nullptr || mean == nullptr || rstd == nullptr))
+    return RD_ERR_INVALID_ARG;
+  if (sums && hidden > 0 && workspace == nullptr) return RD_ERR_INVALID_ARG;
+  if (st != RD_OK) return st;
+  if (!matrix_aligned(x, dtype) || !matrix_aligned(d_x, dtype) || !matrix_aligned(d_out, out_dtype) ||
+      !aligned16(weight) || !aligned16(d_weight) || !aligned16(d_bias) || !matrix_aligned(workspace, RD_F32) ||
+      !aligned4(mean) ||
+      !aligned4(rstd) || !aligned4(limit))
+    return RD_ERR_UNSUPPORTED;
+  const uint64_t n = static_cast<uint64_t>(rows) * hidden, rb = static_cast<uint64_t>(rows) * 4,
+                 hb = static_cast<uint64_t>(hidden) * 4;
+  if (any_overlap<4, 6>({{d_x, n * size_of(dtype)}, {d_weight, hb}, {d_bias, hb}, {sums ? workspace : nullptr, workspace_bytes}},
+                        {{x, n * size_of(dtype)}, {d_out, n * size_of(out_dtype)}, {weight, hb}, {mean, rb}, {rstd, rb}, {limit, 4}}))
+    return RD_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  if (sums && workspace_bytes < norm_bwd_bytes(rows, hidden, sms)) return RD_ERR_INVALID_ARG;
+  if (hidden == 0) return RD_OK;
+  if (rows == 0 && !sums) return RD_OK;
+  NormArgs a = {};
+  a.x = x;
+  a.d_out = d_out;
+  a.weight = weight;
+  a.out = d_x;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.d_weight = d_weight;
+  a.d_bias = d_bias;
+  a.parts = sums ? static_cast<float*>(workspace) : nullptr;
+  a.limit = limit;
+  a.rows = static_cast<int32_t>(rows);
+  a.hidden = static_cast<int32_t>(hidden);
+  return done(launch_layer_norm_bwd(a, dtype, out_dtype, sms, cu(stream)));
+}
+
+extern "C" rd_status rd_dropout_rows(const void* x, int32_t dtype, const void* residual,
+                                     const int64_t* rng, float p, void* out, int32_t out_dtype,
+                                     int64_t rows, int64_t hidden, const int32_t* limit,
+                                     rd_stream_t stream) {
+  rd_status st = check_matrix(rows, hidden, dtype, out_dtype);
+  if (st == RD_ERR_INVALID_ARG) return st;
+  if (!(p >= 0.0f && p <= 1.0f) || rng == nullptr) return RD_ERR_INVALID_ARG;
+  if (rows > 0 && hidden > 0 && (x == nullptr || out == nullptr)) return RD_ERR_INVALID_ARG;
+  if (st != RD_OK) return st;
+  if (!matrix_aligned(x, dtype) || !matrix_aligned(out, out_dtype) || !matrix_aligned(residual, out_dtype) ||
+      (reinterpret_cast<uintptr_t>(rng) & 7u) || !aligned4(limit))
+    return RD_ERR_UNSUPPORTED;
+  const uint64_t n = static_cast<uint64_t>(rows) * hidden;
+  if (any_overlap<1, 4>({{out, n * size_of(out_dtype)}},
+                        {{x, n * size_of(dtype)}, {residual, n * size_of(out_dtype)}, {rng, 16}, {limit, 4}}))
+    return RD_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  if (rows == 0 || hidden == 0) return RD_OK;
+  DropoutArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.out = out;
+  a.rng = rng;
+  a.limit = limit;
+  a.rows = static_cast<int32_t>(rows);
+  a.vecs = static_cast<int32_t>(hidden / 8);
+  a.least = static_cast<int32_t>(floor(static_cast<double>(p) * 65536.0 + 0.5));
+  a.scale = a.least < 65536 ? static_cast<float>(65536.0 / (65536 - a.least)) : 0.0f;
+  return done(launch_dropout_rows(a, dtype, out_dtype, sms, cu(stream)));
+}
+
+// ------------------------------------------------------------------ products with an epilogue
+namespace {
+
+// the checks that rd_linear and its gradient share; without group sizes there is one group of all rows
+rd_status check_linear(int64_t m, int64_t k, int64_t n, const int32_t* group_sizes, int32_t g_total,
+                       int32_t group_offset, int32_t g_local, const int32_t* limit,
+                       const int32_t* status, int32_t act, int32_t out_dtype) {
+  if (act < RD_ACT_NONE || act > RD_ACT_SILU || !known(out_dtype)) return RD_ERR_INVALID_ARG;
+  static const int32_t none = 0;
+  if (group_sizes == nullptr && (g_total != 1 || group_offset != 0 || g_local != 1)) return RD_ERR_INVALID_ARG;
+  rd_status st = check_groups(m, k, n, group_sizes != nullptr ? group_sizes : &none, g_total, group_offset, g_local,
+                              limit, status);
+  if (st != RD_OK) return st;
+  return n > kMaxWidth ? RD_ERR_UNSUPPORTED : RD_OK;
+}
+
+// One weight whose output has so few tiles of the persistent kernel that they leave SMs idle: the kernel that
+// splits k over clusters, on tiles of 64 columns while the rows are few, of 128 otherwise.
+bool use_split(int sms, int64_t m, int64_t n) {
+  const int64_t tiles = (m + kBM - 1) / kBM * ((n + kBN - 1) / kBN);
+  return tiles <= sms;
+}
+
+int split_cols(int64_t m) { return m <= 64 ? 64 : 128; }
+
+// as many CTAs a tile as still all run at once (two an SM), with at least four K blocks each
+int split_cluster(int sms, int64_t tiles, int64_t k) {
+  const int64_t blocks = (k + kBK - 1) / kBK;
+  int c = 1;
+  while (c < 8 && tiles * c * 2 <= 2 * static_cast<int64_t>(sms) && blocks >= 8 * c) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, const void* residual,
+                               int32_t act, void* out, int32_t out_dtype, void* pre, int64_t m,
+                               int64_t k, int64_t n, const int32_t* group_sizes, int32_t g_total,
+                               int32_t group_offset, int32_t g_local, const int32_t* limit,
+                               int32_t* status, rd_stream_t stream) {
+  rd_status st = check_linear(m, k, n, group_sizes, g_total, group_offset, g_local, limit, status, act, out_dtype);
+  if (st != RD_OK) return st;
+  if ((m > 0 && k > 0 && x == nullptr) || (k > 0 && n > 0 && w == nullptr) || (m > 0 && n > 0 && out == nullptr))
+    return RD_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(pre) || !aligned16(bias) || !matrix_aligned(out, out_dtype) ||
+      !matrix_aligned(residual, out_dtype))
+    return RD_ERR_UNSUPPORTED;
+  const uint64_t um = static_cast<uint64_t>(m), ug = static_cast<uint64_t>(g_local), un = static_cast<uint64_t>(n);
+  const uint64_t ob = um * un * size_of(out_dtype);
+  if (any_overlap<2, 7>({{out, ob}, {pre, um * un * 2}},
+                        {{x, um * k * 2},
+                         {w, ug * k * un * 2},
+                         {bias, ug * un * 4},
+                         {residual, ob},
+                         {group_sizes, static_cast<uint64_t>(g_total) * 4},
+                         {limit, 4},
+                         {status, 4}}))
+    return RD_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  if (m == 0 || n == 0) return RD_OK;
+
+  if (group_sizes == nullptr && use_split(sms, m, n)) {
+    const int cols = split_cols(m);
+    const int64_t tiles = (m + kSplitRows - 1) / kSplitRows * ((n + cols - 1) / cols);
+    SplitArgs s = {};
+    s.bias = bias;
+    s.residual = residual;
+    s.out = out;
+    s.pre = pre;
+    s.limit = limit;
+    s.status = status;
+    s.m = static_cast<int32_t>(m);
+    s.k = static_cast<int32_t>(k);
+    s.n = static_cast<int32_t>(n);
+    s.act = act;
+    s.box_rows = static_cast<int32_t>(m < kSplitRows ? (m + 7) / 8 * 8 : kSplitRows);
+    const int stage = s.box_rows * 128 + cols * kBK * 2;
+    s.stages = kSplitRingBytes / stage < kSplitMaxStages ? kSplitRingBytes / stage : kSplitMaxStages;
+    s.cluster = split_cluster(sms, tiles, k);
+    s.timeout_ns = wait_timeout_ns();
+    CUtensorMap tx = {}, tw = {};
+    if (k > 0) {
+      const uint64_t dx[2] = {static_cast<uint64_t>(k), um}, sx[1] = {static_cast<uint64_t>(k) * 2};
+      const uint32_t bx[2] = {64, static_cast<uint32_t>(s.box_rows)};
+      if ((st = encode(&tx, x, 2, dx, sx, bx)) != RD_OK) return st;
+      const uint64_t dw[2] = {un, static_cast<uint64_t>(k)}, sw[1] = {un * 2};
+      const uint32_t bw[2] = {64, kBK};
+      if ((st = encode(&tw, w, 2, dw, sw, bw)) != RD_OK) return st;
+    }
+    return done(launch_gemm_split(out_dtype == RD_F32, cols, tx, tw, s, cu(stream)));
+  }
+
+  const bool pair = use_pair(sms, m, g_total);
+  CUtensorMap ta = {}, tb = {};
+  if (k > 0) {
+    const uint64_t da[2] = {static_cast<uint64_t>(k), um}, sa[1] = {static_cast<uint64_t>(k) * 2};
+    const uint32_t ba[2] = {64, kBM};
+    if ((st = encode(&ta, x, 2, da, sa, ba)) != RD_OK) return st;
+    const uint64_t db[3] = {un, static_cast<uint64_t>(k), ug};
+    const uint64_t sb[2] = {un * 2, static_cast<uint64_t>(k) * un * 2};
+    const uint32_t bb[3] = {64, kBK, 1};
+    if ((st = encode(&tb, w, 3, db, sb, bb)) != RD_OK) return st;
+  }
+  GemmArgs a = {};
+  a.group_sizes = group_sizes;
+  a.limit = limit;
+  a.status = status;
+  a.out = out;
+  a.m = static_cast<int32_t>(m);
+  a.kc = static_cast<int32_t>(k);
+  a.n_out = static_cast<int32_t>(n);
+  a.g_total = g_total;
+  a.group_offset = group_offset;
+  a.g_local = g_local;
+  a.ldo = n;
+  a.zero_cols = static_cast<int32_t>(n);
+  a.n_tiles = static_cast<int32_t>((n + kBN - 1) / kBN);
+  a.timeout_ns = wait_timeout_ns();
+  a.band_tiles = band_tiles(pair);
+  a.bias = bias;
+  a.residual = residual;
+  a.pre = pre;
+  a.act = act;
+  const int64_t tile = pair ? 2 * kBM : kBM;
+  const int64_t tiles = ((m + tile - 1) / tile + g_local) * a.n_tiles;
+  if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
+  const int grid = pair ? pair_grid(sms, tiles) : grid_for(sms, tiles);
+  return done(launch_gemm_linear(out_dtype == RD_F32, pair, ta, tb, a, grid, cu(stream)));
+}
+
+extern "C" rd_status rd_linear_act_bwd_workspace_size(int64_t m, int64_t n, int32_t g_local, size_t* bytes) {
+  if (bytes == nullptr || m < 0 || n < 0 || g_local < 1) return RD_ERR_INVALID_ARG;
+  if (m > kMaxDim || n > kMaxDim || g_local > RD_MAX_GROUPS) return RD_ERR_UNSUPPORTED;
+  *bytes = static_cast<size_t>(linear_act_bwd_bytes(m, n, g_local));
+  return RD_OK;
+}
+
+extern "C" rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, const void* pre,
+                                       int32_t act, void* d_pre, float* d_bias, int64_t m, int64_t n,
+                                       const int32_t* group_sizes, int32_t g_total,
+                                       int32_t group_offset, int32_t g_local, const int32_t* limit,
+                                       void* workspace, size_t workspace_bytes, int32_t* status,
+                                       rd_stream_t stream) {
+  rd_status st = check_linear(m, 0, n, group_sizes, g_total, group_offset, g_local, limit, status, act, out_dtype);
+  if (st != RD_OK) return st;
+  if (m > 0 && n > 0 && (d_out == nullptr || (pre == nullptr) != (act == RD_ACT_NONE))) return RD_ERR_INVALID_ARG;
+  if (d_bias != nullptr && n > 0 && workspace == nullptr) return RD_ERR_INVALID_ARG;
+  if (!matrix_aligned(d_out, out_dtype) || !aligned16(pre) || !aligned16(d_pre) || !aligned16(d_bias) ||
+      !matrix_aligned(workspace, RD_F32))
+    return RD_ERR_UNSUPPORTED;
+  const uint64_t n2 = static_cast<uint64_t>(m) * static_cast<uint64_t>(n);
+  if (any_overlap<3, 5>({{d_pre, n2 * 2},
+                         {d_bias, static_cast<uint64_t>(g_local) * static_cast<uint64_t>(n) * 4},
+                         {d_bias != nullptr ? workspace : nullptr, workspace_bytes}},
+                        {{d_out, n2 * size_of(out_dtype)},
+                         {pre, n2 * 2},
+                         {group_sizes, static_cast<uint64_t>(g_total) * 4},
+                         {limit, 4},
+                         {status, 4}}))
+    return RD_ERR_INVALID_ARG;
+  if (d_bias != nullptr && workspace_bytes < static_cast<uint64_t>(linear_act_bwd_bytes(m, n, g_local)))
+    return RD_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RD_OK) return st;
+  if (n == 0 || (m == 0 && d_bias == nullptr) || (d_pre == nullptr && d_bias == nullptr)) return RD_OK;
+  ActBwdArgs a = {};
+  a.d_out = d_out;
+  a.pre = pre;
+  a.d_pre = d_pre;
+  a.d_bias = d_bias;
+  a.parts = static_cast<float*>(workspace);
+  a.group_sizes = group_sizes;
+  a.limit = limit;
+  a.status = status;
+  a.m = static_cast<int32_t>(m);
+  a.n = static_cast<int32_t>(n);
+  a.g_total = g_total;
+  a.group_offset = group_offset;
+  a.g_local = g_local;
+  a.act = act;
+  return done(launch_linear_act_bwd(a, out_dtype, sms, cu(stream)));
+}

@@ -16,7 +16,9 @@ enum GemmEpi : int {
   kEpiGlu = 1,    // forward: silu(gate) * up from the gate / up halves of the tile
   kEpiGluBwd = 2,  // dx of the down projection: [d_gate | d_up] from dh and the saved [gate | up]
   kEpiF32 = 3,     // dw: store the f32 accumulator as is
-  kEpiF32Acc = 4   // dw: add the f32 accumulator to the f32 output already in memory
+  kEpiF32Acc = 4,  // dw: add the f32 accumulator to the f32 output already in memory
+  kEpiLinear = 5,    // forward: + bias (-> pre), activation, + residual, to bf16
+  kEpiLinearF32 = 6  // the same with an f32 residual and output
 };
 
 // UMMA tile: kBM x kBN (128 x 256) f32 accumulator per CTA, kBK (64) deep K
@@ -53,6 +55,11 @@ struct GemmArgs {
   int32_t a_chunked;           // dw: tmap_a is (64, rows, width / 64): one box per stage
   int32_t b_chunked;           // dw: tmap_b likewise (else 2-D maps, one box per 64 columns)
   uint64_t timeout_ns;         // bound of every wait inside the kernel
+  // kEpiLinear, kEpiLinearF32 (group_sizes may be null: one group of all rows)
+  const float* bias;           // [g_local, n_out] or null
+  const void* residual;        // [m, n_out] of the output's type or null
+  void* pre;                   // bf16 [m, n_out] or null
+  int32_t act;                 // RD_ACT_*
 };
 
 // `pair`: the CTA-pair variant (clusters of two CTAs, 256-row tiles); `grid`
@@ -60,6 +67,9 @@ struct GemmArgs {
 cudaError_t launch_gemm_fwd(bool glu, bool pair, const CUtensorMap& tmap_a,
                             const CUtensorMap& tmap_b, const GemmArgs& args, int grid,
                             cudaStream_t stream);
+cudaError_t launch_gemm_linear(bool f32_out, bool pair, const CUtensorMap& tmap_a,
+                               const CUtensorMap& tmap_b, const GemmArgs& args, int grid,
+                               cudaStream_t stream);
 cudaError_t launch_gemm_dx(bool pair, bool glu_bwd, const CUtensorMap& tmap_a,
                            const CUtensorMap& tmap_b, const GemmArgs& args, int grid,
                            cudaStream_t stream);

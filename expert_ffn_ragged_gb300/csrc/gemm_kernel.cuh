@@ -51,6 +51,7 @@
 #include <atomic>
 
 #include "../../include/rd.h"
+#include "act_math.cuh"
 #include "gemm_args.h"
 #include "glu_math.cuh"
 #include "ptx.cuh"
@@ -112,6 +113,12 @@ __device__ __forceinline__ long long warp_exclusive_scan(long long v, int lane) 
   return incl - v;
 }
 
+// rows of group i; without group sizes the one group has them all
+template <class Args>
+__device__ __forceinline__ int32_t group_size(const Args& a, int i) {
+  return a.group_sizes != nullptr ? a.group_sizes[i] : a.m;
+}
+
 // Run by one warp: group boundaries, tile prefix, zero ranges, status bits (TM: rows of a
 // tile; Shared and Args: the block's shared state and the launch arguments of a grouped kernel).
 template <int OP, int TM, class Shared, class Args>
@@ -128,14 +135,14 @@ __device__ __forceinline__ void build_schedule(Shared& sh, const Args& a, int la
   long long sum = 0;
   int neg = 0;
   for (int i = lo; i < hi; ++i) {
-    const int s = a.group_sizes[i];
+    const int s = group_size(a, i);
     neg |= s < 0;
     sum += s > 0 ? s : 0;
   }
   long long run = warp_exclusive_scan(sum, lane);
   for (int i = lo; i < hi; ++i) {
     sh.bound[i] = clamp_boundary(run, L);
-    const int s = a.group_sizes[i];
+    const int s = group_size(a, i);
     run += s > 0 ? s : 0;
   }
   const long long total = __shfl_sync(0xFFFFFFFFu, run, 31);
@@ -300,6 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(EPI != kEpiGluBwd || OP == kOpDx, "the GLU backward epilogue follows dx");
   static_assert((EPI != kEpiF32 && EPI != kEpiF32Acc) || OP == kOpDw, "f32 output is for dw");
   constexpr bool F32OUT = (EPI == kEpiF32 || EPI == kEpiF32Acc);
+  constexpr bool LINEAR = (EPI == kEpiLinear || EPI == kEpiLinearF32);
+  static_assert(!LINEAR || OP == kOpFwd, "bias, activation and residual follow the forward product");
   using Cfg = TileCfg<PAIR>;
   constexpr int S = Cfg::kStagesN;
   constexpr int TM = Cfg::kTileM;
@@ -585,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // write the 16 packed words of this lane's row into the staging buffer, then
       // store the chunk's 32 rows x 32 columns to global memory
       // (col_off shifts the destination, e.g. to the d_up half of a fused row)
-      auto emit = [&](const uint32_t (&p)[16], int col, int col_off) {
+      // (dst, where given, takes the place of the output: a bf16 matrix of the same rows)
+      auto emit = [&](const uint32_t (&p)[16], int col, int col_off, __nv_bfloat16* dst = nullptr) {
+        if (!LINEAR || dst == nullptr) dst = base;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           stg[lane * 4 + (v ^ ((lane >> 1) & 3))] =
@@ -598,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = wrow0 + rl;
           const int c = col + piece * 8;
           if (row >= lo && row < hi && c + 8 <= args.n_out)
-            *reinterpret_cast<uint4*>(base + static_cast<size_t>(row) * args.ldo + col_off + c) = val;
+            *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * args.ldo + col_off + c) = val;
         }
         __syncwarp();
       };
-      // f32 output of dw, 16 columns (64 bytes a row) at a time through the same
+      // f32 output (of dw or of a linear product), 16 columns (64 bytes a row) at a time through the same
       // staging layout; the accumulating form adds them to what the output holds
       auto emit_f32 = [&](const uint32_t* v16, int col) {
 #pragma unroll
@@ -610,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           stg[lane * 4 + (v ^ ((lane >> 1) & 3))] =
               make_uint4(v16[4 * v], v16[4 * v + 1], v16[4 * v + 2], v16[4 * v + 3]);
         __syncwarp();
-        float* outf = reinterpret_cast<float*>(args.out) +
-                      static_cast<size_t>(tl.j) * args.m_out * args.ldo;
+        float* outf = reinterpret_cast<float*>(args.out);
+        if (OP == kOpDw) outf += static_cast<size_t>(tl.j) * args.m_out * args.ldo;
         // the accumulating form reads the prior values of all four rows before it
         // writes any (one read-modify-write after another serialised four HBM
         // round trips)
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 val = stg[rl * 4 + (piece ^ ((rl >> 1) & 3))];
           const int row = wrow0 + rl;
           const int c = col + piece * 4;
-          if (row < hi && c + 4 <= args.n_out) {
+          if ((OP == kOpDw || row >= lo) && row < hi && c + 4 <= args.n_out) {
             uint4* dst = reinterpret_cast<uint4*>(outf + static_cast<size_t>(row) * args.ldo + c);
             if (EPI == kEpiF32Acc) {
               const uint4 o = prior[it];
@@ -646,6 +657,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
+      if (LINEAR) {
+        // bias, activation and residual on the f32 sums, of which nothing has been rounded yet; a thread
+        // holds a row, so a bias value is one broadcast load and a row's residual 64 or 128 bytes
+        bool ok = true;
+        if (tl.nkb > 0) {
+          ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          ptx::tc_fence_after();
+        }
+        const uint32_t tb =
+            sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kBN);
+        const float* bias = args.bias == nullptr
+                                ? nullptr
+                                : args.bias + static_cast<size_t>(tl.j) * args.n_out;
+        const int row = wrow0 + lane;
+        const bool row_ok = row >= lo && row < hi;
+        const size_t row_at = static_cast<size_t>(row_ok ? row : 0) * args.ldo;
+#pragma unroll 1
+        for (int c = c_begin; c < c_end; ++c) {
+          const int col = col0 + c * 32;
+          if (col >= args.n_out) break;
+          uint32_t v[32];
+          if (tl.nkb > 0) {
+            ptx::tmem_load_32cols(tb + c * 32, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          if (bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (col + 4 * i + 4 > args.n_out) continue;
+              const float4 b4 = __ldg(reinterpret_cast<const float4*>(bias + col) + i);
+              v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + b4.x);
+              v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + b4.y);
+              v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + b4.z);
+              v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + b4.w);
+            }
+          }
+          uint32_t p[16];
+          if (args.pre != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            emit(p, col, 0, reinterpret_cast<__nv_bfloat16*>(args.pre));
+          }
+          with_act(args.act, [&](auto tag) {
+            constexpr int kAct = decltype(tag)::value;
+            if (kAct == RD_ACT_NONE) return;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_value<kAct>(__uint_as_float(v[i])));
+          });
+          if (args.residual != nullptr && row_ok) {
+            if (EPI == kEpiLinearF32) {
+              const float* src = reinterpret_cast<const float*>(args.residual) + row_at + col;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (col + 4 * i + 4 > args.n_out) continue;
+                const float4 r4 = __ldg(reinterpret_cast<const float4*>(src) + i);
+                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + r4.x);
+                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + r4.y);
+                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + r4.z);
+                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + r4.w);
+              }
+            } else {
+              const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(args.residual) + row_at + col;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (col + 8 * i + 8 > args.n_out) continue;
+                const uint4 r4 = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  v[8 * i + 2 * k] = __float_as_uint(__uint_as_float(v[8 * i + 2 * k]) + bf16_lo(rw[k]));
+                  v[8 * i + 2 * k + 1] = __float_as_uint(__uint_as_float(v[8 * i + 2 * k + 1]) + bf16_hi(rw[k]));
+                }
+              }
+            }
+          }
+          if (EPI == kEpiLinearF32) {
+            emit_f32(v, col);
+            emit_f32(v + 16, col + 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            emit(p, col, 0);
+          }
+        }
+        if (tl.nkb == 0) continue;
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && rank != 0)
+            ptx::mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+          else
+            ptx::mbar_arrive(ptx::smem_addr(&sh.tempty[acc]));
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        continue;
+      }
       if (tl.nkb == 0) {
         const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         for (int c = c_begin; c < c_end; ++c) {
@@ -814,10 +928,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      const uint64_t row_bytes = static_cast<uint64_t>(args.ldo) * 2;
+      const uint64_t row_bytes = static_cast<uint64_t>(args.ldo) * (EPI == kEpiLinearF32 ? 4 : 2);
       const uint64_t lo_bytes = static_cast<uint64_t>(sh.zero_lo) * row_bytes;
       const uint64_t z_bytes = lo_bytes + static_cast<uint64_t>(sh.L - sh.zero_hi) * row_bytes;
-      const uint64_t units16 = z_bytes / 16;
+      // a linear product's bf16 rows before the activation follow as bytes [z_bytes, z_all)
+      const uint64_t pre_row = static_cast<uint64_t>(args.ldo) * 2;
+      const uint64_t pre_lo = static_cast<uint64_t>(sh.zero_lo) * pre_row;
+      const uint64_t z_all = z_bytes + (LINEAR && args.pre != nullptr
+                                            ? pre_lo + static_cast<uint64_t>(sh.L - sh.zero_hi) * pre_row
+                                            : 0);
+      const uint64_t units16 = z_all / 16;
       uint64_t u0, u1;
       zero_share(units16, unit, units, total, PAIR, PAIR ? static_cast<int>(blockIdx.x & 1u) : 0,
                  u0, u1);
@@ -855,11 +975,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t b1 = (u0 + target) * 16;
           while (b < b1) {
             const bool low = b < lo_bytes;
-            const uint64_t seg_end = low ? lo_bytes : z_bytes;
-            const uint64_t addr = low ? b : static_cast<uint64_t>(sh.zero_hi) * row_bytes + (b - lo_bytes);
+            uint64_t seg_end = low ? lo_bytes : z_bytes;
+            uint64_t addr = low ? b : static_cast<uint64_t>(sh.zero_hi) * row_bytes + (b - lo_bytes);
+            char* to = base;
+            if (LINEAR && b >= z_bytes) {
+              const uint64_t pb = b - z_bytes;
+              const bool pre_low = pb < pre_lo;
+              seg_end = pre_low ? z_bytes + pre_lo : z_all;
+              addr = pre_low ? pb : static_cast<uint64_t>(sh.zero_hi) * pre_row + (pb - pre_lo);
+              to = reinterpret_cast<char*>(args.pre);
+            }
             uint64_t len = (b1 < seg_end ? b1 : seg_end) - b;
             if (len > 4096) len = 4096;
-            ptx::bulk_copy_s2g(base + addr, src, static_cast<uint32_t>(len));
+            ptx::bulk_copy_s2g(to + addr, src, static_cast<uint32_t>(len));
             b += len;
           }
           ptx::bulk_commit();

@@ -1,0 +1,273 @@
+// gemm_split.cu -- rd_linear with one weight and few output tiles: a decoding batch, whose time is the
+// weights' bytes, or a router's few columns, whose time is the tokens'.
+//
+// The persistent kernel (gemm_kernel.cuh) gives an output tile to one CTA (pair), so with few tiles most SMs
+// would stand still.  Here an output tile of 128 rows x 64 or 128 columns belongs to a cluster of up to
+// eight CTAs that share its k: each streams its part of the weights through its own ring (TMA, 128-byte
+// swizzle) into a tcgen05 accumulator, writes the f32 sums to shared memory, and after a cluster barrier
+// each adds its share of the tile over the cluster's CTAs, in their order, through distributed shared memory; bias,
+// activation and residual follow in f32.  No workspace, no atomics, no second launch.  Two CTAs fit an SM, so
+// that one's set-up and epilogue overlap the other's copies, and all CTAs of a call usually run at once: the
+// copies of all of them together are what HBM sees.
+//
+// The MMA always has 128 rows; x brings only box_rows of them, and the rest of the operand's rows are whatever
+// lies behind in shared memory: their products land in accumulator rows that nothing reads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "act_math.cuh"
+#include "gemm_split.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "schedule.h"
+
+namespace rd {
+namespace {
+
+constexpr int kSplitThreads = 128;
+constexpr uint64_t kSplitDrainNs = 1000000000ull;
+
+struct SplitShared {
+  uint64_t full[kSplitMaxStages];
+  uint64_t empty[kSplitMaxStages];
+  uint64_t done;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+
+template <int BN>
+constexpr size_t split_smem() {
+  return 1024 + kSplitRingBytes + sizeof(SplitShared);
+}
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <class O, int BN>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    gemm_split_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                      const SplitArgs a) {
+  constexpr int kPitch = BN + 4;  // floats between rows of the staged sums: no bank conflicts
+  static_assert(kSplitRows * kPitch * 4 <= kSplitRingBytes, "the staged sums take the ring's place");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  SplitShared& sh = *reinterpret_cast<SplitShared*>(smem + kSplitRingBytes);
+  const uint32_t a_bytes = static_cast<uint32_t>(a.box_rows) * 128;
+  constexpr uint32_t b_bytes = BN * kBK * 2;
+  uint8_t* s_a = smem;
+  uint8_t* s_b = smem + a.stages * a_bytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&sh.full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh.empty[s]), 1);
+    }
+    ptx::mbar_init(ptx::smem_addr(&sh.done), 1);
+    sh.abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmap_x);
+    ptx::prefetch_tmap(&tmap_w);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(&sh.tmem_base), BN);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
+
+  const int C = a.cluster;
+  const int rank = static_cast<int>(blockIdx.x) % C;
+  const int32_t col0 = static_cast<int32_t>(blockIdx.x) / C * BN;
+  const int32_t L = rows_within(a.limit, a.m);
+  const int32_t row0 = static_cast<int32_t>(blockIdx.y) * kSplitRows;
+  const int32_t row_end = L - row0 > kSplitRows ? row0 + kSplitRows : L;  // rows [row0, row_end) are stored
+  const bool live = row_end > row0;                                       // the same in the whole cluster
+  // the box ends at row_end, so that no row at or past L is read (rows before 0 arrive as zeros)
+  const int32_t row_load = row_end - a.box_rows;
+  const int nkb = ceil_div(a.k, kBK);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / C);
+  const int kb1 = live ? static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / C) : kb0;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int fills = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
+        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, a.timeout_ns)) break;
+        ptx::mbar_arrive_expect_tx(bar, a_bytes + b_bytes);
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c)
+          ptx::tma_load_2d(ptx::smem_addr(s_b + stage * b_bytes + c * (kBK * 128)), &tmap_w, bar, col0 + c * 64,
+                           kb * kBK);
+        ptx::tma_load_2d(ptx::smem_addr(s_a + stage * a_bytes), &tmap_x, bar, kb * kBK, row_load);
+        ++fills;
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (*abort_flag) {
+        // the copies in flight land before this CTA's memory is given up
+        volatile int no_abort = 0;
+        const int last = fills < a.stages ? fills : a.stages;
+        for (int i = 1; i <= last; ++i) {
+          const int f = fills - i;
+          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[f % a.stages]), (f / a.stages) & 1, &no_abort, kSplitDrainNs);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(kSplitRows, BN, false, true);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), phase, abort_flag, a.timeout_ns)) break;
+        ptx::tc_fence_after();
+        const uint32_t a_addr = ptx::smem_addr(s_a + stage * a_bytes);
+        const uint32_t b_addr = ptx::smem_addr(s_b + stage * b_bytes);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          ptx::tc_mma_bf16(sh.tmem_base, ptx::sw128_desc(a_addr + kk * 32, 16, 1024),
+                           ptx::sw128_desc(b_addr + kk * 2048, kBK * 128, 1024), idesc,
+                           (kb > kb0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // arrives when every MMA issued above is complete, after a wait that ran out too
+      ptx::tc_commit(ptx::smem_addr(&sh.done));
+    }
+    __syncwarp();
+  }
+  {
+    volatile int no_abort = 0;
+    // (twice the bound of the other waits, which end first and leave the drain above)
+    ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.done), 0, &no_abort, 2 * a.timeout_ns + kSplitDrainNs);
+    ok = __all_sync(0xFFFFFFFFu, ok) && *abort_flag == 0;
+    ptx::tc_fence_after();
+  }
+  __syncthreads();  // every warp is past its waits: the ring is free
+
+  // the accumulator's rows to shared memory, a thread a row
+  float* stage_f = reinterpret_cast<float*>(smem);
+  const int tile_row = warp * 32 + lane;
+  if (live && warp * 32 < a.box_rows) {
+    const uint32_t tb = sh.tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      uint32_t v[32];
+      if (kb1 > kb0) {
+        ptx::tmem_load_32cols(tb + c * 32, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+      }
+      float4* dst = reinterpret_cast<float4*>(stage_f + tile_row * kPitch + c * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                             __uint_as_float(v[4 * i + 3]));
+    }
+  }
+  ptx::tc_fence_before();
+  if (C > 1) ptx::cluster_sync();
+  else __syncthreads();
+
+  if (live && ok) {
+    const int32_t shift = row0 - row_load;  // tile row of row0
+    const int units = (row_end - row0) * (BN / 8);
+    const uint32_t base = ptx::smem_addr(stage_f);
+    O* out = static_cast<O*>(a.out);
+    for (int u = rank * kSplitThreads + threadIdx.x; u < units; u += C * kSplitThreads) {
+      const int r = u / (BN / 8), c = (u % (BN / 8)) * 8;
+      const int32_t col = col0 + c;
+      if (col >= a.n) continue;
+      const uint32_t at = base + static_cast<uint32_t>(((r + shift) * kPitch + c) * 4);
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+      for (int s = 0; s < C; ++s) {
+        const uint32_t from = C > 1 ? ptx::map_to_rank(at, static_cast<uint32_t>(s)) : at;
+        const float4 lo = ld_cluster(from), hi = ld_cluster(from + 16);
+        z[0] += lo.x, z[1] += lo.y, z[2] += lo.z, z[3] += lo.w;
+        z[4] += hi.x, z[5] += hi.y, z[6] += hi.z, z[7] += hi.w;
+      }
+      if (a.bias != nullptr) {
+        float b[8];
+        load8_param(a.bias + col, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += b[e];
+      }
+      const int64_t place = static_cast<int64_t>(row0 + r) * a.n + col;
+      if (a.pre != nullptr) store8(static_cast<bf16*>(a.pre) + place, z);
+      with_act(a.act, [&](auto tag) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = act_value<decltype(tag)::value>(z[e]);
+      });
+      if (a.residual != nullptr) {
+        float b[8];
+        load8(static_cast<const O*>(a.residual) + place, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += b[e];
+      }
+      store8(out + place, z);
+    }
+  }
+  __syncthreads();
+  if (C > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(sh.tmem_base, BN);
+  }
+  if (threadIdx.x == 0 && !ok && a.status != nullptr) atomicOr(a.status, RD_STATUS_TIMEOUT);
+}
+
+template <class O, int BN>
+cudaError_t go(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(gemm_split_kernel<O, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(split_smem<BN>()));
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, BN)) * static_cast<unsigned>(a.cluster),
+                  static_cast<unsigned>(ceil_div(a.m, kSplitRows)));
+  return launch_pdl(gemm_split_kernel<O, BN>, grid, kSplitThreads, split_smem<BN>(), a.cluster, stream, tx, tw, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_split(bool f32_out, int cols, const CUtensorMap& tx, const CUtensorMap& tw,
+                              const SplitArgs& a, cudaStream_t stream) {
+  if (f32_out)
+    return cols == 64 ? go<float, 64>(tx, tw, a, stream) : go<float, 128>(tx, tw, a, stream);
+  return cols == 64 ? go<bf16, 64>(tx, tw, a, stream) : go<bf16, 128>(tx, tw, a, stream);
+}
+
+}  // namespace rd

@@ -1,0 +1,36 @@
+// gemm_split.h -- launch arguments of the product for few output tiles (gemm_split.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace rd {
+
+struct SplitArgs {
+  const float* bias;      // [n] or null
+  const void* residual;   // [m, n] of the output's type or null
+  void* out;              // [m, n] bf16 or f32
+  void* pre;              // [m, n] bf16 or null
+  const int32_t* limit;
+  int32_t* status;
+  int32_t m;
+  int32_t k;
+  int32_t n;
+  int32_t act;
+  int32_t box_rows;       // rows of x that a box brings (multiple of 8, at most 128)
+  int32_t stages;
+  int32_t cluster;        // CTAs that share one output tile's k
+  uint64_t timeout_ns;
+};
+
+constexpr int kSplitMaxStages = 12;
+constexpr int kSplitRows = 128;    // rows of an output tile
+// dynamic shared memory that leaves room for two blocks on an SM
+constexpr int kSplitRingBytes = 108 * 1024;
+
+// columns of an output tile: 64 or 128
+cudaError_t launch_gemm_split(bool f32_out, int cols, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w,
+                              const SplitArgs& args, cudaStream_t stream);
+
+}  // namespace rd
