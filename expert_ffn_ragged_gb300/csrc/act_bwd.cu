@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kActThreads = 256;
 constexpr int kActBatch = 4;                  // rows of a thread in flight
+constexpr int kActBlocks = 3;                 // blocks on an SM
 constexpr int32_t kChunkRows = 64;            // fewest rows of a chunk that is not a whole group
 constexpr int32_t kWholeGroups = 0;           // chunk_rows: every group is one chunk
 constexpr int64_t kPartsAt = 4 * (kMaxGroups + 4);  // bytes of the workspace before the sums
@@ -96,7 +97,7 @@ __device__ __forceinline__ void build_chunks(Chunks& sh, const ActBwdArgs& a, in
 
 template <class D, int ACT, int W>
 __device__ __forceinline__ void act_bwd_chunk(const ActBwdArgs& a, int32_t lo, int32_t hi, int64_t col,
-                                              bool on, int row_lane, float (&sum)[8]) {
+                                              bool on, int row_lane, float2 (&sum)[4]) {
   constexpr int kLanes = kActThreads / W;
   const D* d_out = static_cast<const D*>(a.d_out);
   const bf16* pre = static_cast<const bf16*>(a.pre);
@@ -124,10 +125,14 @@ __device__ __forceinline__ void act_bwd_chunk(const ActBwdArgs& a, int32_t lo, i
           float z[8];
           widen(rp[b], z);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= act_slope<ACT>(z[e]);
+          for (int e = 0; e < 8; e += 2) {
+            const float2 r = mul2(make_float2(d[e], d[e + 1]), act_slope<ACT>(make_float2(z[e], z[e + 1])));
+            d[e] = r.x;
+            d[e + 1] = r.y;
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += d[e];
+        for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], make_float2(d[2 * e], d[2 * e + 1]));
         if (d_pre != nullptr) store8(d_pre + at + b * step, d);
       }
     }
@@ -136,10 +141,10 @@ __device__ __forceinline__ void act_bwd_chunk(const ActBwdArgs& a, int32_t lo, i
 
 // W: vectors of columns of a block
 template <class D, int ACT, int W>
-__global__ void __launch_bounds__(kActThreads, 3) linear_act_bwd_kernel(const ActBwdArgs a) {
+__global__ void __launch_bounds__(kActThreads, kActBlocks) linear_act_bwd_kernel(const ActBwdArgs a) {
   constexpr int kLanes = kActThreads / W;
   __shared__ Chunks sh;
-  __shared__ float across[kLanes][W * 8];
+  __shared__ __align__(16) float across[kLanes][W * 8];  // pairs are stored at once
   pdl_trigger();
   pdl_wait();
   if (threadIdx.x < 32) build_chunks(sh, a, threadIdx.x);
@@ -172,6 +177,7 @@ __global__ void __launch_bounds__(kActThreads, 3) linear_act_bwd_kernel(const Ac
       continue;
     }
     int j = 0, top = a.g_local;  // the last group that starts at or before the chunk: it has rows (or is whole)
+    if (whole) j = top = chunk;
     while (top - j > 1) {
       const int mid = (j + top) >> 1;
       if (sh.start[mid] <= chunk) j = mid; else top = mid;
@@ -182,14 +188,15 @@ __global__ void __launch_bounds__(kActThreads, 3) linear_act_bwd_kernel(const Ac
       lo += (chunk - sh.start[j]) * a.chunk_rows;
       hi = re - lo > a.chunk_rows ? lo + a.chunk_rows : re;
     }
-    float sum[8];
+    float2 sum[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
     act_bwd_chunk<D, ACT, W>(a, lo, hi, col, on, row_lane, sum);
     if (a.d_bias == nullptr) continue;
     __syncthreads();  // the sums of the unit before have been read
 #pragma unroll
-    for (int e = 0; e < 8; ++e) across[row_lane][col_lane * 8 + e] = sum[e];
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float2*>(&across[row_lane][col_lane * 8 + 2 * e]) = sum[e];
     __syncthreads();
     for (int c = threadIdx.x; c < W * 8; c += kActThreads) {
       if (col0 + c >= n) continue;
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(256) linear_bias_parts_kernel(const ActBwdArgs
 template <class D, int ACT, int W>
 cudaError_t go(ActBwdArgs a, int64_t chunks, int sms, cudaStream_t stream) {
   const int64_t units = chunks * ((static_cast<int64_t>(a.n) + W * 8 - 1) / (W * 8));
-  const int64_t most = static_cast<int64_t>(sms) * 6;
+  const int64_t most = static_cast<int64_t>(sms) * kActBlocks;
   return launch_pdl(linear_act_bwd_kernel<D, ACT, W>, dim3(static_cast<unsigned>(units < most ? units : most)), kActThreads,
                     0, 1, stream, a);
 }

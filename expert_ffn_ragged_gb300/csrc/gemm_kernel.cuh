@@ -708,7 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kAct = decltype(tag)::value;
             if (kAct == RD_ACT_NONE) return;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_value<kAct>(__uint_as_float(v[i])));
+            for (int i = 0; i < 32; i += 2) {
+              const float2 r = act_value<kAct>(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+              v[i] = __float_as_uint(r.x);
+              v[i + 1] = __float_as_uint(r.y);
+            }
           });
           if (args.residual != nullptr && row_ok) {
             if (EPI == kEpiLinearF32) {

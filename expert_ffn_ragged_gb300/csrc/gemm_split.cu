@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       if (a.pre != nullptr) store8(static_cast<bf16*>(a.pre) + place, z);
       with_act(a.act, [&](auto tag) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = act_value<decltype(tag)::value>(z[e]);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 r = act_value<decltype(tag)::value>(make_float2(z[e], z[e + 1]));
+          z[e] = r.x;
+          z[e + 1] = r.y;
+        }
       });
       if (a.residual != nullptr) {
         float b[8];

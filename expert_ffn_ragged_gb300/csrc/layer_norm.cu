@@ -1,16 +1,21 @@
 // layer_norm.cu -- layer norm of rows and its gradients (rd_layer_norm_fwd, rd_layer_norm_bwd).
 //
-// Both directions are one pass over HBM.  T threads hold a row in registers, V vectors of eight elements each,
-// so the mean, the squares about it and the result come from one read; the next row's loads are issued before
-// this row's sums, which hides their latency.  Blocks stay on the SM and take rows in turn, so a thread
-// keeps the same columns: weight and bias stay in registers, and the backward pass adds its columns'
-// d_out * y and d_out there.  At the end each block writes its two sums a column to the workspace and a second
-// kernel adds the blocks' sums in their order (no atomics).
+// Both directions are one pass over HBM.  T threads hold a row in registers, V quads of four elements each, so the
+// mean, the squares about it and the result come from one read.  Blocks stay on the SM and take rows in turn:
+// the next S - 1 rows are on their way to shared memory (cp.async, each thread into words that it alone reads,
+// so no barrier is needed for them) while this row is summed.  A thread keeps the same columns throughout:
+// weight and bias stay in registers, and the backward pass adds its columns' d_out * y and d_out there.
+// At the end the blocks of a cluster add their two sums a column through distributed shared memory, in their
+// order, and write one part a cluster to the workspace; a second kernel adds the parts in theirs (no atomics).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "act_math.cuh"
 #include "block_args.h"
 #include "launch.h"
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace rd {
@@ -33,96 +38,110 @@ __device__ __forceinline__ void row_sum2(float& p, float& q, float2* slot) {
 }
 
 // ------------------------------------------------------------------ forward
-template <class X, class O, int T, int V>
-__global__ void __launch_bounds__(T == 32 ? 256 : T) layer_norm_fwd_kernel(const NormArgs a) {
-  constexpr int kRows = T == 32 ? 8 : 1;       // rows of a block at a time
-  constexpr bool kHold = V <= 2 && T <= 512;   // weight and bias in registers
-  constexpr bool kAhead = V <= 2;              // the next row's loads in flight
+// threads of a block, rows of it at a time, and blocks on an SM (of at most 64 registers a thread)
+template <int T>
+struct Shape {
+  static constexpr int kThreads = T == 32 ? 256 : T;
+  static constexpr int kRows = T == 32 ? 8 : 1;
+  static constexpr int kBlocks = 1024 / kThreads;
+};
+
+template <class X, class O, int T, int V, int S>
+__global__ void __launch_bounds__(Shape<T>::kThreads, Shape<T>::kBlocks) layer_norm_fwd_kernel(const NormArgs a) {
+  constexpr int kThreads = Shape<T>::kThreads, kRows = Shape<T>::kRows;
+  constexpr bool kHold = T <= 512;  // weight and bias in registers
+  using Raw = typename Quad<X>::Raw;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[32];
   __shared__ float2 pairs[32];
   pdl_trigger();
   pdl_wait();
+  Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;
   const int t = threadIdx.x % T;
-  const int vecs = a.hidden >> 3;
+  const int quads = a.hidden >> 2;
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   const float inv = 1.0f / static_cast<float>(a.hidden);
-  const X* x = static_cast<const X*>(a.x);
-  O* out = static_cast<O*>(a.out);
+  const X* x = static_cast<const X*>(a.x) + 4 * t;
+  O* out = static_cast<O*>(a.out) + 4 * t;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
   if (row >= L) return;
-  Raw8<X> raw[V];
-  auto fetch = [&](int64_t r) {
+  auto fetch = [&](int64_t r, int s) {
+    if (r < L) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) load_raw(raw[i], x + r * hidden + 8 * (t + i * T));
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) quad_copy(ring + (s * V + i) * kThreads, x + r * hidden + 4 * i * T);
+    }
+    copies_commit();
   };
-  auto param = [&](const float* p, int i, float none, float (&v)[8]) {
-    if (p != nullptr) {
-      load8_param(p + 8 * (t + i * T), v);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = none;
+  for (int s = 0; s < S - 1; ++s) fetch(row + s * step, s);
+  auto param = [&](const float* p, int i, float none, float2 (&v)[2]) {
+    if (p != nullptr) {
+      widen(*reinterpret_cast<const float4*>(p + 4 * (t + i * T)), v);
+    } else {
+      v[0] = v[1] = both(none);
     }
   };
-  fetch(row);
-  float w[kHold ? V : 1][8], b[kHold ? V : 1][8];
+  float2 w[kHold ? V : 1][2], b[kHold ? V : 1][2];
   if (kHold) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
+      if (t + i * T < quads) {
         param(a.weight, i, 1.0f, w[i]);
         param(a.bias, i, 0.0f, b[i]);
       }
   }
+  int stage = 0;
   for (; row < L; row += step) {
-    float v[V][8];
-    float s = 0.0f;
+    fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    copies_wait<S - 1>();
+    float2 v[V][2];
+    float2 s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
-        widen(raw[i], v[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[i][e];
+      if (t + i * T < quads) {
+        widen(ring[(stage * V + i) * kThreads], v[i]);
+        s2 = add2(s2, add2(v[i][0], v[i][1]));
       }
-    if (kAhead && row + step < L) fetch(row + step);
-    const float mean = row_sum<T>(s, sums) * inv;
+    if (++stage == S) stage = 0;
+    const float mean = row_sum<T>(s2.x + s2.y, sums) * inv;
     // What is left of the mean after its rounding (c) is taken out too: a row far from zero would
     // otherwise be off by an ulp of its mean.
-    float c = 0.0f, q = 0.0f;
+    float2 c2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
+      if (t + i * T < quads) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[i][e] -= mean;
-          c += v[i][e];
-          q = fmaf(v[i][e], v[i][e], q);
+        for (int e = 0; e < 2; ++e) {
+          v[i][e] = add2(v[i][e], both(-mean));
+          c2 = add2(c2, v[i][e]);
+          q2 = fma2(v[i][e], v[i][e], q2);
         }
       }
+    float c = c2.x + c2.y, q = q2.x + q2.y;
     row_sum2<T>(c, q, pairs);
     c *= inv;
     const float var = fmaf(-c, c, q * inv);  // never below zero but by rounding; NaN stays NaN
     const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
+    const float2 back = both(-c), r2 = both(rstd);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
+      if (t + i * T < quads) {
         if (!kHold) {
           param(a.weight, i, 1.0f, w[0]);
           param(a.bias, i, 0.0f, b[0]);
         }
-        const float(&wi)[8] = w[kHold ? i : 0];
-        const float(&bi)[8] = b[kHold ? i : 0];
+        const int h = kHold ? i : 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = fmaf((v[i][e] - c) * rstd, wi[e], bi[e]);
-        store8(out + row * hidden + 8 * (t + i * T), v[i]);
+        for (int e = 0; e < 2; ++e) v[i][e] = fma2(mul2(add2(v[i][e], back), r2), w[h][e], b[h][e]);
+        store4(out + row * hidden + 4 * i * T, v[i]);
       }
     if (t == 0 && a.mean != nullptr) {
       a.mean[row] = mean + c;
       a.rstd[row] = rstd;
     }
-    if (!kAhead && row + step < L) fetch(row + step);
   }
 }
 
@@ -182,110 +201,136 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
 }
 
 // ------------------------------------------------------------------ backward
-template <class X, class O, int T, int V>
-__global__ void __launch_bounds__(T == 32 ? 256 : T) layer_norm_bwd_kernel(const NormArgs a) {
-  constexpr int kRows = T == 32 ? 8 : 1;
-  __shared__ float2 slots[2][32];
-  __shared__ float across[T == 32 ? kRows * 2 * 256 : 1];
+constexpr int kNormCluster = 4;  // blocks that add their sums before they go to the workspace
+
+__device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(ptx::map_to_rank(ptx::smem_addr(local), static_cast<uint32_t>(rank)))
+               : "memory");
+  return v;
+}
+
+template <class X, class O, int T, int V, int S>
+__global__ void __launch_bounds__(Shape<T>::kThreads, V > 2 ? 1 : Shape<T>::kBlocks)
+    layer_norm_bwd_kernel(const NormArgs a) {
+  constexpr int kThreads = Shape<T>::kThreads, kRows = Shape<T>::kRows;
+  constexpr int kCols = T * V * 4;
+  using RawX = typename Quad<X>::Raw;
+  using RawO = typename Quad<O>::Raw;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 pairs[2][32];
   pdl_trigger();
   pdl_wait();
+  RawX* ring_x = reinterpret_cast<RawX*>(smem) + threadIdx.x;
+  RawO* ring_d = reinterpret_cast<RawO*>(smem + S * V * kThreads * sizeof(RawX)) + threadIdx.x;
   const int t = threadIdx.x % T;
-  const int vecs = a.hidden >> 3;
+  const int quads = a.hidden >> 2;
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   const float inv = 1.0f / static_cast<float>(a.hidden);
-  const X* x = static_cast<const X*>(a.x);
-  const O* d_out = static_cast<const O*>(a.d_out);
-  X* d_x = static_cast<X*>(a.out);
+  const X* x = static_cast<const X*>(a.x) + 4 * t;
+  const O* d_out = static_cast<const O*>(a.d_out) + 4 * t;
+  X* d_x = static_cast<X*>(a.out) + 4 * t;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
-  Raw8<X> rx[V];
-  Raw8<O> rd_[V];
-  float mean_next = 0.0f, rstd_next = 0.0f;
-  auto fetch = [&](int64_t r) {
+  auto fetch = [&](int64_t r, int s) {
+    if (r < L) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
-        load_raw(rx[i], x + r * hidden + 8 * (t + i * T));
-        load_raw(rd_[i], d_out + r * hidden + 8 * (t + i * T));
-      }
-    mean_next = a.mean[r];
-    rstd_next = a.rstd[r];
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) {
+          quad_copy(ring_x + (s * V + i) * kThreads, x + r * hidden + 4 * i * T);
+          quad_copy(ring_d + (s * V + i) * kThreads, d_out + r * hidden + 4 * i * T);
+        }
+    }
+    copies_commit();
   };
-  if (row < L) fetch(row);
-  float w[V][8], dw[V][8], db[V][8];
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(row + s * step, s);
+  float2 w[V][2], dw[V][2], db[V][2];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[i][e] = 1.0f;
-      dw[i][e] = db[i][e] = 0.0f;
-    }
-    if (a.weight != nullptr && t + i * T < vecs) load8_param(a.weight + 8 * (t + i * T), w[i]);
+    w[i][0] = w[i][1] = both(1.0f);
+    dw[i][0] = dw[i][1] = db[i][0] = db[i][1] = both(0.0f);
+    if (a.weight != nullptr && t + i * T < quads)
+      widen(*reinterpret_cast<const float4*>(a.weight + 4 * (t + i * T)), w[i]);
   }
-  int slot = 0;
+  float mean_next = 0.0f, rstd_next = 0.0f;
+  if (row < L) {
+    mean_next = a.mean[row];
+    rstd_next = a.rstd[row];
+  }
+  int stage = 0, slot = 0;
   for (; row < L; row += step) {
-    float y[V][8], d[V][8];
-    const float mean = mean_next, rstd = rstd_next;
-    float p = 0.0f, q = 0.0f;
+    fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    const float rstd = rstd_next;
+    const float2 r2 = both(rstd), m2 = both(-mean_next);
+    if (row + step < L) {
+      mean_next = a.mean[row + step];
+      rstd_next = a.rstd[row + step];
+    }
+    copies_wait<S - 1>();
+    float2 y[V][2], d[V][2];
+    float2 p2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
-        widen(rx[i], y[i]);
-        widen(rd_[i], d[i]);
-      }
-    if (row + step < L) fetch(row + step);
+      if (t + i * T < quads) {
+        widen(ring_x[(stage * V + i) * kThreads], y[i]);
+        widen(ring_d[(stage * V + i) * kThreads], d[i]);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[i][e] = (y[i][e] - mean) * rstd;
-          dw[i][e] = fmaf(d[i][e], y[i][e], dw[i][e]);
-          db[i][e] += d[i][e];
-          d[i][e] *= w[i][e];
-          p += d[i][e];
-          q = fmaf(d[i][e], y[i][e], q);
+        for (int e = 0; e < 2; ++e) {
+          y[i][e] = mul2(add2(y[i][e], m2), r2);
+          dw[i][e] = fma2(d[i][e], y[i][e], dw[i][e]);
+          db[i][e] = add2(db[i][e], d[i][e]);
+          d[i][e] = mul2(d[i][e], w[i][e]);
+          p2 = add2(p2, d[i][e]);
+          q2 = fma2(d[i][e], y[i][e], q2);
         }
       }
-    row_sum2<T>(p, q, slots[slot]);
+    if (++stage == S) stage = 0;
+    float p = p2.x + p2.y, q = q2.x + q2.y;
+    row_sum2<T>(p, q, pairs[slot]);
     slot ^= 1;
-    p *= inv;
-    q *= inv;
+    p2 = both(-p * inv);
+    q2 = both(-q * inv);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * T < vecs) {
+      if (t + i * T < quads) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[i][e] = rstd * (d[i][e] - fmaf(y[i][e], q, p));
-        store8(d_x + row * hidden + 8 * (t + i * T), d[i]);
+        for (int e = 0; e < 2; ++e) d[i][e] = mul2(r2, add2(d[i][e], fma2(y[i][e], q2, p2)));
+        store4(d_x + row * hidden + 4 * i * T, d[i]);
       }
   }
-  if (a.parts == nullptr) return;
-  float* part = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * hidden;
-  if (T == 32) {
-    // the block's warps hold the same columns: added in their order through shared memory
-    const int warp = threadIdx.x >> 5;
+  if (a.parts == nullptr) return;  // the same in every block
+  // the ring's place is taken by this block's sums: [rows of the block][d_weight, d_bias][columns]
+  copies_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      across[(warp * 2) * 256 + t * 8 + e] = dw[0][e];
-      across[(warp * 2 + 1) * 256 + t * 8 + e] = db[0][e];
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 512; c += 256) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) s += across[i * 512 + c];
-      const int col = c & 255;
-      if (col < hidden) part[(c >> 8) * hidden + col] = s;
-    }
-    return;
+  for (int i = 0; i < V; ++i) {
+    float* at = sums + (threadIdx.x / T) * 2 * kCols + 4 * (t + i * T);
+    store4(at, dw[i]);
+    store4(at + kCols, db[i]);
   }
+  ptx::cluster_sync();
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  float* part = a.parts + static_cast<int64_t>(blockIdx.x / kNormCluster) * 2 * hidden;
+  for (int u = rank * kThreads + threadIdx.x; u < kCols / 2; u += kNormCluster * kThreads) {
+    const int k = u / (kCols / 4), quad = u - k * (kCols / 4);
+    if (quad >= quads) continue;
+    float2 s[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (t + i * T < vecs) {
-      store8(part + 8 * (t + i * T), dw[i]);
-      store8(part + hidden + 8 * (t + i * T), db[i]);
-    }
+    for (int c = 0; c < kNormCluster; ++c)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float4 v = peer_float4(reinterpret_cast<const float4*>(sums + (i * 2 + k) * kCols) + quad, c);
+        s[0] = add2(s[0], make_float2(v.x, v.y));
+        s[1] = add2(s[1], make_float2(v.z, v.w));
+      }
+    store4(part + k * hidden + 4 * quad, s);
+  }
+  ptx::cluster_sync();  // no block leaves while another reads its sums
 }
 
 // rows too long for registers: d_x alone, the row read twice (the second time from L2)
@@ -388,8 +433,7 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormArgs 
   }
 }
 
-// The blocks' sums to the gradients: 32 columns a block, eight threads a column, each every eighth
-// part in order.
+// The parts to the gradients: 32 columns a block, eight threads a column, each every eighth part in order.
 __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormArgs a, int32_t parts) {
   __shared__ float across[8][33];
   pdl_trigger();
@@ -400,7 +444,7 @@ __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormArgs a,
   float s = 0.0f;
   if (c < cols) {
     const float* p = a.parts + c;
-#pragma unroll 8
+#pragma unroll 10
     for (int i = warp; i < parts; i += 8) s += p[i * cols];
   }
   across[warp][lane] = s;
@@ -415,50 +459,104 @@ __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormArgs a,
 
 int64_t ceil_of(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// dynamic shared memory above the default has to be allowed, once a kernel and device
+template <class... P>
+cudaError_t allow_smem(void (*kernel)(P...), size_t bytes, std::atomic<bool> (&set)[64], int* dev) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  if (set[*dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) set[*dev].store(true, std::memory_order_release);
+  return e;
+}
+
 template <class X, class O, int T, int V>
 cudaError_t fwd(const NormArgs& a, int sms, cudaStream_t stream) {
-  constexpr int kRows = T == 32 ? 8 : 1, threads = T == 32 ? 256 : T;
-  const int64_t blocks = ceil_of(a.rows, kRows), most = static_cast<int64_t>(sms) * (T >= 1024 ? 1 : 1024 / threads);
-  return launch_pdl(layer_norm_fwd_kernel<X, O, T, V>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                    threads, 0, 1, stream, a);
+  // three rows of f32 or five of bf16 in the ring: 192 or 160 KB of an SM; the widest rows fill it alone
+  constexpr int S = V > 4 ? 1 : (sizeof(X) == 4 ? 3 : 5);
+  constexpr size_t smem = static_cast<size_t>(S) * V * Shape<T>::kThreads * sizeof(typename Quad<X>::Raw);
+  auto* kernel = layer_norm_fwd_kernel<X, O, T, V, S>;
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  const cudaError_t e = allow_smem(kernel, smem, set, &dev);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = ceil_of(a.rows, Shape<T>::kRows), most = static_cast<int64_t>(sms) * Shape<T>::kBlocks;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), Shape<T>::kThreads, smem, 1,
+                    stream, a);
 }
 
 template <class X, class O>
 cudaError_t fwd_by_width(const NormArgs& a, int sms, cudaStream_t stream) {
-  const int vecs = a.hidden / 8;
-  if (vecs <= 32) return fwd<X, O, 32, 1>(a, sms, stream);
-  if (vecs <= 64) return fwd<X, O, 32, 2>(a, sms, stream);
-  if (vecs <= 128) return fwd<X, O, 128, 1>(a, sms, stream);
-  if (vecs <= 256) return fwd<X, O, 128, 2>(a, sms, stream);
-  if (vecs <= 512) return fwd<X, O, 256, 2>(a, sms, stream);
-  if (vecs <= 1024) return fwd<X, O, 512, 2>(a, sms, stream);
-  if (vecs <= 2048) return fwd<X, O, 1024, 2>(a, sms, stream);
-  if (vecs <= 4096) return fwd<X, O, 1024, 4>(a, sms, stream);
+  const int quads = a.hidden / 4;
+  if (quads <= 64) return fwd<X, O, 32, 2>(a, sms, stream);
+  if (quads <= 128) return fwd<X, O, 32, 4>(a, sms, stream);
+  if (quads <= 256) return fwd<X, O, 128, 2>(a, sms, stream);
+  if (quads <= 512) return fwd<X, O, 128, 4>(a, sms, stream);
+  if (quads <= 1024) return fwd<X, O, 256, 4>(a, sms, stream);
+  if (quads <= 2048) return fwd<X, O, 512, 4>(a, sms, stream);
+  if (quads <= 4096) return fwd<X, O, 1024, 4>(a, sms, stream);
+  if (quads <= 8192) return fwd<X, O, 1024, 8>(a, sms, stream);
   const int64_t most = 2 * static_cast<int64_t>(sms);
   return launch_pdl(layer_norm_fwd_long_kernel<X, O>, dim3(static_cast<unsigned>(a.rows < most ? a.rows : most)),
                     1024, 0, 1, stream, a);
 }
 
-// threads of a row of the backward kernel that holds rows in registers; 0: rows are too long for it
-int bwd_threads(int64_t hidden) {
-  const int64_t vecs = hidden / 8;
-  return vecs <= 32 ? 32 : (vecs <= 128 ? 128 : (vecs <= 256 ? 256 : (vecs <= 1024 ? 512 : 0)));
+// the backward kernel that holds rows in registers: threads and quads of a thread; 0: rows are too long for it
+struct BwdShape {
+  int threads, quads;
+};
+BwdShape bwd_shape(int64_t hidden) {
+  if (hidden <= 256) return {32, 2};
+  if (hidden <= 1024) return {128, 2};
+  if (hidden <= 2048) return {256, 2};
+  if (hidden <= 4096) return {512, 2};
+  if (hidden <= 8192) return {512, 4};
+  return {0, 0};
 }
 
 template <class X, class O, int T, int V>
-cudaError_t bwd(const NormArgs& a, int parts, cudaStream_t stream) {
-  return launch_pdl(layer_norm_bwd_kernel<X, O, T, V>, dim3(static_cast<unsigned>(parts)), T == 32 ? 256 : T, 0, 1,
+cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
+  constexpr int S = sizeof(X) + sizeof(O) >= 6 ? 3 : 4;
+  constexpr size_t ring = static_cast<size_t>(S) * V * Shape<T>::kThreads *
+                          (sizeof(typename Quad<X>::Raw) + sizeof(typename Quad<O>::Raw));
+  constexpr size_t sums = static_cast<size_t>(Shape<T>::kRows) * 2 * T * V * 4 * 4;
+  constexpr size_t smem = ring > sums ? ring : sums;
+  auto* kernel = layer_norm_bwd_kernel<X, O, T, V, S>;
+  static std::atomic<bool> set[64];
+  static std::atomic<int> resident[64];  // clusters on the device at once
+  int dev = 0;
+  cudaError_t e = allow_smem(kernel, smem, set, &dev);
+  if (e != cudaSuccess) return e;
+  int clusters = resident[dev].load(std::memory_order_acquire);
+  if (clusters == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kNormCluster, 1, 1);
+    cfg.blockDim = dim3(Shape<T>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kNormCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) clusters = 1;
+    resident[dev].store(clusters, std::memory_order_release);
+  }
+  if (clusters < *parts) *parts = clusters;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(*parts * kNormCluster)), Shape<T>::kThreads, smem, kNormCluster,
                     stream, a);
 }
 
 template <class X, class O>
-cudaError_t bwd_by_width(const NormArgs& a, int parts, int sms, cudaStream_t stream) {
-  const int vecs = a.hidden / 8;
-  switch (bwd_threads(a.hidden)) {
-    case 32: return bwd<X, O, 32, 1>(a, parts, stream);
-    case 128: return bwd<X, O, 128, 1>(a, parts, stream);
-    case 256: return bwd<X, O, 256, 1>(a, parts, stream);
-    case 512: return vecs <= 512 ? bwd<X, O, 512, 1>(a, parts, stream) : bwd<X, O, 512, 2>(a, parts, stream);
+cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t stream) {
+  const BwdShape shape = bwd_shape(a.hidden);
+  switch (shape.threads) {
+    case 32: return bwd<X, O, 32, 2>(a, parts, stream);
+    case 128: return bwd<X, O, 128, 2>(a, parts, stream);
+    case 256: return bwd<X, O, 256, 2>(a, parts, stream);
+    case 512: return shape.quads == 2 ? bwd<X, O, 512, 2>(a, parts, stream) : bwd<X, O, 512, 4>(a, parts, stream);
     default: break;
   }
   const int64_t most = 2 * static_cast<int64_t>(sms);
@@ -469,8 +567,8 @@ cudaError_t bwd_by_width(const NormArgs& a, int parts, int sms, cudaStream_t str
   }
   if (a.parts == nullptr) return cudaSuccess;
   return launch_pdl(layer_norm_columns_kernel<X, O>,
-                    dim3(static_cast<unsigned>(ceil_of(a.hidden, 256)), static_cast<unsigned>(parts)), 256, 0, 1,
-                    stream, a, static_cast<int32_t>(ceil_of(a.rows, parts)));
+                    dim3(static_cast<unsigned>(ceil_of(a.hidden, 256)), static_cast<unsigned>(*parts)), 256, 0, 1,
+                    stream, a, static_cast<int32_t>(ceil_of(a.rows, *parts)));
 }
 
 }  // namespace
@@ -484,27 +582,31 @@ cudaError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, int out_dtype, i
                              : fwd_by_width<bf16, bf16>(a, sms, stream);
 }
 
+// the most that the kernels write: as many clusters as fit the SMs' threads, and no more than the rows fill
 int layer_norm_bwd_parts(int64_t rows, int64_t hidden, int sms) {
-  const int threads = bwd_threads(hidden);
-  if (threads == 0) {
-    const int64_t p = ceil_of(rows, 64);
-    return static_cast<int>(p < 1 ? 1 : (p < 64 ? p : 64));
+  const BwdShape shape = bwd_shape(hidden);
+  int64_t p, most;
+  if (shape.threads == 0) {
+    p = ceil_of(rows, 64);
+    most = 64;
+  } else {
+    const int threads = shape.threads == 32 ? 256 : shape.threads;
+    p = ceil_of(rows, kNormCluster * (shape.threads == 32 ? 8 : 1));
+    most = ceil_of(static_cast<int64_t>(sms) * (shape.quads > 2 ? 1 : 1024 / threads), kNormCluster);
   }
-  const int64_t per_block = threads == 32 ? 8 : 1;
-  const int64_t p = ceil_of(rows, 4 * per_block), most = static_cast<int64_t>(sms) * (threads == 32 ? 4 : 1024 / threads);
   return static_cast<int>(p < 1 ? 1 : (p < most ? p : most));
 }
 
 cudaError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, int out_dtype, int sms,
                                   cudaStream_t stream) {
-  const int parts = layer_norm_bwd_parts(a.rows, a.hidden, sms);
+  int parts = layer_norm_bwd_parts(a.rows, a.hidden, sms);
   cudaError_t e;
   if (dtype == RD_F32)
-    e = out_dtype == RD_F32 ? bwd_by_width<float, float>(a, parts, sms, stream)
-                            : bwd_by_width<float, bf16>(a, parts, sms, stream);
+    e = out_dtype == RD_F32 ? bwd_by_width<float, float>(a, &parts, sms, stream)
+                            : bwd_by_width<float, bf16>(a, &parts, sms, stream);
   else
-    e = out_dtype == RD_F32 ? bwd_by_width<bf16, float>(a, parts, sms, stream)
-                            : bwd_by_width<bf16, bf16>(a, parts, sms, stream);
+    e = out_dtype == RD_F32 ? bwd_by_width<bf16, float>(a, &parts, sms, stream)
+                            : bwd_by_width<bf16, bf16>(a, &parts, sms, stream);
   if (e != cudaSuccess || a.parts == nullptr) return e;
   return launch_pdl(layer_norm_parts_kernel, dim3(static_cast<unsigned>(ceil_of(2 * static_cast<int64_t>(a.hidden), 32))),
                     256, 0, 1, stream, a, static_cast<int32_t>(parts));

@@ -86,6 +86,51 @@ __device__ __forceinline__ void load8_param(const float* p, float (&v)[8]) {
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
+// ---- quads: four elements, the unit that a thread copies to shared memory ahead of its use (16 bytes
+// of f32, 8 of bf16: a warp's copies are whole lines in both)
+template <class E>
+struct Quad;
+template <>
+struct Quad<float> {
+  using Raw = float4;
+};
+template <>
+struct Quad<bf16> {
+  using Raw = uint2;
+};
+
+__device__ __forceinline__ void quad_copy(float4* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void quad_copy(uint2* dst, const bf16* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the N newest groups of this thread's copies have landed
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void widen(float4 r, float2 (&v)[2]) {
+  v[0] = make_float2(r.x, r.y);
+  v[1] = make_float2(r.z, r.w);
+}
+__device__ __forceinline__ void widen(uint2 r, float2 (&v)[2]) {
+  v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+  v[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+}
+__device__ __forceinline__ void store4(float* p, const float2 (&v)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+__device__ __forceinline__ void store4(bf16* p, const float2 (&v)[2]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
