@@ -196,6 +196,20 @@ def layer_norm_bwd(d_out, x, weight, mean, rstd, limit=None, need_weight: bool =
     return d_x, d_weight, d_bias
 
 
+_act_sizes = {}
+
+
+def _act_bytes(m, n, g_local):
+    """linear_act_bwd_workspace_bytes, asked once for each set of sizes."""
+    key = (m, n, g_local)
+    need = _act_sizes.get(key)
+    if need is None:
+        if len(_act_sizes) >= 1024:
+            _act_sizes.clear()
+        need = _act_sizes[key] = linear_act_bwd_workspace_bytes(m, n, g_local)
+    return need
+
+
 def _groups(group_sizes, idx):
     """(address, g_total) of optional group sizes."""
     if group_sizes is None:
@@ -281,10 +295,11 @@ def linear_act_bwd(d_out, pre, act: int = ACT_NONE, group_sizes=None, group_offs
         _want(d_bias, "d_bias", shape, f32, idx)
     elif need_bias:
         d_bias = torch.empty(shape, dtype=f32, device=dev)
-    scratch = None
+    scratch = workspace
     if d_bias is not None and g_local >= 1:
-        need = 0 if workspace is not None else linear_act_bwd_workspace_bytes(m, n, g_local)
-        scratch = _scratch(workspace, need, dev, idx)
+        need = 0 if workspace is not None else _act_bytes(m, n, g_local)
+        if workspace is not None or need:
+            scratch = _scratch(workspace, need, dev, idx)
     _launch(lib.rd_linear_act_bwd, "rd_linear_act_bwd", idx, dev, stream, d_out.data_ptr(), out_type, _at(pre), act,
             _at(d_pre), _at(d_bias), m, n, sizes_at, g_total, group_offset, g_local, _word(limit, "limit", idx),
             _at(scratch), 0 if scratch is None else scratch.numel(), _word(status, "status", idx))

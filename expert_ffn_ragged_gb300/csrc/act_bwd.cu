@@ -1,13 +1,17 @@
 // act_bwd.cu -- the gradients of rd_linear in front of its activation (rd_linear_act_bwd).
 //
 // One pass: d_out and pre are read once, d_pre is written once, and the column sums of the unrounded
-// products, group by group, come from the same registers.  The rows of a group are cut into chunks; a block
-// takes a chunk and W vectors of columns, 256 / W rows at a time, adds its rows' products in registers
-// and across its threads in a fixed order, and writes one sum a column to the workspace; a second
-// kernel adds a group's chunks in their order (no atomics).  Where all rows are few, a whole group is one chunk and its
-// sums are the result: one launch, no workspace.
+// products, group by group, come from the same registers.  A block takes W vectors of eight columns and one of
+// P equal shares of the rows, 256 / W rows at a time with the next two on their way to shared memory; P is as many as
+// run at once.  It keeps its sums in registers until its rows' group ends, then adds its threads' in a fixed order
+// and writes one sum a column to the workspace.  Along the rows p and j only rise, so no two meetings of a
+// share p and a group j have the same p + j, and that numbers the sums; a second kernel adds a group's in their
+// order (no atomics).  A few rows over many groups are taken a group a block instead: its sums are the
+// result, and there is neither a workspace nor a second launch (2048 x 1024, 64 groups: 8.4 us against 10.1).
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "act_math.cuh"
 #include "block_args.h"
@@ -19,33 +23,22 @@ namespace rd {
 namespace {
 
 constexpr int kActThreads = 256;
-constexpr int kActBatch = 4;                  // rows of a thread in flight
+constexpr int kActStages = 3;                 // rows of a thread in its ring
 constexpr int kActBlocks = 3;                 // blocks on an SM
-constexpr int32_t kChunkRows = 64;            // fewest rows of a chunk that is not a whole group
-constexpr int32_t kWholeGroups = 0;           // chunk_rows: every group is one chunk
-constexpr int64_t kPartsAt = 4 * (kMaxGroups + 4);  // bytes of the workspace before the sums
+constexpr int kActSlots = 152 * kActBlocks;   // blocks that run at once
+constexpr int kActLeastRows = 16;             // rows of a share
+// the workspace before the sums: rows of a share, then the local groups' boundaries
+constexpr int64_t kPartsAt = 4 * (kMaxGroups + 8);
 
-struct Chunks {
+struct Bounds {
   int32_t bound[kMaxGroups + 1];  // group boundaries, clamped to L
-  int32_t start[kMaxGroups + 1];  // first chunk of each local group
   int32_t L;
-  int32_t zero_lo, zero_hi;       // rows [0, zero_lo) and [zero_hi, L) of d_pre are zero
-  int32_t zeros_lo, zeros;        // chunks of the first range, and of both
 };
 
 // Run by one warp; the sums of group sizes in 64 bits.
-__device__ __forceinline__ void build_chunks(Chunks& sh, const ActBwdArgs& a, int lane) {
+__device__ __forceinline__ void build_bounds(Bounds& sh, const ActBwdArgs& a, int lane) {
   const int32_t L = rows_within(a.limit, a.m);
   auto size_of = [&](int i) { return a.group_sizes != nullptr ? a.group_sizes[i] : a.m; };
-  auto scan = [&](long long v) {
-    long long incl = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    return incl - v;
-  };
   const int G = a.g_total, per = (G + 31) / 32, lo = min(lane * per, G), hi = min(lo + per, G);
   long long sum = 0;
   bool neg = false;
@@ -54,7 +47,13 @@ __device__ __forceinline__ void build_chunks(Chunks& sh, const ActBwdArgs& a, in
     neg |= s < 0;
     sum += s > 0 ? s : 0;
   }
-  long long run = scan(sum);
+  long long incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  long long run = incl - sum;
   for (int i = lo; i < hi; ++i) {
     sh.bound[i] = clamp_boundary(run, L);
     const int32_t s = size_of(i);
@@ -70,146 +69,197 @@ __device__ __forceinline__ void build_chunks(Chunks& sh, const ActBwdArgs& a, in
       if (bits) atomicOr(a.status, bits);
     }
   }
-  __syncwarp();
-  const int32_t R = a.chunk_rows;
-  auto chunks_of = [&](int j) -> long long {
-    if (R == kWholeGroups) return 1;
-    return ceil_div(sh.bound[a.group_offset + j + 1] - sh.bound[a.group_offset + j], R);
-  };
-  const int GL = a.g_local, per2 = (GL + 31) / 32, lo2 = min(lane * per2, GL), hi2 = min(lo2 + per2, GL);
-  long long mine = 0;
-  for (int j = lo2; j < hi2; ++j) mine += chunks_of(j);
-  long long at = scan(mine);
-  for (int j = lo2; j < hi2; ++j) {
-    sh.start[j] = static_cast<int32_t>(at);
-    at += chunks_of(j);
-  }
-  at = __shfl_sync(0xFFFFFFFFu, at, 31);
-  if (lane == 0) {
-    sh.start[GL] = static_cast<int32_t>(at);
-    sh.zero_lo = sh.bound[a.group_offset];
-    sh.zero_hi = sh.bound[a.group_offset + GL];
-    const int32_t zr = kChunkRows;
-    sh.zeros_lo = a.d_pre != nullptr ? ceil_div(sh.zero_lo, zr) : 0;
-    sh.zeros = sh.zeros_lo + (a.d_pre != nullptr ? ceil_div(L - sh.zero_hi, zr) : 0);
-  }
 }
 
+// A thread's eight columns of one row, on their way to or in shared memory.  bf16 is one 16-byte copy.  f32
+// is two, and so that a warp's copies are whole lines, lane l copies the 16-byte pieces l and l + W of its row's 2 W
+// and finds its own, 2 l and 2 l + 1, after the warp's barrier.
+template <class D, int W>
+struct RowPiece;
+template <int W>
+struct RowPiece<bf16, W> {
+  static constexpr int kBytes = 16;  // of a thread
+  static __device__ __forceinline__ void fetch(uint8_t* block, int thread, const bf16* row, int lane, int64_t cols) {
+    if (8 * lane < cols)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(block + 16 * thread))),
+                   "l"(row + 8 * lane)
+                   : "memory");
+  }
+  static __device__ __forceinline__ void read(const uint8_t* block, int thread, float (&v)[8]) {
+    const uint4 r = *reinterpret_cast<const uint4*>(block + 16 * thread);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+template <int W>
+struct RowPiece<float, W> {
+  static constexpr int kBytes = 32;
+  static __device__ __forceinline__ void fetch(uint8_t* block, int thread, const float* row, int lane, int64_t cols) {
+    uint8_t* to = block + 32 * (thread - lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int piece = lane + h * W;
+      if (4 * piece < cols) quad_copy(reinterpret_cast<float4*>(to) + piece, row + 4 * piece);
+    }
+  }
+  static __device__ __forceinline__ void read(const uint8_t* block, int thread, float (&v)[8]) {
+    const float4* p = reinterpret_cast<const float4*>(block + 32 * thread);
+    const float4 x = p[0], y = p[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  }
+};
+
+// Rows [lo, hi), columns [col0, col0 + 8 W): a row a thread at a time, the next kActStages - 1 on their way.
 template <class D, int ACT, int W>
-__device__ __forceinline__ void act_bwd_chunk(const ActBwdArgs& a, int32_t lo, int32_t hi, int64_t col,
-                                              bool on, int row_lane, float2 (&sum)[4]) {
+__device__ __forceinline__ void act_bwd_rows(const ActBwdArgs& a, int32_t lo, int32_t hi, int64_t col0, uint8_t* ring,
+                                              float2 (&sum)[4]) {
+  using PD = RowPiece<D, W>;
+  using PZ = RowPiece<bf16, W>;
   constexpr int kLanes = kActThreads / W;
+  constexpr int kStage = kActThreads * (PD::kBytes + (ACT != RD_ACT_NONE ? PZ::kBytes : 0));
+  const int lane = threadIdx.x % W;
+  const int64_t n = a.n, cols = n - col0;
+  const int row_lane = threadIdx.x / W;
+  const int32_t left = hi - lo - row_lane;  // rows from this thread's first one on
+  const int64_t step = static_cast<int64_t>(kLanes) * n;
+  const int64_t at = (static_cast<int64_t>(lo) + row_lane) * n + col0;  // of this thread's first row
   const D* d_out = static_cast<const D*>(a.d_out);
   const bf16* pre = static_cast<const bf16*>(a.pre);
   bf16* d_pre = static_cast<bf16*>(a.d_pre);
-  const int64_t n = a.n;
-  if (!on) return;
-  const int64_t step = static_cast<int64_t>(kLanes) * n;
-  int64_t at = (static_cast<int64_t>(lo) + row_lane) * n + col;
-  for (int32_t left = hi - lo - row_lane; left > 0; left -= kLanes * kActBatch, at += step * kActBatch) {
-    Raw8<D> rd_[kActBatch];
-    Raw8<bf16> rp[kActBatch];
-#pragma unroll
-    for (int b = 0; b < kActBatch; ++b) {
-      if (left > b * kLanes) {
-        load_raw(rd_[b], d_out + at + b * step);
-        if (ACT != RD_ACT_NONE) load_raw(rp[b], pre + at + b * step);
-      }
+  const bool on = 8 * lane < cols;
+  // every thread of a warp takes as many turns as its first row lane (32 / W rows a warp)
+  const int32_t warp_left = hi - lo - static_cast<int32_t>(threadIdx.x & ~31u) / W;
+  const int turns = warp_left > 0 ? (warp_left - 1) / kLanes + 1 : 0;
+  auto fetch = [&](int turn, int stage) {
+    if (turn * kLanes < left) {
+      uint8_t* to = ring + stage * kStage;
+      PD::fetch(to, threadIdx.x, d_out + at + turn * step, lane, cols);
+      if (ACT != RD_ACT_NONE)
+        PZ::fetch(to + kActThreads * PD::kBytes, threadIdx.x, pre + at + turn * step, lane, cols);
     }
+    copies_commit();
+  };
 #pragma unroll
-    for (int b = 0; b < kActBatch; ++b) {
-      if (left > b * kLanes) {
-        float d[8];
-        widen(rd_[b], d);
-        if (ACT != RD_ACT_NONE) {
-          float z[8];
-          widen(rp[b], z);
+  for (int s = 0; s < kActStages - 1; ++s) fetch(s, s);
+  int stage = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < turns; ++turn) {
+    if (PD::kBytes == 32) __syncwarp();  // the stage's pieces have been read
+    fetch(turn + kActStages - 1, stage == 0 ? kActStages - 1 : stage - 1);
+    copies_wait<kActStages - 1>();
+    if (PD::kBytes == 32) __syncwarp();  // the other lanes' pieces are there too
+    if (on && turn * kLanes < left) {
+      const uint8_t* from = ring + stage * kStage;
+      float d[8];
+      PD::read(from, threadIdx.x, d);
+      if (ACT != RD_ACT_NONE) {
+        float z[8];
+        PZ::read(from + kActThreads * PD::kBytes, threadIdx.x, z);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 r = mul2(make_float2(d[e], d[e + 1]), act_slope<ACT>(make_float2(z[e], z[e + 1])));
-            d[e] = r.x;
-            d[e + 1] = r.y;
-          }
+        for (int e = 0; e < 8; e += 2) {
+          const float2 r = mul2(make_float2(d[e], d[e + 1]), act_slope<ACT>(make_float2(z[e], z[e + 1])));
+          d[e] = r.x;
+          d[e + 1] = r.y;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], make_float2(d[2 * e], d[2 * e + 1]));
-        if (d_pre != nullptr) store8(d_pre + at + b * step, d);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], make_float2(d[2 * e], d[2 * e + 1]));
+      if (d_pre != nullptr) store8(d_pre + at + turn * step + 8 * lane, d);
     }
+    if (++stage == kActStages) stage = 0;
   }
+  copies_wait<0>();
+  if (PD::kBytes == 32) __syncwarp();
 }
 
 // W: vectors of columns of a block
 template <class D, int ACT, int W>
 __global__ void __launch_bounds__(kActThreads, kActBlocks) linear_act_bwd_kernel(const ActBwdArgs a) {
   constexpr int kLanes = kActThreads / W;
-  __shared__ Chunks sh;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ Bounds sh;
   __shared__ __align__(16) float across[kLanes][W * 8];  // pairs are stored at once
   pdl_trigger();
   pdl_wait();
-  if (threadIdx.x < 32) build_chunks(sh, a, threadIdx.x);
+  if (threadIdx.x < 32) build_bounds(sh, a, threadIdx.x);
   __syncthreads();
   const int col_lane = threadIdx.x % W, row_lane = threadIdx.x / W;
   const int64_t n = a.n;
-  const int64_t col_blocks = (n + W * 8 - 1) / (W * 8);
-  const int32_t chunks = sh.start[a.g_local];
-  const int64_t units = (static_cast<int64_t>(chunks) + sh.zeros) * col_blocks;
-  const bool whole = a.chunk_rows == kWholeGroups;
+  const int32_t col_blocks = ceil_div(a.n, W * 8);
+  const int32_t L = sh.L, rows = max(ceil_div(L, max(a.shares, 1)), 1);
+  const int32_t* bound = sh.bound + a.group_offset;
+  const int32_t zero_lo = bound[0], zero_hi = bound[a.g_local];
+  const bool whole = a.shares == 0;
   if (!whole && blockIdx.x == 0 && a.d_bias != nullptr) {
-    // the second kernel finds a group's chunks here
+    // what the second kernel needs to know
     int32_t* head = reinterpret_cast<int32_t*>(a.parts);
-    for (int j = threadIdx.x; j <= a.g_local; j += kActThreads) head[j] = sh.start[j];
+    if (threadIdx.x == 0) head[0] = rows;
+    for (int j = threadIdx.x; j <= a.g_local; j += kActThreads) head[1 + j] = bound[j];
   }
-  float* parts = whole ? a.d_bias : a.parts + kPartsAt / 4;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int32_t chunk = static_cast<int32_t>(u / col_blocks);
-    const int64_t col0 = (u - chunk * col_blocks) * (W * 8), col = col0 + col_lane * 8;
-    const bool on = col < n;
-    if (chunk >= chunks) {
-      const int32_t z = chunk - chunks;
-      const bool low = z < sh.zeros_lo;
-      const int32_t lo = low ? z * kChunkRows : sh.zero_hi + (z - sh.zeros_lo) * kChunkRows;
-      const int32_t end = low ? sh.zero_lo : sh.L;
-      const int32_t hi = end - lo > kChunkRows ? lo + kChunkRows : end;
-      if (on)
-        for (int32_t r = lo + row_lane; r < hi; r += kLanes)
-          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.d_pre) + r * n + col) = make_uint4(0, 0, 0, 0);
+  const int32_t share = static_cast<int32_t>(blockIdx.x / col_blocks);
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x - share * col_blocks) * (W * 8);
+  int32_t r, end;
+  int j = 0;
+  if (whole) {
+    // share: a local group, or the rows before or after them
+    j = share < a.g_local ? share : 0;
+    r = share < a.g_local ? bound[j] : (share == a.g_local ? 0 : zero_hi);
+    end = share < a.g_local ? bound[j + 1] : (share == a.g_local ? zero_lo : L);
+    if (share < a.g_local && r == end && a.d_bias != nullptr)
+      for (int c = threadIdx.x; c < W * 8; c += kActThreads)
+        if (col0 + c < n) a.d_bias[j * n + col0 + c] = 0.0f;
+  } else {
+    const int64_t from = static_cast<int64_t>(share) * rows;
+    if (from >= L) return;
+    r = static_cast<int32_t>(from);
+    end = L - r > rows ? r + rows : L;
+    // the last group that starts at or before r: it has rows, where r is in a group
+    for (int top = a.g_local; top - j > 1;) {
+      const int mid = (j + top) >> 1;
+      if (bound[mid] <= r) j = mid; else top = mid;
+    }
+  }
+  while (r < end) {
+    if (r < zero_lo || r >= zero_hi) {
+      const int32_t hi = r < zero_lo && zero_lo < end ? zero_lo : end;
+      const int64_t col = col0 + col_lane * 8;
+      if (a.d_pre != nullptr && col < n)
+        for (int64_t row = r + static_cast<int64_t>(row_lane); row < hi; row += kLanes)
+          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.d_pre) + row * n + col) = make_uint4(0, 0, 0, 0);
+      r = hi;
       continue;
     }
-    int j = 0, top = a.g_local;  // the last group that starts at or before the chunk: it has rows (or is whole)
-    if (whole) j = top = chunk;
-    while (top - j > 1) {
-      const int mid = (j + top) >> 1;
-      if (sh.start[mid] <= chunk) j = mid; else top = mid;
-    }
-    const int32_t re = sh.bound[a.group_offset + j + 1];
-    int32_t lo = sh.bound[a.group_offset + j], hi = re;
-    if (!whole) {
-      lo += (chunk - sh.start[j]) * a.chunk_rows;
-      hi = re - lo > a.chunk_rows ? lo + a.chunk_rows : re;
-    }
+    while (bound[j + 1] <= r) ++j;
+    const int32_t hi = bound[j + 1] < end ? bound[j + 1] : end;
     float2 sum[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
-    act_bwd_chunk<D, ACT, W>(a, lo, hi, col, on, row_lane, sum);
+    act_bwd_rows<D, ACT, W>(a, r, hi, col0, ring, sum);
+    r = hi;
     if (a.d_bias == nullptr) continue;
-    __syncthreads();  // the sums of the unit before have been read
+    __syncthreads();  // the sums of the rows before have been read
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<float2*>(&across[row_lane][col_lane * 8 + 2 * e]) = sum[e];
     __syncthreads();
+    float* part = whole ? a.d_bias + j * n + col0
+                        : a.parts + kPartsAt / 4 + (static_cast<int64_t>(share) + j) * n + col0;
     for (int c = threadIdx.x; c < W * 8; c += kActThreads) {
       if (col0 + c >= n) continue;
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < kLanes; ++i) s += across[i][c];
-      parts[(whole ? j : chunk) * n + col0 + c] = s;
+      part[c] = s;
     }
   }
 }
 
-// A group's chunks to its gradient: 128 columns a block, eight warps that each take every eighth chunk in
-// order.
+// A group's sums to its gradient: 128 columns a block, eight warps that each take every eighth share in order.
 __global__ void __launch_bounds__(256) linear_bias_parts_kernel(const ActBwdArgs a) {
   __shared__ float4 across[8][32];
   pdl_trigger();
@@ -218,62 +268,69 @@ __global__ void __launch_bounds__(256) linear_bias_parts_kernel(const ActBwdArgs
   const int64_t n = a.n, col_blocks = (n + 127) / 128;
   const int32_t* head = reinterpret_cast<const int32_t*>(a.parts);
   const float* parts = a.parts + kPartsAt / 4;
+  const int32_t rows = head[0];
   const int64_t units = col_blocks * a.g_local;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t j = u / col_blocks, col = (u - j * col_blocks) * 128 + lane * 4;
-    const int32_t lo = head[j], hi = head[j + 1];
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int32_t lo = head[1 + j], hi = head[2 + j];
+    const int32_t first = lo / rows, last = hi > lo ? (hi - 1) / rows : first - 1;
+    float2 s[2] = {both(0.0f), both(0.0f)};
     if (col < n) {
 #pragma unroll 8
-      for (int32_t c = lo + warp; c < hi; c += 8) {
-        const float4 p = *reinterpret_cast<const float4*>(parts + c * n + col);
-        s.x += p.x;
-        s.y += p.y;
-        s.z += p.z;
-        s.w += p.w;
+      for (int32_t p = first + warp; p <= last; p += 8) {
+        const float4 v = *reinterpret_cast<const float4*>(parts + (p + j) * n + col);
+        s[0] = add2(s[0], make_float2(v.x, v.y));
+        s[1] = add2(s[1], make_float2(v.z, v.w));
       }
     }
     __syncthreads();
-    across[warp][lane] = s;
+    across[warp][lane] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
     __syncthreads();
     if (warp == 0 && col < n) {
-      s = across[0][lane];
+      widen(across[0][lane], s);
 #pragma unroll
       for (int i = 1; i < 8; ++i) {
-        const float4 p = across[i][lane];
-        s.x += p.x;
-        s.y += p.y;
-        s.z += p.z;
-        s.w += p.w;
+        const float4 v = across[i][lane];
+        s[0] = add2(s[0], make_float2(v.x, v.y));
+        s[1] = add2(s[1], make_float2(v.z, v.w));
       }
-      *reinterpret_cast<float4*>(a.d_bias + j * n + col) = s;
+      store4(a.d_bias + j * n + col, s);
     }
   }
 }
 
+// whether a block takes a whole group: groups enough for all SMs, and no group that could be long
+bool whole_groups(int64_t m, int64_t n, int32_t g_local) { return m <= 2048 && (n + 63) / 64 * g_local >= 304; }
+
 template <class D, int ACT, int W>
-cudaError_t go(ActBwdArgs a, int64_t chunks, int sms, cudaStream_t stream) {
-  const int64_t units = chunks * ((static_cast<int64_t>(a.n) + W * 8 - 1) / (W * 8));
-  const int64_t most = static_cast<int64_t>(sms) * kActBlocks;
-  return launch_pdl(linear_act_bwd_kernel<D, ACT, W>, dim3(static_cast<unsigned>(units < most ? units : most)), kActThreads,
-                    0, 1, stream, a);
+cudaError_t go(ActBwdArgs a, cudaStream_t stream) {
+  constexpr size_t smem = static_cast<size_t>(kActStages) * kActThreads *
+                          (RowPiece<D, W>::kBytes + (ACT != RD_ACT_NONE ? RowPiece<bf16, W>::kBytes : 0));
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  const cudaError_t e = allow_smem(linear_act_bwd_kernel<D, ACT, W>, smem, set, &dev);
+  if (e != cudaSuccess) return e;
+  const int32_t col_blocks = ceil_div(a.n, W * 8);
+  int64_t blocks = a.g_local + 2;
+  a.shares = 0;
+  if (!whole_groups(a.m, a.n, a.g_local)) {
+    a.shares = kActSlots / col_blocks;
+    const int32_t most = ceil_div(a.m, kActLeastRows);
+    if (a.shares > most) a.shares = most;
+    if (a.shares < 1) a.shares = 1;
+    blocks = a.shares;
+  }
+  return launch_pdl(linear_act_bwd_kernel<D, ACT, W>, dim3(static_cast<unsigned>(blocks * col_blocks)), kActThreads, smem, 1,
+                    stream, a);
 }
 
 template <class D, int ACT>
-cudaError_t by_width(ActBwdArgs a, int sms, cudaStream_t stream) {
-  // Whole groups where no more than 2048 rows could meet in one group; chunks of 256 rows where they
-  // still leave each SM eight blocks' work, else of 64.
-  const bool whole = a.m <= 2048;
-  a.chunk_rows = whole ? kWholeGroups
-                       : (static_cast<int64_t>(a.m) / 256 * ((a.n + 255) / 256) >= 8 * static_cast<int64_t>(sms)
-                              ? 4 * kChunkRows
-                              : kChunkRows);
-  const int64_t chunks = whole ? a.g_local + (a.m + kChunkRows - 1) / kChunkRows
-                               : static_cast<int64_t>(a.m) / a.chunk_rows + 1 + a.g_local;
+cudaError_t by_width(const ActBwdArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e;
-  if (whole || a.n <= 64) e = go<D, ACT, 8>(a, chunks, sms, stream);
-  else if (a.n <= 128) e = go<D, ACT, 16>(a, chunks, sms, stream);
-  else e = go<D, ACT, 32>(a, chunks, sms, stream);
+  const bool whole = whole_groups(a.m, a.n, a.g_local);
+  if (whole || a.n <= 64) e = go<D, ACT, 8>(a, stream);
+  else if (a.n <= 128) e = go<D, ACT, 16>(a, stream);
+  else e = go<D, ACT, 32>(a, stream);
   if (e != cudaSuccess || whole || a.d_bias == nullptr) return e;
   const int64_t units = (static_cast<int64_t>(a.n) + 127) / 128 * a.g_local, most = static_cast<int64_t>(sms) * 8;
   return launch_pdl(linear_bias_parts_kernel, dim3(static_cast<unsigned>(units < most ? units : most)), 256, 0, 1,
@@ -282,8 +339,15 @@ cudaError_t by_width(ActBwdArgs a, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+// room for the sums of every share and group (no more shares than go() makes)
 int64_t linear_act_bwd_bytes(int64_t m, int64_t n, int32_t g_local) {
-  return kPartsAt + 4 * n * ((m + kChunkRows - 1) / kChunkRows + g_local);
+  if (whole_groups(m, n, g_local)) return 0;
+  const int64_t width = n <= 64 ? 64 : (n <= 128 ? 128 : 256);
+  int64_t shares = kActSlots / ((n + width - 1) / width > 0 ? (n + width - 1) / width : 1);
+  const int64_t most = (m + kActLeastRows - 1) / kActLeastRows;
+  if (shares > most) shares = most;
+  if (shares < 1) shares = 1;
+  return kPartsAt + 4 * n * (shares + g_local);
 }
 
 namespace {

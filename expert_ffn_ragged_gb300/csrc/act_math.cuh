@@ -2,14 +2,13 @@
 //
 // Products and sums are the packed f32x2 forms, an instruction for two values: an elementwise pass over bf16 is
 // otherwise bound by instructions before it is by HBM.  exp is the hardware base-2 exponential and 1/x
-// the hardware reciprocal (glu_math.cuh), both within a few f32 ulps.
+// the hardware reciprocal, both within a few f32 ulps.
 //
 // Normal distribution function, from its tail, so that z P(z) keeps its relative precision for z far below zero:
 //   P(-|z|) = exp(-z^2 / 2) q(|z|),  q(a) = exp(a^2 / 2) P(-a),  P(|z|) = 1 - P(-|z|).
 // q is a polynomial without constant term in t = 1 / (1 + 0.362 a), fitted to it over [0, 14.5] for
-// the least relative error (8.5e-7; 1.2e-6 as evaluated in f32); past 14.5 the exponential is below
-// f32's smallest number.
-// Logistic: 1 / (1 + exp(-u)), which keeps its relative precision on both sides; below u = -88.7 it is 0.
+// the least relative error (8.5e-7; 1.2e-6 as evaluated in f32); past 13.3 the exponential is taken as 0.
+// Logistic: 1 / (1 + exp(-u)), which keeps its relative precision on both sides; below u = -87.3 it is 0.
 //
 // Slopes: arguments are cut to where the slope has reached its limit (0 or 1) exactly, so that infinite z
 // give that limit and not 0 * inf; the cuts let NaN through.
@@ -59,12 +58,24 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 2^x and 1 / x of the hardware, numbers below 2^-126 to 0 (without that, each would be several instructions)
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // q(a) and exp(-a^2 / 2)
 __device__ __forceinline__ void normal_tail(float2 a, float2& q, float2& e) {
   const float2 x = mul2(mul2(a, both(-0.72134752f)), a);  // log2(e) / 2
-  e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+  e = make_float2(exp2_ftz(x.x), exp2_ftz(x.y));
   const float2 d = fma2(a, both(0.362f), both(1.0f));
-  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 t = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
   q = fma2(both(0.0476632722f), t, both(-0.179082657f));
   q = fma2(q, t, both(0.175375615f));
   q = fma2(q, t, both(0.0296722452f));
@@ -76,8 +87,8 @@ __device__ __forceinline__ void normal_tail(float2 a, float2& q, float2& e) {
 
 // 1 / (1 + 2^x): the logistic of u for x = -u log2(e)
 __device__ __forceinline__ float2 logistic2(float2 x) {
-  const float2 d = add2(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.0f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 d = add2(make_float2(exp2_ftz(x.x), exp2_ftz(x.y)), both(1.0f));
+  return make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
 }
 
 constexpr float kLog2e = 1.44269504f;

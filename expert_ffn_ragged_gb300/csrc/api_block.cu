@@ -193,20 +193,34 @@ rd_status check_linear(int64_t m, int64_t k, int64_t n, const int32_t* group_siz
   return n > kMaxWidth ? RD_ERR_UNSUPPORTED : RD_OK;
 }
 
-// One weight whose output has so few tiles of the persistent kernel that they leave SMs idle: the kernel that
-// splits k over clusters, on tiles of 64 columns while the rows are few, of 128 otherwise.
-bool use_split(int sms, int64_t m, int64_t n) {
-  const int64_t tiles = (m + kBM - 1) / kBM * ((n + kBN - 1) / kBN);
-  return tiles <= sms;
-}
+// Tiles of 128 x 128, by which the two rules below go.
+int64_t square_tiles(int64_t m, int64_t n) { return (m + 127) / 128 * ((n + 127) / 128); }
 
-int split_cols(int64_t m) { return m <= 64 ? 64 : 128; }
+// One weight: the kernel that splits k over clusters, or the persistent one, whose tiles are twice as wide (and on
+// CTA pairs twice as high).  At k = 4096, us split / persistent:
+//   m x n     16 x 14336  256 x 14336  512 x 4096  2048 x 1024  16381 x 128  1024 x 4096  16384 x 256
+//   tiles     112         224          128         128          128          256          256
+//             23 / 37     39 / 39      23 / 30     23 / 29      32 / 35      33 / 30      39 / 36
+bool use_split(int sms, int64_t m, int64_t n) { return 2 * square_tiles(m, n) <= 3 * static_cast<int64_t>(sms); }
 
-// as many CTAs a tile as still all run at once (two an SM), with at least four K blocks each
-int split_cluster(int sms, int64_t tiles, int64_t k) {
+// Its tiles have 128 columns where these are tiles enough for two thirds of the SMs, else 64.  At k = 4096, us 64 / 128:
+//   m x n     256 x 4096  4096 x 256  64 x 4096 (k = 14336)  1 x 14336  128 x 14336  512 x 4096  2048 x 1024  256 x 14336
+//   tiles     64          64          32                     112        112          128         128          224
+//             17 / 20     17 / 20     25 / 29                24 / 23    31 / 29      24 / 23     25 / 23      53 / 39
+int split_cols(int sms, int64_t m, int64_t n) { return 3 * square_tiles(m, n) >= 2 * static_cast<int64_t>(sms) ? 128 : 64; }
+
+// Where tiles of 128 columns are two thirds of the SMs and no more than all, each has an SM and a deep ring for
+// itself (us against two CTAs a tile on half the ring, k = 4096: 1 x 14336 21.6 / 22.2, 96 x 14336 25.8 / 27.4, 16381 x 128
+// 30.6 / 31.9).  Otherwise as many CTAs a tile as still all run at once, two on an SM, with at least four K blocks each
+// (tiles of 64 columns, 256 x 4096: 16.3 on two CTAs a tile, 19.8 alone; 64 x 4096, k = 14336: 23.9 on four, 33 on two
+// with the deep ring).
+bool split_alone(int sms, int cols, int64_t tiles) { return cols == 128 && tiles <= sms; }
+
+int split_cluster(int sms, int cols, int64_t tiles, int64_t k) {
+  if (split_alone(sms, cols, tiles)) return 1;
   const int64_t blocks = (k + kBK - 1) / kBK;
   int c = 1;
-  while (c < 8 && tiles * c * 2 <= 2 * static_cast<int64_t>(sms) && blocks >= 8 * c) c *= 2;
+  while (c < 8 && tiles * c <= sms && blocks >= 8 * c) c *= 2;
   return c;
 }
 
@@ -240,7 +254,7 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
   if (m == 0 || n == 0) return RD_OK;
 
   if (group_sizes == nullptr && use_split(sms, m, n)) {
-    const int cols = split_cols(m);
+    const int cols = split_cols(sms, m, n);
     const int64_t tiles = (m + kSplitRows - 1) / kSplitRows * ((n + cols - 1) / cols);
     SplitArgs s = {};
     s.bias = bias;
@@ -255,8 +269,9 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
     s.act = act;
     s.box_rows = static_cast<int32_t>(m < kSplitRows ? (m + 7) / 8 * 8 : kSplitRows);
     const int stage = s.box_rows * 128 + cols * kBK * 2;
-    s.stages = kSplitRingBytes / stage < kSplitMaxStages ? kSplitRingBytes / stage : kSplitMaxStages;
-    s.cluster = split_cluster(sms, tiles, k);
+    s.ring_bytes = split_alone(sms, cols, tiles) ? kSplitRingAlone : kSplitRing;
+    s.stages = s.ring_bytes / stage < kSplitMaxStages ? s.ring_bytes / stage : kSplitMaxStages;
+    s.cluster = split_cluster(sms, cols, tiles, k);
     s.timeout_ns = wait_timeout_ns();
     CUtensorMap tx = {}, tw = {};
     if (k > 0) {
@@ -324,7 +339,8 @@ extern "C" rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, con
   rd_status st = check_linear(m, 0, n, group_sizes, g_total, group_offset, g_local, limit, status, act, out_dtype);
   if (st != RD_OK) return st;
   if (m > 0 && n > 0 && (d_out == nullptr || (pre == nullptr) != (act == RD_ACT_NONE))) return RD_ERR_INVALID_ARG;
-  if (d_bias != nullptr && n > 0 && workspace == nullptr) return RD_ERR_INVALID_ARG;
+  const uint64_t need = static_cast<uint64_t>(linear_act_bwd_bytes(m, n, g_local));
+  if (d_bias != nullptr && n > 0 && need > 0 && workspace == nullptr) return RD_ERR_INVALID_ARG;
   if (!matrix_aligned(d_out, out_dtype) || !aligned16(pre) || !aligned16(d_pre) || !aligned16(d_bias) ||
       !matrix_aligned(workspace, RD_F32))
     return RD_ERR_UNSUPPORTED;
@@ -338,8 +354,7 @@ extern "C" rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, con
                          {limit, 4},
                          {status, 4}}))
     return RD_ERR_INVALID_ARG;
-  if (d_bias != nullptr && workspace_bytes < static_cast<uint64_t>(linear_act_bwd_bytes(m, n, g_local)))
-    return RD_ERR_INVALID_ARG;
+  if (d_bias != nullptr && workspace_bytes < need) return RD_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = current_device(&sms)) != RD_OK) return st;
   if (n == 0 || (m == 0 && d_bias == nullptr) || (d_pre == nullptr && d_bias == nullptr)) return RD_OK;

@@ -54,7 +54,7 @@ struct ActBwdArgs {
   const void* pre;       // bf16 or null (no activation)
   void* d_pre;           // bf16 or null
   float* d_bias;         // [g_local, n] or null
-  float* parts;          // workspace: the groups' first chunks, then [chunks][n]
+  float* parts;          // workspace: boundaries, then the sums [shares + groups][n]
   const int32_t* group_sizes;  // or null: one group of all rows
   const int32_t* limit;
   int32_t* status;
@@ -64,7 +64,7 @@ struct ActBwdArgs {
   int32_t group_offset;
   int32_t g_local;
   int32_t act;
-  int32_t chunk_rows;    // rows of a chunk (set by the launcher)
+  int32_t shares;        // of the rows, a block's each (set by the launcher)
 };
 
 cudaError_t launch_linear_act_bwd(const ActBwdArgs& a, int out_dtype, int sms, cudaStream_t stream);

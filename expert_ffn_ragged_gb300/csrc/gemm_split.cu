@@ -28,7 +28,7 @@
 namespace rd {
 namespace {
 
-constexpr int kSplitThreads = 128;
+constexpr int kSplitThreads = 256;  // warps 0 and 1 copy and issue the MMAs; all eight take the sums
 constexpr uint64_t kSplitDrainNs = 1000000000ull;
 
 struct SplitShared {
@@ -39,10 +39,7 @@ struct SplitShared {
   int32_t abort_flag;
 };
 
-template <int BN>
-constexpr size_t split_smem() {
-  return 1024 + kSplitRingBytes + sizeof(SplitShared);
-}
+constexpr size_t split_smem(int ring_bytes) { return 1024 + ring_bytes + sizeof(SplitShared); }
 
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   float4 v;
@@ -53,16 +50,16 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   return v;
 }
 
-template <class O, int BN>
+template <class O, int BN, int C>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     gemm_split_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const SplitArgs a) {
   constexpr int kPitch = BN + 4;  // floats between rows of the staged sums: no bank conflicts
-  static_assert(kSplitRows * kPitch * 4 <= kSplitRingBytes, "the staged sums take the ring's place");
+  static_assert(kSplitRows * kPitch * 4 <= kSplitRing, "the staged sums take the ring's place");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  SplitShared& sh = *reinterpret_cast<SplitShared*>(smem + kSplitRingBytes);
+  SplitShared& sh = *reinterpret_cast<SplitShared*>(smem + a.ring_bytes);
   const uint32_t a_bytes = static_cast<uint32_t>(a.box_rows) * 128;
   constexpr uint32_t b_bytes = BN * kBK * 2;
   uint8_t* s_a = smem;
@@ -91,7 +88,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   pdl_trigger();
   pdl_wait();
 
-  const int C = a.cluster;
   const int rank = static_cast<int>(blockIdx.x) % C;
   const int32_t col0 = static_cast<int32_t>(blockIdx.x) / C * BN;
   const int32_t L = rows_within(a.limit, a.m);
@@ -161,6 +157,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       ptx::tc_commit(ptx::smem_addr(&sh.done));
     }
     __syncwarp();
+  } else if (live) {
+    // the other warps have nothing to do until the sums are there: the tile's bias and this CTA's rows of the
+    // residual to L2, a line each (the bias' few lines from one thread only: they are everybody's)
+    constexpr int kLine = 128 / static_cast<int>(sizeof(O)), kLines = BN / kLine;
+    constexpr int kIdle = kSplitThreads - 64;
+    const int i0 = static_cast<int>(threadIdx.x) - 64;
+    if (a.bias != nullptr && i0 < BN / 32 && col0 + i0 * 32 < a.n) ptx::prefetch_l2(a.bias + col0 + i0 * 32);
+    if (a.residual != nullptr) {
+      for (int i = i0 + rank * kIdle; i < (row_end - row0) * kLines; i += C * kIdle) {
+        const int32_t col = col0 + (i % kLines) * kLine;
+        if (col < a.n)
+          ptx::prefetch_l2(static_cast<const O*>(a.residual) + static_cast<int64_t>(row0 + i / kLines) * a.n + col);
+      }
+    }
+    __syncwarp();
   }
   {
     volatile int no_abort = 0;
@@ -171,13 +182,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   __syncthreads();  // every warp is past its waits: the ring is free
 
-  // the accumulator's rows to shared memory, a thread a row
+  // the accumulator's rows to shared memory: a thread a row, two warps a quarter of the rows
   float* stage_f = reinterpret_cast<float*>(smem);
-  const int tile_row = warp * 32 + lane;
-  if (live && warp * 32 < a.box_rows) {
-    const uint32_t tb = sh.tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  const int quarter = warp & 3;  // of tensor memory's lanes, the one that this warp may read
+  const int tile_row = quarter * 32 + lane;
+  if (live && quarter * 32 < a.box_rows) {
+    const uint32_t tb = sh.tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = warp >> 2; c < BN / 32; c += kSplitThreads / 128) {
       uint32_t v[32];
       if (kb1 > kb0) {
         ptx::tmem_load_32cols(tb + c * 32, v);
@@ -196,52 +208,74 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   if (C > 1) ptx::cluster_sync();
   else __syncthreads();
 
-  if (live && ok) {
-    const int32_t shift = row0 - row_load;  // tile row of row0
-    const int units = (row_end - row0) * (BN / 8);
-    const uint32_t base = ptx::smem_addr(stage_f);
-    O* out = static_cast<O*>(a.out);
-    for (int u = rank * kSplitThreads + threadIdx.x; u < units; u += C * kSplitThreads) {
-      const int r = u / (BN / 8), c = (u % (BN / 8)) * 8;
-      const int32_t col = col0 + c;
-      if (col >= a.n) continue;
-      const uint32_t at = base + static_cast<uint32_t>(((r + shift) * kPitch + c) * 4);
-      float z[8];
+  // Every CTA of the cluster adds its share of the tile, its own sums first, then the others' in their order, in
+  // units of four columns and batches whose loads (the units' sums from the other CTAs, bias and residual)
+  // are all in flight at once: a remote load takes half a microsecond.  After its last remote loads it arrives at
+  // the barrier that keeps the CTAs' shared memory until all have read it.
+  constexpr int kBatch = C == 8 ? 2 : 4;  // units (more of them make code that is slower to fetch than the loads to wait for)
+  constexpr int kUnits = BN / 4;                         // of a row
+  const int32_t shift = row0 - row_load;                 // tile row of row0
+  const int units = live && ok ? (row_end - row0) * kUnits : 0;
+  const uint32_t base = ptx::smem_addr(stage_f);
+  const O* residual = static_cast<const O*>(a.residual);
+  O* out = static_cast<O*>(a.out);
+  constexpr int kStride = C * kSplitThreads;
+  bool arrived = C == 1;
+  for (int first = 0; first < units || !arrived; first += kBatch * kStride) {
+    const int u0 = first + rank * kSplitThreads + static_cast<int>(threadIdx.x);
+    float4 part[kBatch][C > 1 ? C - 1 : 1], bias[kBatch];
+    typename Quad<O>::Raw res[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-      for (int s = 0; s < C; ++s) {
-        const uint32_t from = C > 1 ? ptx::map_to_rank(at, static_cast<uint32_t>(s)) : at;
-        const float4 lo = ld_cluster(from), hi = ld_cluster(from + 16);
-        z[0] += lo.x, z[1] += lo.y, z[2] += lo.z, z[3] += lo.w;
-        z[4] += hi.x, z[5] += hi.y, z[6] += hi.z, z[7] += hi.w;
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * kStride, r = u / kUnits, c = (u % kUnits) * 4;
+      if (u < units && col0 + c < a.n) {
+        const uint32_t at = base + static_cast<uint32_t>(((r + shift) * kPitch + c) * 4);
+#pragma unroll
+        for (int s = 1; s < C; ++s) part[i][s - 1] = ld_cluster(ptx::map_to_rank(at, (rank + s) % C));
+        if (a.bias != nullptr) bias[i] = *reinterpret_cast<const float4*>(a.bias + col0 + c);
+        if (residual != nullptr)
+          res[i] = *reinterpret_cast<const typename Quad<O>::Raw*>(
+              residual + static_cast<int64_t>(row0 + r) * a.n + col0 + c);
       }
-      if (a.bias != nullptr) {
-        float b[8];
-        load8_param(a.bias + col, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += b[e];
-      }
-      const int64_t place = static_cast<int64_t>(row0 + r) * a.n + col;
-      if (a.pre != nullptr) store8(static_cast<bf16*>(a.pre) + place, z);
-      with_act(a.act, [&](auto tag) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float2 r = act_value<decltype(tag)::value>(make_float2(z[e], z[e + 1]));
-          z[e] = r.x;
-          z[e + 1] = r.y;
-        }
-      });
-      if (a.residual != nullptr) {
-        float b[8];
-        load8(static_cast<const O*>(a.residual) + place, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += b[e];
-      }
-      store8(out + place, z);
     }
+    if (C > 1 && !arrived && first + kBatch * kStride >= units) {
+      // the same batch for every thread of the block; the arrival orders this thread's loads before it
+      __syncwarp();
+      ptx::cluster_arrive();
+      arrived = true;
+    }
+    with_act(a.act, [&](auto tag) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = u0 + i * kStride, r = u / kUnits, c = (u % kUnits) * 4;
+        if (u >= units || col0 + c >= a.n) continue;
+        float2 z[2];
+        widen(*reinterpret_cast<const float4*>(stage_f + (r + shift) * kPitch + c), z);
+#pragma unroll
+        for (int s = 1; s < C; ++s) {
+          z[0] = add2(z[0], make_float2(part[i][s - 1].x, part[i][s - 1].y));
+          z[1] = add2(z[1], make_float2(part[i][s - 1].z, part[i][s - 1].w));
+        }
+        if (a.bias != nullptr) {
+          z[0] = add2(z[0], make_float2(bias[i].x, bias[i].y));
+          z[1] = add2(z[1], make_float2(bias[i].z, bias[i].w));
+        }
+        const int64_t place = static_cast<int64_t>(row0 + r) * a.n + col0 + c;
+        if (a.pre != nullptr) store4(static_cast<bf16*>(a.pre) + place, z);
+        z[0] = act_value<decltype(tag)::value>(z[0]);
+        z[1] = act_value<decltype(tag)::value>(z[1]);
+        if (residual != nullptr) {
+          float2 e[2];
+          widen(res[i], e);
+          z[0] = add2(z[0], e[0]);
+          z[1] = add2(z[1], e[1]);
+        }
+        store4(out + place, z);
+      }
+    });
   }
-  __syncthreads();
-  if (C > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
+  __syncwarp();
+  if (C > 1) ptx::cluster_wait();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(sh.tmem_base, BN);
@@ -249,20 +283,30 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   if (threadIdx.x == 0 && !ok && a.status != nullptr) atomicOr(a.status, RD_STATUS_TIMEOUT);
 }
 
-template <class O, int BN>
+template <class O, int BN, int C>
 cudaError_t go(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_split_kernel<O, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(split_smem<BN>()));
+    const cudaError_t e = cudaFuncSetAttribute(gemm_split_kernel<O, BN, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(split_smem(kSplitRingAlone)));
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, BN)) * static_cast<unsigned>(a.cluster),
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, BN)) * static_cast<unsigned>(C),
                   static_cast<unsigned>(ceil_div(a.m, kSplitRows)));
-  return launch_pdl(gemm_split_kernel<O, BN>, grid, kSplitThreads, split_smem<BN>(), a.cluster, stream, tx, tw, a);
+  return launch_pdl(gemm_split_kernel<O, BN, C>, grid, kSplitThreads, split_smem(a.ring_bytes), C, stream, tx, tw, a);
+}
+
+template <class O, int BN>
+cudaError_t by_cluster(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
+  switch (a.cluster) {
+    case 8: return go<O, BN, 8>(tx, tw, a, stream);
+    case 4: return go<O, BN, 4>(tx, tw, a, stream);
+    case 2: return go<O, BN, 2>(tx, tw, a, stream);
+    default: return go<O, BN, 1>(tx, tw, a, stream);
+  }
 }
 
 }  // namespace
@@ -270,8 +314,8 @@ cudaError_t go(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a,
 cudaError_t launch_gemm_split(bool f32_out, int cols, const CUtensorMap& tx, const CUtensorMap& tw,
                               const SplitArgs& a, cudaStream_t stream) {
   if (f32_out)
-    return cols == 64 ? go<float, 64>(tx, tw, a, stream) : go<float, 128>(tx, tw, a, stream);
-  return cols == 64 ? go<bf16, 64>(tx, tw, a, stream) : go<bf16, 128>(tx, tw, a, stream);
+    return cols == 64 ? by_cluster<float, 64>(tx, tw, a, stream) : by_cluster<float, 128>(tx, tw, a, stream);
+  return cols == 64 ? by_cluster<bf16, 64>(tx, tw, a, stream) : by_cluster<bf16, 128>(tx, tw, a, stream);
 }
 
 }  // namespace rd

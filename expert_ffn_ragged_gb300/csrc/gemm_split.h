@@ -20,14 +20,16 @@ struct SplitArgs {
   int32_t act;
   int32_t box_rows;       // rows of x that a box brings (multiple of 8, at most 128)
   int32_t stages;
+  int32_t ring_bytes;     // of shared memory for the stages: kSplitRing or kSplitRingAlone
   int32_t cluster;        // CTAs that share one output tile's k
   uint64_t timeout_ns;
 };
 
 constexpr int kSplitMaxStages = 12;
 constexpr int kSplitRows = 128;    // rows of an output tile
-// dynamic shared memory that leaves room for two blocks on an SM
-constexpr int kSplitRingBytes = 108 * 1024;
+// rings that leave room for two CTAs on an SM, and for one
+constexpr int kSplitRing = 108 * 1024;
+constexpr int kSplitRingAlone = 216 * 1024;
 
 // columns of an output tile: 64 or 128
 cudaError_t launch_gemm_split(bool f32_out, int cols, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w,

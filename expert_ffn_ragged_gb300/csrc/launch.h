@@ -14,6 +14,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace rd {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -38,6 +40,17 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// dynamic shared memory above the default has to be allowed, once a kernel and device
+template <class... P>
+cudaError_t allow_smem(void (*kernel)(P...), size_t bytes, std::atomic<bool> (&set)[64], int* dev) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  if (set[*dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) set[*dev].store(true, std::memory_order_release);
+  return e;
 }
 
 }  // namespace rd

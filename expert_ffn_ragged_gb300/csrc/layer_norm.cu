@@ -21,39 +21,22 @@
 namespace rd {
 namespace {
 
-// two sums across a row's threads with one barrier (the slots as in row_sum)
-template <int T>
-__device__ __forceinline__ void row_sum2(float& p, float& q, float2* slot) {
-  p = warp_sum(p);
-  q = warp_sum(q);
-  if (T == 32) return;
-  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = make_float2(p, q);
-  __syncthreads();
-  p = q = 0.0f;
-#pragma unroll
-  for (int i = 0; i < T / 32; ++i) {
-    p += slot[i].x;
-    q += slot[i].y;
-  }
-}
-
 // ------------------------------------------------------------------ forward
-// threads of a block, rows of it at a time, and blocks on an SM (of at most 64 registers a thread)
+// T threads hold R rows of V quads a thread; a block of fewer than 128 such threads takes several row groups
 template <int T>
 struct Shape {
   static constexpr int kThreads = T == 32 ? 256 : T;
-  static constexpr int kRows = T == 32 ? 8 : 1;
-  static constexpr int kBlocks = 1024 / kThreads;
+  static constexpr int kGroups = kThreads / T;
 };
 
-template <class X, class O, int T, int V, int S>
-__global__ void __launch_bounds__(Shape<T>::kThreads, Shape<T>::kBlocks) layer_norm_fwd_kernel(const NormArgs a) {
-  constexpr int kThreads = Shape<T>::kThreads, kRows = Shape<T>::kRows;
+template <class X, class O, int T, int V, int R, int S, int B>
+__global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_fwd_kernel(const NormArgs a) {
+  constexpr int kThreads = Shape<T>::kThreads, kGroups = Shape<T>::kGroups;
   constexpr bool kHold = T <= 512;  // weight and bias in registers
   using Raw = typename Quad<X>::Raw;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[32];
-  __shared__ float2 pairs[32];
+  __shared__ __align__(16) float sums[32 * R];
+  __shared__ __align__(16) float pairs[32 * 2 * R];
   pdl_trigger();
   pdl_wait();
   Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;
@@ -61,18 +44,21 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, Shape<T>::kBlocks) layer_n
   const int quads = a.hidden >> 2;
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups * R;
   const float inv = 1.0f / static_cast<float>(a.hidden);
   const X* x = static_cast<const X*>(a.x) + 4 * t;
   O* out = static_cast<O*>(a.out) + 4 * t;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / T) * R;
   if (row >= L) return;
-  auto fetch = [&](int64_t r, int s) {
-    if (r < L) {
+  auto fetch = [&](int64_t first, int s) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (t + i * T < quads) quad_copy(ring + (s * V + i) * kThreads, x + r * hidden + 4 * i * T);
-    }
+    for (int j = 0; j < R; ++j)
+      if (first + j < L) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < quads)
+            quad_copy(ring + ((s * R + j) * V + i) * kThreads, x + (first + j) * hidden + 4 * i * T);
+      }
     copies_commit();
   };
 #pragma unroll
@@ -97,50 +83,65 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, Shape<T>::kBlocks) layer_n
   for (; row < L; row += step) {
     fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
     copies_wait<S - 1>();
-    float2 v[V][2];
-    float2 s2 = both(0.0f);
+    // rows past the last one hold whatever the ring held: their sums are not used
+    float2 v[R][V][2];
+    float mean[R], cq[2 * R];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < quads) {
-        widen(ring[(stage * V + i) * kThreads], v[i]);
-        s2 = add2(s2, add2(v[i][0], v[i][1]));
-      }
+    for (int j = 0; j < R; ++j) {
+      float2 s2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) {
+          widen(ring[((stage * R + j) * V + i) * kThreads], v[j][i]);
+          s2 = add2(s2, add2(v[j][i][0], v[j][i][1]));
+        }
+      mean[j] = s2.x + s2.y;
+    }
     if (++stage == S) stage = 0;
-    const float mean = row_sum<T>(s2.x + s2.y, sums) * inv;
+    row_sums<T>(mean, sums);
     // What is left of the mean after its rounding (c) is taken out too: a row far from zero would
     // otherwise be off by an ulp of its mean.
-    float2 c2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < quads) {
+    for (int j = 0; j < R; ++j) {
+      mean[j] *= inv;
+      float2 c2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[i][e] = add2(v[i][e], both(-mean));
-          c2 = add2(c2, v[i][e]);
-          q2 = fma2(v[i][e], v[i][e], q2);
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            v[j][i][e] = add2(v[j][i][e], both(-mean[j]));
+            c2 = add2(c2, v[j][i][e]);
+            q2 = fma2(v[j][i][e], v[j][i][e], q2);
+          }
         }
-      }
-    float c = c2.x + c2.y, q = q2.x + q2.y;
-    row_sum2<T>(c, q, pairs);
-    c *= inv;
-    const float var = fmaf(-c, c, q * inv);  // never below zero but by rounding; NaN stays NaN
-    const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
-    const float2 back = both(-c), r2 = both(rstd);
+      cq[2 * j] = c2.x + c2.y;
+      cq[2 * j + 1] = q2.x + q2.y;
+    }
+    row_sums<T>(cq, pairs);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < quads) {
-        if (!kHold) {
-          param(a.weight, i, 1.0f, w[0]);
-          param(a.bias, i, 0.0f, b[0]);
+    for (int j = 0; j < R; ++j) {
+      const float c = cq[2 * j] * inv;
+      const float var = fmaf(-c, c, cq[2 * j + 1] * inv);  // never below zero but by rounding; NaN stays NaN
+      const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
+      const float2 r2 = both(rstd), back = both(-c * rstd);
+      if (R > 1 && row + j >= L) break;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) {
+          if (!kHold) {
+            param(a.weight, i, 1.0f, w[0]);
+            param(a.bias, i, 0.0f, b[0]);
+          }
+          const int h = kHold ? i : 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) v[j][i][e] = fma2(fma2(v[j][i][e], r2, back), w[h][e], b[h][e]);
+          store4(out + (row + j) * hidden + 4 * i * T, v[j][i]);
         }
-        const int h = kHold ? i : 0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) v[i][e] = fma2(mul2(add2(v[i][e], back), r2), w[h][e], b[h][e]);
-        store4(out + row * hidden + 4 * i * T, v[i]);
+      if (t == 0 && a.mean != nullptr) {
+        a.mean[row + j] = mean[j] + c;
+        a.rstd[row + j] = rstd;
       }
-    if (t == 0 && a.mean != nullptr) {
-      a.mean[row] = mean + c;
-      a.rstd[row] = rstd;
     }
   }
 }
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, Shape<T>::kBlocks) layer_n
 // rows too long for registers: three reads of the row, of which the last two come from L2
 template <class X, class O>
 __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArgs a) {
-  __shared__ float sums[32];
-  __shared__ float2 pairs[32];
+  __shared__ __align__(16) float sums[32];
+  __shared__ __align__(16) float pairs[64];
   pdl_trigger();
   pdl_wait();
   const int vecs = a.hidden >> 3;
@@ -159,13 +160,14 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
   for (int64_t row = blockIdx.x; row < L; row += gridDim.x) {
     const X* x = static_cast<const X*>(a.x) + row * hidden;
     O* out = static_cast<O*>(a.out) + row * hidden;
-    float s = 0.0f, c = 0.0f, q = 0.0f;
+    float s[1] = {0.0f}, cq[2] = {0.0f, 0.0f};
     for (int64_t v = threadIdx.x; v < vecs; v += 1024) {
       float e[8];
       load8(x + 8 * v, e);
-      s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      s[0] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
     }
-    const float mean = row_sum<1024>(s, sums) * inv;
+    row_sums<1024>(s, sums);
+    const float mean = s[0] * inv;
     for (int64_t v = threadIdx.x; v < vecs; v += 1024) {
       float e[8];
       load8(x + 8 * v, e);
@@ -175,12 +177,12 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
         k += e[i] - mean;
         p = fmaf(e[i] - mean, e[i] - mean, p);
       }
-      c += k;
-      q += p;
+      cq[0] += k;
+      cq[1] += p;
     }
-    row_sum2<1024>(c, q, pairs);
-    c *= inv;
-    const float var = fmaf(-c, c, q * inv);  // never below zero but by rounding; NaN stays NaN
+    row_sums<1024>(cq, pairs);
+    const float c = cq[0] * inv;
+    const float var = fmaf(-c, c, cq[1] * inv);  // never below zero but by rounding; NaN stays NaN
     const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
     for (int64_t v = threadIdx.x; v < vecs; v += 1024) {
       float e[8], w[8], b[8];
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kNormCluster = 4;  // blocks that add their sums before they go to the workspace
+constexpr int kNormCluster = 2;  // blocks that add their sums before they go to the workspace
 
 __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
   float4 v;
@@ -212,38 +214,39 @@ __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
   return v;
 }
 
-template <class X, class O, int T, int V, int S>
-__global__ void __launch_bounds__(Shape<T>::kThreads, V > 2 ? 1 : Shape<T>::kBlocks)
-    layer_norm_bwd_kernel(const NormArgs a) {
-  constexpr int kThreads = Shape<T>::kThreads, kRows = Shape<T>::kRows;
+template <class X, class O, int T, int V, int R, int S, int B>
+__global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(const NormArgs a) {
+  constexpr int kThreads = Shape<T>::kThreads, kGroups = Shape<T>::kGroups;
   constexpr int kCols = T * V * 4;
   using RawX = typename Quad<X>::Raw;
   using RawO = typename Quad<O>::Raw;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 pairs[2][32];
+  __shared__ __align__(16) float pairs[2][32 * 2 * R];
   pdl_trigger();
   pdl_wait();
   RawX* ring_x = reinterpret_cast<RawX*>(smem) + threadIdx.x;
-  RawO* ring_d = reinterpret_cast<RawO*>(smem + S * V * kThreads * sizeof(RawX)) + threadIdx.x;
+  RawO* ring_d = reinterpret_cast<RawO*>(smem + S * R * V * kThreads * sizeof(RawX)) + threadIdx.x;
   const int t = threadIdx.x % T;
   const int quads = a.hidden >> 2;
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups * R;
   const float inv = 1.0f / static_cast<float>(a.hidden);
   const X* x = static_cast<const X*>(a.x) + 4 * t;
   const O* d_out = static_cast<const O*>(a.d_out) + 4 * t;
   X* d_x = static_cast<X*>(a.out) + 4 * t;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
-  auto fetch = [&](int64_t r, int s) {
-    if (r < L) {
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / T) * R;
+  auto fetch = [&](int64_t first, int s) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (t + i * T < quads) {
-          quad_copy(ring_x + (s * V + i) * kThreads, x + r * hidden + 4 * i * T);
-          quad_copy(ring_d + (s * V + i) * kThreads, d_out + r * hidden + 4 * i * T);
-        }
-    }
+    for (int j = 0; j < R; ++j)
+      if (first + j < L) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < quads) {
+            quad_copy(ring_x + ((s * R + j) * V + i) * kThreads, x + (first + j) * hidden + 4 * i * T);
+            quad_copy(ring_d + ((s * R + j) * V + i) * kThreads, d_out + (first + j) * hidden + 4 * i * T);
+          }
+      }
     copies_commit();
   };
 #pragma unroll
@@ -256,51 +259,70 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, V > 2 ? 1 : Shape<T>::kBlo
     if (a.weight != nullptr && t + i * T < quads)
       widen(*reinterpret_cast<const float4*>(a.weight + 4 * (t + i * T)), w[i]);
   }
-  float mean_next = 0.0f, rstd_next = 0.0f;
-  if (row < L) {
-    mean_next = a.mean[row];
-    rstd_next = a.rstd[row];
-  }
+  float mean_next[R], rstd_next[R];
+  auto stats = [&](int64_t first) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mean_next[j] = rstd_next[j] = 0.0f;
+      if (first + j < L) {
+        mean_next[j] = a.mean[first + j];
+        rstd_next[j] = a.rstd[first + j];
+      }
+    }
+  };
+  stats(row);
   int stage = 0, slot = 0;
   for (; row < L; row += step) {
     fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-    const float rstd = rstd_next;
-    const float2 r2 = both(rstd), m2 = both(-mean_next);
-    if (row + step < L) {
-      mean_next = a.mean[row + step];
-      rstd_next = a.rstd[row + step];
+    float2 r2[R], m2[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      r2[j] = both(rstd_next[j]);
+      m2[j] = both(-mean_next[j]);
     }
+    stats(row + step);
     copies_wait<S - 1>();
-    float2 y[V][2], d[V][2];
-    float2 p2 = both(0.0f), q2 = both(0.0f);
+    float2 y[R][V][2], d[R][V][2];
+    float pq[2 * R];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < quads) {
-        widen(ring_x[(stage * V + i) * kThreads], y[i]);
-        widen(ring_d[(stage * V + i) * kThreads], d[i]);
+    for (int j = 0; j < R; ++j) {
+      float2 p2 = both(0.0f), q2 = both(0.0f);
+      if (R == 1 || row + j < L) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[i][e] = mul2(add2(y[i][e], m2), r2);
-          dw[i][e] = fma2(d[i][e], y[i][e], dw[i][e]);
-          db[i][e] = add2(db[i][e], d[i][e]);
-          d[i][e] = mul2(d[i][e], w[i][e]);
-          p2 = add2(p2, d[i][e]);
-          q2 = fma2(d[i][e], y[i][e], q2);
-        }
+        for (int i = 0; i < V; ++i)
+          if (t + i * T < quads) {
+            widen(ring_x[((stage * R + j) * V + i) * kThreads], y[j][i]);
+            widen(ring_d[((stage * R + j) * V + i) * kThreads], d[j][i]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              y[j][i][e] = mul2(add2(y[j][i][e], m2[j]), r2[j]);
+              dw[i][e] = fma2(d[j][i][e], y[j][i][e], dw[i][e]);
+              db[i][e] = add2(db[i][e], d[j][i][e]);
+              d[j][i][e] = mul2(d[j][i][e], w[i][e]);
+              p2 = add2(p2, d[j][i][e]);
+              q2 = fma2(d[j][i][e], y[j][i][e], q2);
+            }
+          }
       }
+      pq[2 * j] = p2.x + p2.y;
+      pq[2 * j + 1] = q2.x + q2.y;
+    }
     if (++stage == S) stage = 0;
-    float p = p2.x + p2.y, q = q2.x + q2.y;
-    row_sum2<T>(p, q, pairs[slot]);
+    row_sums<T>(pq, pairs[slot]);
     slot ^= 1;
-    p2 = both(-p * inv);
-    q2 = both(-q * inv);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (t + i * T < quads) {
+    for (int j = 0; j < R; ++j) {
+      if (R > 1 && row + j >= L) break;
+      // d_x = rstd g - rstd p / h - y rstd q / h
+      const float2 p2 = both(-pq[2 * j] * inv * r2[j].x), q2 = both(-pq[2 * j + 1] * inv * r2[j].x);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) d[i][e] = mul2(r2, add2(d[i][e], fma2(y[i][e], q2, p2)));
-        store4(d_x + row * hidden + 4 * i * T, d[i]);
-      }
+      for (int i = 0; i < V; ++i)
+        if (t + i * T < quads) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) d[j][i][e] = fma2(y[j][i][e], q2, fma2(d[j][i][e], r2[j], p2));
+          store4(d_x + (row + j) * hidden + 4 * i * T, d[j][i]);
+        }
+    }
   }
   if (a.parts == nullptr) return;  // the same in every block
   // the ring's place is taken by this block's sums: [rows of the block][d_weight, d_bias][columns]
@@ -323,7 +345,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, V > 2 ? 1 : Shape<T>::kBlo
 #pragma unroll
     for (int c = 0; c < kNormCluster; ++c)
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+      for (int i = 0; i < kGroups; ++i) {
         const float4 v = peer_float4(reinterpret_cast<const float4*>(sums + (i * 2 + k) * kCols) + quad, c);
         s[0] = add2(s[0], make_float2(v.x, v.y));
         s[1] = add2(s[1], make_float2(v.z, v.w));
@@ -336,7 +358,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, V > 2 ? 1 : Shape<T>::kBlo
 // rows too long for registers: d_x alone, the row read twice (the second time from L2)
 template <class X, class O>
 __global__ void __launch_bounds__(1024) layer_norm_dx_long_kernel(const NormArgs a) {
-  __shared__ float2 slots[2][32];
+  __shared__ __align__(16) float slots[2][64];
   pdl_trigger();
   pdl_wait();
   const int vecs = a.hidden >> 3;
@@ -349,7 +371,7 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_long_kernel(const NormArgs
     const O* d_out = static_cast<const O*>(a.d_out) + row * hidden;
     X* d_x = static_cast<X*>(a.out) + row * hidden;
     const float mean = a.mean[row], rstd = a.rstd[row];
-    float p = 0.0f, q = 0.0f;
+    float pq[2] = {0.0f, 0.0f};
     auto at = [&](int64_t v, float (&y)[8], float (&d)[8]) {
       load8(x + 8 * v, y);
       load8(d_out + 8 * v, d);
@@ -370,12 +392,11 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_long_kernel(const NormArgs
         pv += d[i];
         qv = fmaf(d[i], y[i], qv);
       }
-      p += pv;
-      q += qv;
+      pq[0] += pv;
+      pq[1] += qv;
     }
-    row_sum2<1024>(p, q, slots[slot]);
-    p *= inv;
-    q *= inv;
+    row_sums<1024>(pq, slots[slot]);
+    const float p = pq[0] * inv, q = pq[1] * inv;
     for (int64_t v = threadIdx.x; v < vecs; v += 1024) {
       float y[8], d[8];
       at(v, y, d);
@@ -433,9 +454,11 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormArgs 
   }
 }
 
-// The parts to the gradients: 32 columns a block, eight threads a column, each every eighth part in order.
-__global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormArgs a, int32_t parts) {
-  __shared__ float across[8][33];
+// The parts to the gradients: 32 columns a block, sixteen threads a column, each every sixteenth part in
+// order (few enough loads to be in flight at once).
+constexpr int kPartLanes = 16;
+__global__ void __launch_bounds__(32 * kPartLanes) layer_norm_parts_kernel(const NormArgs a, int32_t parts) {
+  __shared__ float across[kPartLanes][33];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -445,42 +468,30 @@ __global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormArgs a,
   if (c < cols) {
     const float* p = a.parts + c;
 #pragma unroll 10
-    for (int i = warp; i < parts; i += 8) s += p[i * cols];
+    for (int i = warp; i < parts; i += kPartLanes) s += p[i * cols];
   }
   across[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= cols) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += across[i][lane];
+  for (int i = 0; i < kPartLanes; ++i) s += across[i][lane];
   float* out = c < a.hidden ? a.d_weight : a.d_bias;
   if (out != nullptr) out[c < a.hidden ? c : c - a.hidden] = s;
 }
 
 int64_t ceil_of(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// dynamic shared memory above the default has to be allowed, once a kernel and device
-template <class... P>
-cudaError_t allow_smem(void (*kernel)(P...), size_t bytes, std::atomic<bool> (&set)[64], int* dev) {
-  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
-  if (set[*dev].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) set[*dev].store(true, std::memory_order_release);
-  return e;
-}
-
-template <class X, class O, int T, int V>
+// R rows at a time, S of these in the ring, B blocks on an SM
+template <class X, class O, int T, int V, int R, int S, int B>
 cudaError_t fwd(const NormArgs& a, int sms, cudaStream_t stream) {
-  // three rows of f32 or five of bf16 in the ring: 192 or 160 KB of an SM; the widest rows fill it alone
-  constexpr int S = V > 4 ? 1 : (sizeof(X) == 4 ? 3 : 5);
-  constexpr size_t smem = static_cast<size_t>(S) * V * Shape<T>::kThreads * sizeof(typename Quad<X>::Raw);
-  auto* kernel = layer_norm_fwd_kernel<X, O, T, V, S>;
+  constexpr size_t smem = static_cast<size_t>(S) * R * V * Shape<T>::kThreads * sizeof(typename Quad<X>::Raw);
+  auto* kernel = layer_norm_fwd_kernel<X, O, T, V, R, S, B>;
   static std::atomic<bool> set[64];
   int dev = 0;
   const cudaError_t e = allow_smem(kernel, smem, set, &dev);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = ceil_of(a.rows, Shape<T>::kRows), most = static_cast<int64_t>(sms) * Shape<T>::kBlocks;
+  const int64_t blocks = ceil_of(a.rows, Shape<T>::kGroups * R), most = static_cast<int64_t>(sms) * B;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), Shape<T>::kThreads, smem, 1,
                     stream, a);
 }
@@ -488,40 +499,52 @@ cudaError_t fwd(const NormArgs& a, int sms, cudaStream_t stream) {
 template <class X, class O>
 cudaError_t fwd_by_width(const NormArgs& a, int sms, cudaStream_t stream) {
   const int quads = a.hidden / 4;
-  if (quads <= 64) return fwd<X, O, 32, 2>(a, sms, stream);
-  if (quads <= 128) return fwd<X, O, 32, 4>(a, sms, stream);
-  if (quads <= 256) return fwd<X, O, 128, 2>(a, sms, stream);
-  if (quads <= 512) return fwd<X, O, 128, 4>(a, sms, stream);
-  if (quads <= 1024) return fwd<X, O, 256, 4>(a, sms, stream);
-  if (quads <= 2048) return fwd<X, O, 512, 4>(a, sms, stream);
-  if (quads <= 4096) return fwd<X, O, 1024, 4>(a, sms, stream);
-  if (quads <= 8192) return fwd<X, O, 1024, 8>(a, sms, stream);
+  // Long pieces of a row a thread and few threads a row (little to exchange), and no more bytes on their way than it
+  // takes: with 1024 threads an SM and three rows in the ring, 28157 x 4096 f32 took 122 us instead of 106.
+  // GB/s of f32 to bf16 / bf16 to bf16 / f32 to f32, other forms in brackets:
+  //   256:  - / 5300 / -   (one row at a time 4820, no fewer than three blocks)
+  //   1024: - / 6020 / -   (64 x 4: 5560, 128 x 2 x 2 rows: 5010)
+  //   2048: - / 6170 / -   (128 x 4: 5760)
+  //   4096: 6540 / 6300 / 6630   (256 x 4: bf16 5750, f32 to f32 on three blocks 5810; 128 x 8: f32 6290)
+  //   8192: 6270 / - / -   (512 x 4: 5790);  16384: 6480 / - / -   (1024 x 4: 4730)
+  if (quads <= 64) return fwd<X, O, 32, 2, 2, 2, 3>(a, sms, stream);
+  if (quads <= 128) return fwd<X, O, 32, 4, 1, 2, 3>(a, sms, stream);
+  if (quads <= 256) return fwd<X, O, 32, 8, 1, 2, 2>(a, sms, stream);
+  if (quads <= 512) return fwd<X, O, 64, 8, 1, 2, 8>(a, sms, stream);
+  if (quads <= 1024) {
+    if (sizeof(X) == 2) return fwd<X, O, 128, 8, 1, 2, 4>(a, sms, stream);
+    return fwd<X, O, 256, 4, 1, 2, sizeof(O) == 4 ? 2 : 3>(a, sms, stream);
+  }
+  if (quads <= 2048) return fwd<X, O, 256, 8, 1, 2, 2>(a, sms, stream);
+  if (quads <= 4096) return fwd<X, O, 512, 8, 1, 2, 1>(a, sms, stream);
+  if (quads <= 8192) return fwd<X, O, 1024, 8, 1, 1, 1>(a, sms, stream);
   const int64_t most = 2 * static_cast<int64_t>(sms);
   return launch_pdl(layer_norm_fwd_long_kernel<X, O>, dim3(static_cast<unsigned>(a.rows < most ? a.rows : most)),
                     1024, 0, 1, stream, a);
 }
 
-// the backward kernel that holds rows in registers: threads and quads of a thread; 0: rows are too long for it
+// the backward kernel that holds rows in registers: rows that a block takes at a time and blocks on an
+// SM; 0: rows are too long for it
 struct BwdShape {
-  int threads, quads;
+  int rows, blocks;
 };
 BwdShape bwd_shape(int64_t hidden) {
-  if (hidden <= 256) return {32, 2};
-  if (hidden <= 1024) return {128, 2};
-  if (hidden <= 2048) return {256, 2};
-  if (hidden <= 4096) return {512, 2};
-  if (hidden <= 8192) return {512, 4};
+  if (hidden <= 256) return {8, 3};
+  if (hidden <= 1024) return {2, 4};
+  if (hidden <= 2048) return {2, 2};
+  if (hidden <= 4096) return {1, 2};
+  if (hidden <= 8192) return {1, 1};
   return {0, 0};
 }
 
-template <class X, class O, int T, int V>
+template <class X, class O, int T, int V, int R, int B>
 cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
-  constexpr int S = sizeof(X) + sizeof(O) >= 6 ? 3 : 4;
-  constexpr size_t ring = static_cast<size_t>(S) * V * Shape<T>::kThreads *
+  constexpr int S = 2;
+  constexpr size_t ring = static_cast<size_t>(S) * R * V * Shape<T>::kThreads *
                           (sizeof(typename Quad<X>::Raw) + sizeof(typename Quad<O>::Raw));
-  constexpr size_t sums = static_cast<size_t>(Shape<T>::kRows) * 2 * T * V * 4 * 4;
+  constexpr size_t sums = static_cast<size_t>(Shape<T>::kGroups) * 2 * T * V * 4 * 4;
   constexpr size_t smem = ring > sums ? ring : sums;
-  auto* kernel = layer_norm_bwd_kernel<X, O, T, V, S>;
+  auto* kernel = layer_norm_bwd_kernel<X, O, T, V, R, S, B>;
   static std::atomic<bool> set[64];
   static std::atomic<int> resident[64];  // clusters on the device at once
   int dev = 0;
@@ -551,14 +574,12 @@ cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
 
 template <class X, class O>
 cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t stream) {
-  const BwdShape shape = bwd_shape(a.hidden);
-  switch (shape.threads) {
-    case 32: return bwd<X, O, 32, 2>(a, parts, stream);
-    case 128: return bwd<X, O, 128, 2>(a, parts, stream);
-    case 256: return bwd<X, O, 256, 2>(a, parts, stream);
-    case 512: return shape.quads == 2 ? bwd<X, O, 512, 2>(a, parts, stream) : bwd<X, O, 512, 4>(a, parts, stream);
-    default: break;
-  }
+  // (rows at a time and blocks as bwd_shape has them)
+  if (a.hidden <= 256) return bwd<X, O, 32, 2, 1, 3>(a, parts, stream);
+  if (a.hidden <= 1024) return bwd<X, O, 128, 2, 2, 4>(a, parts, stream);
+  if (a.hidden <= 2048) return bwd<X, O, 256, 2, 2, 2>(a, parts, stream);
+  if (a.hidden <= 4096) return bwd<X, O, 256, 4, 1, 2>(a, parts, stream);
+  if (a.hidden <= 8192) return bwd<X, O, 512, 4, 1, 1>(a, parts, stream);
   const int64_t most = 2 * static_cast<int64_t>(sms);
   if (a.rows > 0) {
     const cudaError_t e = launch_pdl(layer_norm_dx_long_kernel<X, O>,
@@ -586,13 +607,12 @@ cudaError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, int out_dtype, i
 int layer_norm_bwd_parts(int64_t rows, int64_t hidden, int sms) {
   const BwdShape shape = bwd_shape(hidden);
   int64_t p, most;
-  if (shape.threads == 0) {
+  if (shape.rows == 0) {
     p = ceil_of(rows, 64);
     most = 64;
   } else {
-    const int threads = shape.threads == 32 ? 256 : shape.threads;
-    p = ceil_of(rows, kNormCluster * (shape.threads == 32 ? 8 : 1));
-    most = ceil_of(static_cast<int64_t>(sms) * (shape.quads > 2 ? 1 : 1024 / threads), kNormCluster);
+    p = ceil_of(rows, kNormCluster * shape.rows);
+    most = ceil_of(static_cast<int64_t>(sms) * shape.blocks, kNormCluster);
   }
   return static_cast<int>(p < 1 ? 1 : (p < most ? p : most));
 }
@@ -609,7 +629,7 @@ cudaError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, int out_dtype, i
                             : bwd_by_width<bf16, bf16>(a, &parts, sms, stream);
   if (e != cudaSuccess || a.parts == nullptr) return e;
   return launch_pdl(layer_norm_parts_kernel, dim3(static_cast<unsigned>(ceil_of(2 * static_cast<int64_t>(a.hidden), 32))),
-                    256, 0, 1, stream, a, static_cast<int32_t>(parts));
+                    32 * kPartLanes, 0, 1, stream, a, static_cast<int32_t>(parts));
 }
 
 }  // namespace rd

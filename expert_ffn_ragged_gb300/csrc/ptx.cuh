@@ -138,6 +138,14 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// the two halves of cluster_sync, for work in between that the other CTAs need not wait for
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // arrive on an mbarrier of another CTA of the cluster (release at cluster scope)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)

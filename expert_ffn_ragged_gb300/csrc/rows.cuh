@@ -131,25 +131,42 @@ __device__ __forceinline__ void store4(bf16* p, const float2 (&v)[2]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// N sums over the T threads of a row (T = 32: a warp; else the whole block), in a fixed order, the same
+// in every thread, with one barrier.  The words of `slot` [T / 32][N] may be written again only after the
+// barrier of another call in between.
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* slot) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  return v;
-}
-
-// Sum over the T threads of a row (T = 32: a warp; else the whole block), in a fixed order, the
-// same in every thread.  `slot` alternates between calls: its words may be written again only
-// after the barrier of another call in between.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
-  v = warp_sum(v);
-  if (T == 32) return v;
-  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
+  if (T == 32) return;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) slot[(threadIdx.x >> 5) * N + i] = v[i];
+  }
   __syncthreads();
-  float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < T / 32; ++i) s += slot[i];
-  return s;
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const float4 p = reinterpret_cast<const float4*>(slot)[w * (N / 4) + i];
+        v[4 * i] += p.x, v[4 * i + 1] += p.y, v[4 * i + 2] += p.z, v[4 * i + 3] += p.w;
+      }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 p = reinterpret_cast<const float2*>(slot)[w * (N / 2) + i];
+        v[2 * i] += p.x, v[2 * i + 1] += p.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += slot[w * N + i];
+    }
+  }
 }
 
 }  // namespace rd

@@ -96,7 +96,7 @@ rd_status rd_linear(const void* x, const void* w, const float* bias, const void*
  *   d_out [m, n] of `out_dtype`, pre [m, n] bf16 (NULL with RD_ACT_NONE), d_pre [m, n] bf16, d_bias [g_local, n].
  *   No atomics: the same result on every run.
  *   workspace  device scratch of rd_linear_act_bwd_workspace_size bytes, 32-byte aligned; may be NULL
- *              when d_bias is.  Its contents before and after do not matter.
+ *              when d_bias is or that size is 0.  Its contents before and after do not matter.
  * Requires n % 8 == 0.
  */
 rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, const void* pre, int32_t act,
@@ -105,7 +105,7 @@ rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, const void* pr
                             int32_t g_local, const int32_t* limit, void* workspace,
                             size_t workspace_bytes, int32_t* status, rd_stream_t stream);
 
-/* The workspace of rd_linear_act_bwd on the current device. */
+/* The workspace of rd_linear_act_bwd; 0 where it needs none (few rows over many groups). */
 rd_status rd_linear_act_bwd_workspace_size(int64_t m, int64_t n, int32_t g_local, size_t* bytes);
 
 /*

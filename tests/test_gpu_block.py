@@ -393,6 +393,8 @@ def test_act_bwd(rd_lib, kind, ot, m, n):
     ([0, 0, 0], 0, None, None),
     ([643, 0], 0, 2, 0),
     ([1] * 300 + [0] * 300 + [1] * 43, 100, 520, None),
+    ([3] * 200, 20, 170, 500),
+    ([0, 643] + [0] * 400, 1, 350, None),
 ])
 def test_act_bwd_by_expert(rd_lib, m, sizes, off, gl, limit):
     _check_act_bwd(rd_lib, m, 136, block.SILU, "bf16", sizes, off, gl, limit)
