@@ -201,60 +201,63 @@ __global__ void __launch_bounds__(kActThreads, kActBlocks) linear_act_bwd_kernel
     if (threadIdx.x == 0) head[0] = rows;
     for (int j = threadIdx.x; j <= a.g_local; j += kActThreads) head[1 + j] = bound[j];
   }
-  const int32_t share = static_cast<int32_t>(blockIdx.x / col_blocks);
-  const int64_t col0 = static_cast<int64_t>(blockIdx.x - share * col_blocks) * (W * 8);
-  int32_t r, end;
-  int j = 0;
-  if (whole) {
-    // share: a local group, or the rows before or after them
-    j = share < a.g_local ? share : 0;
-    r = share < a.g_local ? bound[j] : (share == a.g_local ? 0 : zero_hi);
-    end = share < a.g_local ? bound[j + 1] : (share == a.g_local ? zero_lo : L);
-    if (share < a.g_local && r == end && a.d_bias != nullptr)
-      for (int c = threadIdx.x; c < W * 8; c += kActThreads)
-        if (col0 + c < n) a.d_bias[j * n + col0 + c] = 0.0f;
-  } else {
-    const int64_t from = static_cast<int64_t>(share) * rows;
-    if (from >= L) return;
-    r = static_cast<int32_t>(from);
-    end = L - r > rows ? r + rows : L;
-    // the last group that starts at or before r: it has rows, where r is in a group
-    for (int top = a.g_local; top - j > 1;) {
-      const int mid = (j + top) >> 1;
-      if (bound[mid] <= r) j = mid; else top = mid;
+  const int64_t units = static_cast<int64_t>(whole ? a.g_local + 2 : a.shares) * col_blocks;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int32_t share = static_cast<int32_t>(u / col_blocks);
+    const int64_t col0 = (u - static_cast<int64_t>(share) * col_blocks) * (W * 8);
+    int32_t r, end;
+    int j = 0;
+    if (whole) {
+      // share: a local group, or the rows before or after them
+      j = share < a.g_local ? share : 0;
+      r = share < a.g_local ? bound[j] : (share == a.g_local ? 0 : zero_hi);
+      end = share < a.g_local ? bound[j + 1] : (share == a.g_local ? zero_lo : L);
+      if (share < a.g_local && r == end && a.d_bias != nullptr)
+        for (int c = threadIdx.x; c < W * 8; c += kActThreads)
+          if (col0 + c < n) a.d_bias[j * n + col0 + c] = 0.0f;
+    } else {
+      const int64_t from = static_cast<int64_t>(share) * rows;
+      if (from >= L) continue;
+      r = static_cast<int32_t>(from);
+      end = L - r > rows ? r + rows : L;
+      // the last group that starts at or before r: it has rows, where r is in a group
+      for (int top = a.g_local; top - j > 1;) {
+        const int mid = (j + top) >> 1;
+        if (bound[mid] <= r) j = mid; else top = mid;
+      }
     }
-  }
-  while (r < end) {
-    if (r < zero_lo || r >= zero_hi) {
-      const int32_t hi = r < zero_lo && zero_lo < end ? zero_lo : end;
-      const int64_t col = col0 + col_lane * 8;
-      if (a.d_pre != nullptr && col < n)
-        for (int64_t row = r + static_cast<int64_t>(row_lane); row < hi; row += kLanes)
-          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.d_pre) + row * n + col) = make_uint4(0, 0, 0, 0);
+    while (r < end) {
+      if (r < zero_lo || r >= zero_hi) {
+        const int32_t hi = r < zero_lo && zero_lo < end ? zero_lo : end;
+        const int64_t col = col0 + col_lane * 8;
+        if (a.d_pre != nullptr && col < n)
+          for (int64_t row = r + static_cast<int64_t>(row_lane); row < hi; row += kLanes)
+            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.d_pre) + row * n + col) = make_uint4(0, 0, 0, 0);
+        r = hi;
+        continue;
+      }
+      while (bound[j + 1] <= r) ++j;
+      const int32_t hi = bound[j + 1] < end ? bound[j + 1] : end;
+      float2 sum[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
+      act_bwd_rows<D, ACT, W>(a, r, hi, col0, ring, sum);
       r = hi;
-      continue;
-    }
-    while (bound[j + 1] <= r) ++j;
-    const int32_t hi = bound[j + 1] < end ? bound[j + 1] : end;
-    float2 sum[4];
+      if (a.d_bias == nullptr) continue;
+      __syncthreads();  // the sums of the rows before have been read
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
-    act_bwd_rows<D, ACT, W>(a, r, hi, col0, ring, sum);
-    r = hi;
-    if (a.d_bias == nullptr) continue;
-    __syncthreads();  // the sums of the rows before have been read
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float2*>(&across[row_lane][col_lane * 8 + 2 * e]) = sum[e];
+      __syncthreads();
+      float* part = whole ? a.d_bias + j * n + col0
+                          : a.parts + kPartsAt / 4 + (static_cast<int64_t>(share) + j) * n + col0;
+      for (int c = threadIdx.x; c < W * 8; c += kActThreads) {
+        if (col0 + c >= n) continue;
+        float s = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<float2*>(&across[row_lane][col_lane * 8 + 2 * e]) = sum[e];
-    __syncthreads();
-    float* part = whole ? a.d_bias + j * n + col0
-                        : a.parts + kPartsAt / 4 + (static_cast<int64_t>(share) + j) * n + col0;
-    for (int c = threadIdx.x; c < W * 8; c += kActThreads) {
-      if (col0 + c >= n) continue;
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLanes; ++i) s += across[i][c];
-      part[c] = s;
+        for (int i = 0; i < kLanes; ++i) s += across[i][c];
+        part[c] = s;
+      }
     }
   }
 }
@@ -311,17 +314,18 @@ cudaError_t go(ActBwdArgs a, cudaStream_t stream) {
   const cudaError_t e = allow_smem(linear_act_bwd_kernel<D, ACT, W>, smem, set, &dev);
   if (e != cudaSuccess) return e;
   const int32_t col_blocks = ceil_div(a.n, W * 8);
-  int64_t blocks = a.g_local + 2;
+  // a whole group a turn, on as many blocks as run at once (each finds the boundaries once), or a share a block
+  int64_t blocks = static_cast<int64_t>(a.g_local + 2) * col_blocks;
+  if (blocks > kActSlots) blocks = kActSlots;
   a.shares = 0;
   if (!whole_groups(a.m, a.n, a.g_local)) {
     a.shares = kActSlots / col_blocks;
     const int32_t most = ceil_div(a.m, kActLeastRows);
     if (a.shares > most) a.shares = most;
     if (a.shares < 1) a.shares = 1;
-    blocks = a.shares;
+    blocks = static_cast<int64_t>(a.shares) * col_blocks;
   }
-  return launch_pdl(linear_act_bwd_kernel<D, ACT, W>, dim3(static_cast<unsigned>(blocks * col_blocks)), kActThreads, smem, 1,
-                    stream, a);
+  return launch_pdl(linear_act_bwd_kernel<D, ACT, W>, dim3(static_cast<unsigned>(blocks)), kActThreads, smem, 1, stream, a);
 }
 
 template <class D, int ACT>
