@@ -207,7 +207,11 @@ bool use_split(int sms, int64_t m, int64_t n) { return 2 * square_tiles(m, n) <=
 //   m x n     256 x 4096  4096 x 256  64 x 4096 (k = 14336)  1 x 14336  128 x 14336  512 x 4096  2048 x 1024  256 x 14336
 //   tiles     64          64          32                     112        112          128         128          224
 //             17 / 20     17 / 20     25 / 29                24 / 23    31 / 29      24 / 23     25 / 23      53 / 39
-int split_cols(int sms, int64_t m, int64_t n) { return 3 * square_tiles(m, n) >= 2 * static_cast<int64_t>(sms) ? 128 : 64; }
+// An f32 output of 128 columns holds a row's sums in so many registers that its CTA has the SM for itself.
+int split_cols(int sms, int64_t m, int64_t n, bool f32) {
+  const int64_t tiles = square_tiles(m, n);
+  return 3 * tiles >= 2 * static_cast<int64_t>(sms) && (!f32 || tiles <= sms) ? 128 : 64;
+}
 
 // Where tiles of 128 columns are two thirds of the SMs and no more than all, each has an SM and a deep ring for
 // itself (us against two CTAs a tile on half the ring, k = 4096: 1 x 14336 21.6 / 22.2, 96 x 14336 25.8 / 27.4, 16381 x 128
@@ -254,8 +258,8 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
   if (m == 0 || n == 0) return RD_OK;
 
   if (group_sizes == nullptr && use_split(sms, m, n)) {
-    const int cols = split_cols(sms, m, n);
-    const int64_t tiles = (m + kSplitRows - 1) / kSplitRows * ((n + cols - 1) / cols);
+    const int cols = split_cols(sms, m, n, out_dtype == RD_F32);
+    const int64_t col_tiles = (n + cols - 1) / cols, tiles = (m + kSplitRows - 1) / kSplitRows * col_tiles;
     SplitArgs s = {};
     s.bias = bias;
     s.residual = residual;

@@ -18,7 +18,7 @@ struct SplitArgs {
   int32_t k;
   int32_t n;
   int32_t act;
-  int32_t box_rows;       // rows of x that a box brings (multiple of 8, at most 128)
+  int32_t box_rows;       // rows of an output tile and of x's boxes (multiple of 8, at most kSplitRows)
   int32_t stages;
   int32_t ring_bytes;     // of shared memory for the stages: kSplitRing or kSplitRingAlone
   int32_t cluster;        // CTAs that share one output tile's k
@@ -26,7 +26,7 @@ struct SplitArgs {
 };
 
 constexpr int kSplitMaxStages = 12;
-constexpr int kSplitRows = 128;    // rows of an output tile
+constexpr int kSplitRows = 128;    // rows of an MMA, and most rows of an output tile
 // rings that leave room for two CTAs on an SM, and for one
 constexpr int kSplitRing = 108 * 1024;
 constexpr int kSplitRingAlone = 216 * 1024;

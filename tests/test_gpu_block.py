@@ -267,6 +267,24 @@ def test_linear_few_rows(rd_lib, m, k, n):
     _check_linear(rd_lib, m, k, n, kind, residual=m % 2 == 0, pre=m % 3 == 0, ot="f32" if m % 4 == 1 else "bf16")
 
 
+def test_linear_f32_output_is_as_exact_as_f32(rd_lib):
+    """Router logits: the tensor core cuts its sums off (by less than an ulp, 2^-23) at each of 32 steps, then a
+    rounded sum takes over, whatever k is: at most 32 ulp of the result's norm."""
+    for m, k, n in ((300, 8192, 136), (2500, 4096, 128), (9, 16384, 72), (130, 4096, 14336)):
+        rng = np.random.default_rng(m)
+        x, w = _rows(rng, (m, k), "bf16"), _rows(rng, (k, n), "bf16", 1 / math.sqrt(k))
+        got = rd_lib.linear(x.to(DEV), w.to(DEV), out_dtype=torch.float32)
+        ref = x.to(DEV).double() @ w.to(DEV).double()
+        assert float((got.double() - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23, (m, k, n)
+
+
+@pytest.mark.parametrize("m,k,n", [(16381, 72, 128), (2047, 136, 1000), (19000, 64, 64), (700, 200, 2000)])
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+def test_linear_low_tiles(rd_lib, m, k, n, ot):
+    """Tiles cut lower than the MMA so that every SM has one."""
+    _check_linear(rd_lib, m, k, n, block.GELU, residual=True, pre=True, ot=ot, limit=m - 5)
+
+
 @pytest.mark.parametrize("kind", block.ACTS)
 @pytest.mark.parametrize("ot", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n", [(5, 1000), (100, 264), (3000, 520)])
