@@ -24,6 +24,7 @@ struct NormArgs {
   const int32_t* limit;
   int32_t rows;
   int32_t hidden;
+  int32_t split;         // backward: blocks that share a row too long for one (set by the launcher)
   float eps;
 };
 

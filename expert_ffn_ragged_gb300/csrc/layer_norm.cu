@@ -7,6 +7,13 @@
 // weight and bias stay in registers, and the backward pass adds its columns' d_out * y and d_out there.
 // At the end the blocks of a cluster add their two sums a column through distributed shared memory, in their
 // order, and write one part a cluster to the workspace; a second kernel adds the parts in theirs (no atomics).
+// Rows of the backward pass too long for one block's registers (past 8192) are shared by a cluster, whose blocks send
+// each other the row's two sums; past 65536 the row is read twice and the columns are summed by a kernel of their own.
+//
+// Bound: HBM.  28157 x 4096, f32 stream, bf16 in the products: forward 692 MB in 106 us (6.5 TB/s), gradients 1.15 GB in
+// 175 us (6.6 TB/s, the second kernel's 3 us among them).  bf16 throughout the gradients take 121 us (5.7 TB/s): issue
+// slots, 22 packed operations for four elements.  One row takes 2.0 us, 509 rows' gradients 10.8 us (two launches, each some 4 us
+// from its start to its first result).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -205,6 +212,18 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
 // ------------------------------------------------------------------ backward
 constexpr int kNormCluster = 2;  // blocks that add their sums before they go to the workspace
 
+constexpr int kNormMaxSplit = 8;  // blocks that share a row too long for one
+constexpr uint64_t kNormWaitNs = 4000000000ull;  // bound of the wait for their sums
+
+// two sums to the same words of another block of the cluster, counted on its barrier there (no fence: a release at
+// cluster scope would wait for the row's global stores too)
+__device__ __forceinline__ void put_peer(float2* local, uint64_t* bar, int rank, float x, float y) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   ptx::map_to_rank(ptx::smem_addr(local), static_cast<uint32_t>(rank))),
+               "f"(x), "f"(y), "r"(ptx::map_to_rank(ptx::smem_addr(bar), static_cast<uint32_t>(rank)))
+               : "memory");
+}
+
 __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -214,7 +233,8 @@ __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
   return v;
 }
 
-template <class X, class O, int T, int V, int R, int S, int B>
+// SPLIT: a cluster holds a row, each block kCols of its columns; the row's two sums cross the cluster
+template <class X, class O, int T, int V, int R, int S, int B, bool SPLIT>
 __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(const NormArgs a) {
   constexpr int kThreads = Shape<T>::kThreads, kGroups = Shape<T>::kGroups;
   constexpr int kCols = T * V * 4;
@@ -222,20 +242,38 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
   using RawO = typename Quad<O>::Raw;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float pairs[2][32 * 2 * R];
+  __shared__ float2 joined[2][kNormMaxSplit][R];  // SPLIT: the sums of the cluster's blocks
+  __shared__ uint64_t joined_full[2];
+  __shared__ int gave_up;
+  static_assert(!SPLIT || T != 32, "a block's threads share their rows");
+  if (SPLIT) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_addr(&joined_full[i]), 1);
+      gave_up = 0;
+      ptx::fence_mbar_init();
+    }
+    ptx::cluster_sync();  // every block of the cluster runs and its barriers are ready
+  }
   pdl_trigger();
   pdl_wait();
+  const int split = SPLIT ? a.split : 1;
+  const int rank = SPLIT ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int64_t col0 = SPLIT ? static_cast<int64_t>(rank) * kCols : 0;  // of this block
   RawX* ring_x = reinterpret_cast<RawX*>(smem) + threadIdx.x;
   RawO* ring_d = reinterpret_cast<RawO*>(smem + S * R * V * kThreads * sizeof(RawX)) + threadIdx.x;
   const int t = threadIdx.x % T;
-  const int quads = a.hidden >> 2;
+  const int quads = static_cast<int>((a.hidden - col0) >> 2);  // from col0 on
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups * R;
+  const int blocks = SPLIT ? gridDim.x / split : gridDim.x;  // (clusters)
+  const int block = SPLIT ? blockIdx.x / split : blockIdx.x;
+  const int64_t step = static_cast<int64_t>(blocks) * kGroups * R;
   const float inv = 1.0f / static_cast<float>(a.hidden);
-  const X* x = static_cast<const X*>(a.x) + 4 * t;
-  const O* d_out = static_cast<const O*>(a.d_out) + 4 * t;
-  X* d_x = static_cast<X*>(a.out) + 4 * t;
-  int64_t row = (static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / T) * R;
+  const X* x = static_cast<const X*>(a.x) + col0 + 4 * t;
+  const O* d_out = static_cast<const O*>(a.d_out) + col0 + 4 * t;
+  X* d_x = static_cast<X*>(a.out) + col0 + 4 * t;
+  const float* weight = a.weight == nullptr ? nullptr : a.weight + col0;
+  int64_t row = (static_cast<int64_t>(block) * kGroups + threadIdx.x / T) * R;
   auto fetch = [&](int64_t first, int s) {
 #pragma unroll
     for (int j = 0; j < R; ++j)
@@ -256,8 +294,8 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
   for (int i = 0; i < V; ++i) {
     w[i][0] = w[i][1] = both(1.0f);
     dw[i][0] = dw[i][1] = db[i][0] = db[i][1] = both(0.0f);
-    if (a.weight != nullptr && t + i * T < quads)
-      widen(*reinterpret_cast<const float4*>(a.weight + 4 * (t + i * T)), w[i]);
+    if (weight != nullptr && t + i * T < quads)
+      widen(*reinterpret_cast<const float4*>(weight + 4 * (t + i * T)), w[i]);
   }
   float mean_next[R], rstd_next[R];
   auto stats = [&](int64_t first) {
@@ -271,6 +309,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     }
   };
   stats(row);
+  uint32_t joined_phase = 0;  // a bit a slot
   int stage = 0, slot = 0;
   for (; row < L; row += step) {
     fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
@@ -309,6 +348,28 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     }
     if (++stage == S) stage = 0;
     row_sums<T>(pq, pairs[slot]);
+    if (SPLIT) {
+      // Every block's sums to every block.  A slot's words are written again two turns on, by blocks that have this
+      // block's sums of the turn in between, which it sends after it has read the slot.
+      const uint32_t bar = ptx::smem_addr(&joined_full[slot]);
+      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, split * R * 8);
+      if (threadIdx.x < split) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+          put_peer(&joined[slot][rank][j], &joined_full[slot], static_cast<int>(threadIdx.x), pq[2 * j], pq[2 * j + 1]);
+      }
+      const bool there = ptx::mbar_wait_bounded(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWaitNs);
+      joined_phase ^= 1u << slot;
+#pragma unroll
+      for (int j = 0; j < 2 * R; ++j) pq[j] = 0.0f;
+      for (int i = 0; i < split; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          pq[2 * j] += joined[slot][i][j].x;
+          pq[2 * j + 1] += joined[slot][i][j].y;
+        }
+      if (!there) pq[0] = __int_as_float(0x7FC00000);  // a block of the cluster never came: the row shows it
+    }
     slot ^= 1;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -324,6 +385,18 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
         }
     }
   }
+  if (SPLIT) {
+    // (a block leaves when it has all blocks' sums of the last turn: nothing more is written to it)
+    if (a.parts == nullptr) return;
+    float* part = a.parts + static_cast<int64_t>(block) * 2 * hidden + col0 + 4 * t;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (t + i * T < quads) {
+        store4(part + 4 * i * T, dw[i]);
+        store4(part + hidden + 4 * i * T, db[i]);
+      }
+    return;
+  }
   if (a.parts == nullptr) return;  // the same in every block
   // the ring's place is taken by this block's sums: [rows of the block][d_weight, d_bias][columns]
   copies_wait<0>();
@@ -336,9 +409,9 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     store4(at + kCols, db[i]);
   }
   ptx::cluster_sync();
-  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const int peer = static_cast<int>(ptx::cluster_ctarank());
   float* part = a.parts + static_cast<int64_t>(blockIdx.x / kNormCluster) * 2 * hidden;
-  for (int u = rank * kThreads + threadIdx.x; u < kCols / 2; u += kNormCluster * kThreads) {
+  for (int u = peer * kThreads + threadIdx.x; u < kCols / 2; u += kNormCluster * kThreads) {
     const int k = u / (kCols / 4), quad = u - k * (kCols / 4);
     if (quad >= quads) continue;
     float2 s[2] = {both(0.0f), both(0.0f)};
@@ -523,55 +596,63 @@ cudaError_t fwd_by_width(const NormArgs& a, int sms, cudaStream_t stream) {
                     1024, 0, 1, stream, a);
 }
 
-// the backward kernel that holds rows in registers: rows that a block takes at a time and blocks on an
-// SM; 0: rows are too long for it
+// the backward kernel that holds rows in registers: rows that a block takes at a time, blocks on an SM and
+// blocks that share a row; 0: rows are too long for it
 struct BwdShape {
-  int rows, blocks;
+  int rows, blocks, split;
 };
 BwdShape bwd_shape(int64_t hidden) {
-  if (hidden <= 256) return {8, 3};
-  if (hidden <= 1024) return {2, 4};
-  if (hidden <= 2048) return {2, 2};
-  if (hidden <= 4096) return {1, 2};
-  if (hidden <= 8192) return {1, 1};
-  return {0, 0};
+  if (hidden <= 256) return {8, 3, 1};
+  if (hidden <= 1024) return {2, 4, 1};
+  if (hidden <= 2048) return {2, 2, 1};
+  if (hidden <= 4096) return {1, 2, 1};
+  if (hidden <= 8192) return {1, 1, 1};
+  if (hidden <= 4096 * kNormMaxSplit) return {2, 1, static_cast<int>(ceil_of(hidden, 4096))};
+  if (hidden <= 8192 * kNormMaxSplit) return {1, 1, static_cast<int>(ceil_of(hidden, 8192))};
+  return {0, 0, 1};
 }
 
-template <class X, class O, int T, int V, int R, int B>
+template <class X, class O, int T, int V, int R, int B, bool SPLIT = false>
 cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
-  constexpr int S = 2;
+  constexpr int S = SPLIT ? 3 : 2;
   constexpr size_t ring = static_cast<size_t>(S) * R * V * Shape<T>::kThreads *
                           (sizeof(typename Quad<X>::Raw) + sizeof(typename Quad<O>::Raw));
   constexpr size_t sums = static_cast<size_t>(Shape<T>::kGroups) * 2 * T * V * 4 * 4;
   constexpr size_t smem = ring > sums ? ring : sums;
-  auto* kernel = layer_norm_bwd_kernel<X, O, T, V, R, S, B>;
+  auto* kernel = layer_norm_bwd_kernel<X, O, T, V, R, S, B, SPLIT>;
+  const int cluster = SPLIT ? a.split : kNormCluster;
   static std::atomic<bool> set[64];
-  static std::atomic<int> resident[64];  // clusters on the device at once
+  static std::atomic<int> known[64][kNormMaxSplit + 1];  // clusters on the device at once, by their size
   int dev = 0;
   cudaError_t e = allow_smem(kernel, smem, set, &dev);
   if (e != cudaSuccess) return e;
-  int clusters = resident[dev].load(std::memory_order_acquire);
+  std::atomic<int>& resident = known[dev][cluster];
+  int clusters = resident.load(std::memory_order_acquire);
   if (clusters == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kNormCluster, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster), 1, 1);
     cfg.blockDim = dim3(Shape<T>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kNormCluster;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (clusters < 1) clusters = 1;
-    resident[dev].store(clusters, std::memory_order_release);
+    resident.store(clusters, std::memory_order_release);
   }
   if (clusters < *parts) *parts = clusters;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(*parts * kNormCluster)), Shape<T>::kThreads, smem, kNormCluster,
-                    stream, a);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(*parts * cluster)), Shape<T>::kThreads, smem, cluster, stream, a);
 }
 
+// GB/s with f32 rows and bf16 d_out / bf16 both, other forms in brackets:
+//   256: - / 5110 (two rows at a time 3360);  1024: - / 5820 (64 threads x 4 quads 4650);  2048: - / 5670
+//   4096: 6580 / 5710 (512 threads x 2 quads, two rows at a time: 6410 / 5070; one row: 5420 / 4350);  8192: 6530 / -
+//   12288: - / 3630, 16384: 5570 / -, 32768: - / 3050 (a row read twice by one block instead of shared by a cluster:
+//   1970, 2970, 2200)
 template <class X, class O>
 cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t stream) {
   // (rows at a time and blocks as bwd_shape has them)
@@ -580,6 +661,13 @@ cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t st
   if (a.hidden <= 2048) return bwd<X, O, 256, 2, 2, 2>(a, parts, stream);
   if (a.hidden <= 4096) return bwd<X, O, 256, 4, 1, 2>(a, parts, stream);
   if (a.hidden <= 8192) return bwd<X, O, 512, 4, 1, 1>(a, parts, stream);
+  const int split = bwd_shape(a.hidden).split;
+  if (split > 1) {
+    NormArgs shared = a;
+    shared.split = split;
+    return a.hidden <= 4096 * kNormMaxSplit ? bwd<X, O, 512, 2, 2, 1, true>(shared, parts, stream)
+                                            : bwd<X, O, 512, 4, 1, 1, true>(shared, parts, stream);
+  }
   const int64_t most = 2 * static_cast<int64_t>(sms);
   if (a.rows > 0) {
     const cudaError_t e = launch_pdl(layer_norm_dx_long_kernel<X, O>,
@@ -611,8 +699,9 @@ int layer_norm_bwd_parts(int64_t rows, int64_t hidden, int sms) {
     p = ceil_of(rows, 64);
     most = 64;
   } else {
-    p = ceil_of(rows, kNormCluster * shape.rows);
-    most = ceil_of(static_cast<int64_t>(sms) * shape.blocks, kNormCluster);
+    const int cluster = shape.split > 1 ? shape.split : kNormCluster;
+    p = ceil_of(rows, shape.split > 1 ? shape.rows : kNormCluster * shape.rows);
+    most = ceil_of(static_cast<int64_t>(sms) * shape.blocks, cluster);
   }
   return static_cast<int>(p < 1 ? 1 : (p < most ? p : most));
 }

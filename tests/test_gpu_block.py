@@ -173,26 +173,27 @@ def _check_norm_bwd(rd, rows, hidden, dt, ot, weight=True, limit=None, need=(Tru
         assert_close(_f64(d_b), ref_b, (L + 64) * U * np.abs(d64).sum(0), "d_bias")
 
 
-@pytest.mark.parametrize("hidden", [8, 64, 248, 256, 264, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 20000])
+@pytest.mark.parametrize("hidden", [8, 64, 248, 256, 264, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384, 16392,
+                                    20000, 32776, 65536, 65544])
 @pytest.mark.parametrize("dt,ot", [("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 def test_norm_bwd(rd_lib, hidden, dt, ot):
     _check_norm_bwd(rd_lib, 37, hidden, dt, ot)
 
 
 @pytest.mark.parametrize("rows", [0, 1, 3, 8, 9, 600, 3001])
-@pytest.mark.parametrize("hidden", [64, 1032, 4096])
+@pytest.mark.parametrize("hidden", [64, 1032, 4096, 12000])
 def test_norm_bwd_rows(rd_lib, rows, hidden):
     _check_norm_bwd(rd_lib, rows, hidden, "bf16", "bf16")
 
 
 @pytest.mark.parametrize("limit", [-1, 0, 1, 20, 33, 50])
-@pytest.mark.parametrize("hidden", [248, 4096, 9000])
+@pytest.mark.parametrize("hidden", [248, 4096, 9000, 70000])
 def test_norm_bwd_limit(rd_lib, limit, hidden):
     _check_norm_bwd(rd_lib, 33, hidden, "f32", "bf16", limit=limit)
 
 
 @pytest.mark.parametrize("need", [(True, False), (False, True), (False, False)])
-@pytest.mark.parametrize("hidden", [64, 2048, 9000])
+@pytest.mark.parametrize("hidden", [64, 2048, 9000, 70000])
 def test_norm_bwd_parts_left_out(rd_lib, need, hidden):
     _check_norm_bwd(rd_lib, 21, hidden, "bf16", "f32", weight=False, need=need)
 
