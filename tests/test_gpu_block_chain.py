@@ -1,6 +1,9 @@
-"""A whole feed-forward block made of the library's calls: norm, router, experts beside a dense feed-forward,
-dropout onto an f32 residual stream; a training step against automatic differentiation in 64 bits, and
-its forward from a CUDA graph."""
+"""The block of examples/feed_forward_block.py (norm, router, experts beside a dense feed-forward, dropout onto
+an f32 residual stream): a training step against automatic differentiation in 64 bits, its forward from a
+CUDA graph, one decoding token."""
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 
@@ -10,66 +13,23 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TOKENS, HIDDEN, EXPERTS, TOPK, INNER, DENSE = 40, 64, 8, 2, 32, 96
 P = 0.25
 WORDS = (41, 1 << 40)
 
 
-def _params(seed):
-    g = torch.Generator().manual_seed(seed)
-
-    def n(*shape, std=1.0, shift=0.0):
-        return torch.randn(*shape, generator=g, dtype=torch.float64) * std + shift
-
-    p = dict(x=n(TOKENS, HIDDEN, shift=0.2), gain=n(HIDDEN, std=0.1, shift=1.0), shift=n(HIDDEN, std=0.1),
-             wr=n(HIDDEN, EXPERTS, std=HIDDEN ** -0.5), br=n(EXPERTS, std=0.1),
-             up=n(EXPERTS, HIDDEN, 2 * INNER, std=HIDDEN ** -0.5), down=n(EXPERTS, INNER, HIDDEN, std=INNER ** -0.5),
-             w1=n(HIDDEN, DENSE, std=HIDDEN ** -0.5), b1=n(DENSE, std=0.1),
-             w2=n(DENSE, HIDDEN, std=DENSE ** -0.5), b2=n(HIDDEN, std=0.1))
-    f32 = ("x", "gain", "shift", "br", "b1", "b2")
-    return {k: (v.float() if k in f32 else v.to(torch.bfloat16)) for k, v in p.items()}
+@pytest.fixture(scope="module")
+def example(rd_lib):
+    path = os.path.join(ROOT, "examples", "feed_forward_block.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
 
 
-def _forward(rd, p, words):
-    norm = rd.layer_norm_fwd(p["x"], p["gain"], p["shift"], out_dtype=torch.bfloat16)
-    logits = rd.linear(norm.out, p["wr"], p["br"], out_dtype=torch.float32)
-    r = rd.route(logits, TOPK)
-    packed = rd.dispatch_rows(norm.out, r.pos)
-    fused = rd.ragged_dot(packed, p["up"], r.group_sizes)
-    h = rd.glu_fwd(fused)
-    y = rd.ragged_dot(h, p["down"], r.group_sizes)
-    mixed = rd.combine_rows(y, r.pos, r.weights)
-    u, pre = rd.linear(norm.out, p["w1"], p["b1"], act=rd.ACT_GELU, save_pre=True)
-    both = rd.linear(u, p["w2"], p["b2"], residual=mixed)
-    out = rd.dropout_rows(both, words, P, residual=p["x"])
-    return out, (norm, logits, r, packed, fused, h, y, u, pre)
-
-
-def _backward(rd, p, words, saved, d_out):
-    norm, logits, r, packed, fused, h, y, u, pre = saved
-    sizes = torch.tensor([TOKENS], dtype=torch.int32, device=DEV)     # one weight as one group
-
-    def through(d, x, w):
-        """(dx, dw) of a product with one weight."""
-        return rd.ragged_dot_trans_rhs(d, w.unsqueeze(0), sizes), rd.trans_ragged_dot(x, d, sizes)[0]
-
-    d_both = rd.dropout_rows(d_out, words, P, out_dtype=torch.bfloat16)
-    _, d_b2 = rd.linear_act_bwd(d_both, None, rd.ACT_NONE, need_pre=False)
-    d_u, d_w2 = through(d_both, u, p["w2"])
-    d_pre, d_b1 = rd.linear_act_bwd(d_u, pre, rd.ACT_GELU)
-    d_n1, d_w1 = through(d_pre, norm.out, p["w1"])
-    d_y, d_weights = rd.combine_rows_bwd(d_both, y, r.pos, r.weights)
-    d_fused = rd.ragged_dot_trans_rhs_glu_bwd(d_y, p["down"], fused, r.group_sizes)
-    d_down = rd.trans_ragged_dot(h, d_y, r.group_sizes)
-    d_up = rd.trans_ragged_dot(packed, d_fused, r.group_sizes)
-    d_n2 = rd.combine_rows(rd.ragged_dot_trans_rhs(d_fused, p["up"], r.group_sizes), r.pos)
-    d_logits = rd.route_bwd(logits, r.ids, d_weights)
-    d_l, d_br = rd.linear_act_bwd(d_logits, None, rd.ACT_NONE)
-    d_n3, d_wr = through(d_l, norm.out, p["wr"])
-    d_norm = (d_n1.float() + d_n2.float() + d_n3.float())
-    d_x, d_gain, d_shift = rd.layer_norm_bwd(d_norm, p["x"], p["gain"], norm.mean, norm.rstd)
-    return dict(x=d_x + d_out, gain=d_gain, shift=d_shift, wr=d_wr, br=d_br, up=d_up, down=d_down, w1=d_w1, b1=d_b1,
-                w2=d_w2, b2=d_b2)
+def _block(example, seed, device=DEV):
+    return example.make_block(TOKENS, EXPERTS, HIDDEN, INNER, DENSE, seed=seed, device=device)
 
 
 def _forward64(p, ids, kept):
@@ -93,13 +53,13 @@ def _forward64(p, ids, kept):
     return torch.where(kept, both * (65536 / (65536 - least)), torch.zeros_like(both)) + x
 
 
-def test_training_step(rd_lib):
-    params = _params(1)
+def test_training_step(example):
+    params = _block(example, 1, "cpu")
     p = {k: v.to(DEV) for k, v in params.items()}
     words = torch.tensor(WORDS, device=DEV)
-    out, saved = _forward(rd_lib, p, words)
+    out, saved = example.forward(p, TOPK, words, P)
     d_out = torch.randn(TOKENS, HIDDEN, generator=torch.Generator().manual_seed(2))
-    grads = _backward(rd_lib, p, words, saved, d_out.to(DEV))
+    grads = example.backward(d_out.to(DEV), saved, p, words, P)
 
     ids = saved[2].ids.long().cpu()
     kept = torch.from_numpy(oblock.dropout(np.ones((TOKENS, HIDDEN)), *WORDS, P)[1])
@@ -122,9 +82,9 @@ def test_training_step(rd_lib):
         assert abs(float(((got - want) * way).sum())) <= 5 * noise + 2.0 ** -6 * abs(float((want * way).sum())), name
 
 
-def test_gradients_against_differences(rd_lib):
+def test_gradients_against_differences(example):
     """The gradients of the 64-bit block are those of its differences, so that the test above means what it says."""
-    p = {k: v.double() for k, v in _params(3).items()}
+    p = {k: v.double() for k, v in _block(example, 3, "cpu").items()}
     ids = torch.randint(0, EXPERTS, (TOKENS, TOPK), generator=torch.Generator().manual_seed(4))
     kept = torch.from_numpy(oblock.dropout(np.ones((TOKENS, HIDDEN)), *WORDS, P)[1])
     d = torch.randn(TOKENS, HIDDEN, generator=torch.Generator().manual_seed(5), dtype=torch.float64)
@@ -140,29 +100,29 @@ def test_gradients_against_differences(rd_lib):
         assert abs(got - want) <= 1e-6 * (1 + abs(want)), name
 
 
-def test_forward_from_a_graph(rd_lib):
+def test_forward_from_a_graph(example):
     """One capture, replayed with other tokens and other words of the generator: the eager call's bits."""
-    p = {k: v.to(DEV) for k, v in _params(7).items()}
+    p = _block(example, 7)
     words = torch.tensor(WORDS, device=DEV)
-    _forward(rd_lib, p, words)
+    example.forward(p, TOPK, words, P)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        captured, _ = _forward(rd_lib, p, words)
+        captured, _ = example.forward(p, TOPK, words, P)
     seen = []
     for i in range(3):
-        p["x"].copy_(_params(20 + i)["x"])
+        p["x"].copy_(_block(example, 20 + i)["x"])
         words.add_(1)
         graph.replay()
         got = captured.clone()
-        assert torch.equal(got, _forward(rd_lib, p, words)[0])
+        assert torch.equal(got, example.forward(p, TOPK, words, P)[0])
         seen.append(got)
     assert not torch.equal(seen[0], seen[1])
 
 
-def test_one_decoding_token(rd_lib):
+def test_one_decoding_token(example, rd_lib):
     """A single token through the dense part, as a decoding step calls it."""
-    p = _params(9)
-    dev = {k: v.to(DEV) for k, v in p.items()}
+    dev = _block(example, 9)
+    p = {k: v.cpu() for k, v in dev.items()}
     x = dev["x"][:1].contiguous()
     n = rd_lib.layer_norm_fwd(x, dev["gain"], dev["shift"], out_dtype=torch.bfloat16, stats=False)
     assert n.mean is None and n.rstd is None
@@ -174,3 +134,29 @@ def test_one_decoding_token(rd_lib):
     want = oblock.act(z, oblock.GELU) @ p64["w2"].numpy() + p64["b2"].numpy() + p64["x"][:1].numpy()
     # two bf16 roundings on the way (norm, activation), each 2^-8 of values that add up in quadrature
     assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0 ** -5 * max(1.0, np.abs(want).max())
+
+
+def test_example_runs(example):
+    assert torch.isfinite(example.main([])).all()
+
+
+def test_first_calls_inside_a_capture(rd_lib):
+    """Widths and types that no call has had yet: kernel attributes are set while the stream is captured."""
+    x = torch.randn(5, 136, device=DEV)
+    y = torch.randn(5, 6008, device=DEV, dtype=torch.bfloat16)
+    for v in (x, y):                                   # the entry points themselves have been called before
+        f = rd_lib.layer_norm_fwd(torch.ones(2, 64, device=DEV))
+        rd_lib.layer_norm_bwd(torch.ones(2, 64, device=DEV), torch.ones(2, 64, device=DEV), None, f.mean, f.rstd)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = []
+        for v in (x, y):
+            f = rd_lib.layer_norm_fwd(v)
+            got += [f.out, *rd_lib.layer_norm_bwd(v, v, None, f.mean, f.rstd)]
+    graph.replay()
+    torch.cuda.synchronize()
+    want = []
+    for v in (x, y):
+        f = rd_lib.layer_norm_fwd(v)
+        want += [f.out, *rd_lib.layer_norm_bwd(v, v, None, f.mean, f.rstd)]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
