@@ -24,8 +24,13 @@ namespace {
 
 constexpr int kActThreads = 256;
 constexpr int kActStages = 3;                 // rows of a thread in its ring
-constexpr int kActBlocks = 3;                 // blocks on an SM
-constexpr int kActSlots = 152 * kActBlocks;   // blocks that run at once
+// blocks on an SM: with two streams in and one out, three of them have more on their way than is good (16384 x 14336, us
+// three / two: gelu 239 / 227, tanh form 239 / 220; without an activation 147 / 166)
+template <int ACT>
+constexpr int kActBlocks = ACT == RD_ACT_NONE ? 3 : 2;
+template <int ACT>
+constexpr int kActSlots = 152 * kActBlocks<ACT>;  // blocks that run at once
+constexpr int kActMostSlots = kActSlots<RD_ACT_NONE>;
 constexpr int kActLeastRows = 16;             // rows of a share
 // the workspace before the sums: rows of a share, then the local groups' boundaries
 constexpr int64_t kPartsAt = 4 * (kMaxGroups + 8);
@@ -179,7 +184,7 @@ __device__ __forceinline__ void act_bwd_rows(const ActBwdArgs& a, int32_t lo, in
 
 // W: vectors of columns of a block
 template <class D, int ACT, int W>
-__global__ void __launch_bounds__(kActThreads, kActBlocks) linear_act_bwd_kernel(const ActBwdArgs a) {
+__global__ void __launch_bounds__(kActThreads, kActBlocks<ACT>) linear_act_bwd_kernel(const ActBwdArgs a) {
   constexpr int kLanes = kActThreads / W;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ Bounds sh;
@@ -316,10 +321,10 @@ cudaError_t go(ActBwdArgs a, cudaStream_t stream) {
   const int32_t col_blocks = ceil_div(a.n, W * 8);
   // a whole group a turn, on as many blocks as run at once (each finds the boundaries once), or a share a block
   int64_t blocks = static_cast<int64_t>(a.g_local + 2) * col_blocks;
-  if (blocks > kActSlots) blocks = kActSlots;
+  if (blocks > kActSlots<ACT>) blocks = kActSlots<ACT>;
   a.shares = 0;
   if (!whole_groups(a.m, a.n, a.g_local)) {
-    a.shares = kActSlots / col_blocks;
+    a.shares = kActSlots<ACT> / col_blocks;
     const int32_t most = ceil_div(a.m, kActLeastRows);
     if (a.shares > most) a.shares = most;
     if (a.shares < 1) a.shares = 1;
@@ -343,11 +348,11 @@ cudaError_t by_width(const ActBwdArgs& a, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-// room for the sums of every share and group (no more shares than go() makes)
+// room for the sums of every share and group (no more shares than go() makes: its widths, and the most slots)
 int64_t linear_act_bwd_bytes(int64_t m, int64_t n, int32_t g_local) {
   if (whole_groups(m, n, g_local)) return 0;
   const int64_t width = n <= 64 ? 64 : (n <= 128 ? 128 : 256);
-  int64_t shares = kActSlots / ((n + width - 1) / width > 0 ? (n + width - 1) / width : 1);
+  int64_t shares = kActMostSlots / ((n + width - 1) / width > 0 ? (n + width - 1) / width : 1);
   const int64_t most = (m + kActLeastRows - 1) / kActLeastRows;
   if (shares > most) shares = most;
   if (shares < 1) shares = 1;
