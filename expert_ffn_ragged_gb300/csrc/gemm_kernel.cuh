@@ -40,6 +40,11 @@
 //     stores only the rows it owns.  dw uses the same shift on its row (K)
 //     blocks, skips whole 16-row K steps before the group and has warp 10
 //     zero, in shared memory, the rows of the straddling step (NaN-safe);
+//   * rd_linear's epilogues (kEpiLinear, kEpiLinearF32) add the bias, keep the rows before the activation,
+//     apply it and add the residual, all in f32 on the accumulator.  An f32 output is kept as exact as a rounded f32 sum:
+//     the tensor core cuts its sums off after every step of 16 along k (4.3e-6 of the result's norm at k = 4096), so
+//     the two accumulators take turns every 512 of k and 16 epilogue warps add the complete one to sums in
+//     registers (4.7e-7; 16384 x 4096 x 4096: 362 us against 289 for bf16, which rounds far coarser anyway);
 //   * every wait is bounded; on expiry the CTA unwinds, drains its TMA and
 //     MMA work, frees TMEM and reports RD_STATUS_TIMEOUT.
 #pragma once
@@ -63,9 +68,13 @@ namespace rd {
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr uint64_t kGraceNs = 200000ull;
 
-template <bool PAIR>
+// FINE: f32 outputs whose sums the epilogue takes over every kFineBlocks K blocks (kEpiLinearF32): 16 epilogue warps
+// with 64 sums a thread, and one stage less for their staging.
+template <bool PAIR, bool FINE = false>
 struct TileCfg {
-  static constexpr int kStagesN = PAIR ? 6 : 4;
+  static constexpr int kStagesN = (PAIR ? 6 : 4) - (FINE ? 1 : 0);
+  static constexpr int kEpiWarpsN = FINE ? 16 : kEpiWarps;
+  static constexpr int kThreadsN = FINE ? 32 * (2 + 16 + 1) : kThreads;
   static constexpr int kTileM = PAIR ? 2 * kBM : kBM;   // rows of one (pair) tile
   static constexpr int kBCols = PAIR ? kBN / 2 : kBN;   // B columns held by one CTA
   static constexpr int kStageA = kBM * kBK * 2;         // 16 KB
@@ -73,9 +82,11 @@ struct TileCfg {
   static constexpr int kStageBytes = kStageA + kStageB;
 };
 
-template <bool PAIR>
+constexpr int kFineBlocks = 8;
+
+template <bool PAIR, bool FINE = false>
 struct alignas(128) GemmShared {
-  static constexpr int S = TileCfg<PAIR>::kStagesN;
+  static constexpr int S = TileCfg<PAIR, FINE>::kStagesN;
   uint64_t full[S];
   uint64_t empty[S];
   uint64_t efull[S];   // dw: this CTA's copy of an edge block landed (edge fills only)
@@ -92,14 +103,14 @@ struct alignas(128) GemmShared {
   int32_t fills;      // stages the producer has filled so far (paces the zero fill)
   int32_t bound[kMaxGroups + 1];       // group boundaries, clamped to L
   int32_t tile_start[kMaxGroups + 1];  // fwd/dx: first tile of each local group; dw: group order
-  uint4 epi[kEpiWarps][32 * 4];        // epilogue staging per warp: 32 rows x 64 bytes
+  uint4 epi[TileCfg<PAIR, FINE>::kEpiWarpsN][32 * 4];  // epilogue staging per warp: 32 rows x 64 bytes
   uint4 zeros[256];                    // 4 KB zero block, the source of the zero-fill copies
 };
 
-template <bool PAIR>
+template <bool PAIR, bool FINE>
 constexpr size_t gemm_smem_bytes_t() {
-  return 1024 + static_cast<size_t>(TileCfg<PAIR>::kStagesN) * TileCfg<PAIR>::kStageBytes +
-         sizeof(GemmShared<PAIR>);
+  return 1024 + static_cast<size_t>(TileCfg<PAIR, FINE>::kStagesN) * TileCfg<PAIR, FINE>::kStageBytes +
+         sizeof(GemmShared<PAIR, FINE>);
 }
 
 // Exclusive prefix of a per-lane chunk sum across one warp.
@@ -199,8 +210,8 @@ __device__ __forceinline__ void build_schedule(Shared& sh, const Args& a, int la
   }
 }
 
-template <int OP, bool PAIR>
-__device__ __forceinline__ Tile decode_tile(const GemmShared<PAIR>& sh, const GemmArgs& a, int t) {
+template <int OP, bool PAIR, class Shared>
+__device__ __forceinline__ Tile decode_tile(const Shared& sh, const GemmArgs& a, int t) {
   SchedView v;
   v.bound = sh.bound;
   v.tile_start = sh.tile_start;
@@ -300,7 +311,7 @@ __device__ __forceinline__ void stage_boxes(const Tile& tl, int kb, uint32_t ran
 }
 
 template <int OP, int EPI, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         const __grid_constant__ CUtensorMap tmap_b, const GemmArgs args) {
   constexpr bool GLU = (EPI == kEpiGlu);
@@ -309,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool F32OUT = (EPI == kEpiF32 || EPI == kEpiF32Acc);
   constexpr bool LINEAR = (EPI == kEpiLinear || EPI == kEpiLinearF32);
   static_assert(!LINEAR || OP == kOpFwd, "bias, activation and residual follow the forward product");
-  using Cfg = TileCfg<PAIR>;
+  constexpr bool FINE = (EPI == kEpiLinearF32);
+  using Cfg = TileCfg<PAIR, FINE>;
+  constexpr int kEpiWarpsN = Cfg::kEpiWarpsN;
   constexpr int S = Cfg::kStagesN;
   constexpr int TM = Cfg::kTileM;
 
@@ -318,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + S * Cfg::kStageA;
-  GemmShared<PAIR>& sh = *reinterpret_cast<GemmShared<PAIR>*>(smem + S * Cfg::kStageBytes);
+  using Shared = GemmShared<PAIR, FINE>;
+  Shared& sh = *reinterpret_cast<Shared*>(smem + S * Cfg::kStageBytes);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_addr(&sh.tfull[b]), 1);
-      ptx::mbar_init(ptx::smem_addr(&sh.tempty[b]), PAIR ? 2 * kEpiWarps : kEpiWarps);
+      ptx::mbar_init(ptx::smem_addr(&sh.tempty[b]), PAIR ? 2 * kEpiWarpsN : kEpiWarpsN);
     }
     ptx::mbar_init(ptx::smem_addr(&sh.drain), 1);
     sh.abort_flag = 0;
@@ -480,12 +494,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = decode_tile<OP, PAIR>(sh, args, t);
         if (tl.nkb == 0) continue;
-        ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag,
-                                    tlimit);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t d_tmem = sh.tmem_base + static_cast<uint32_t>(acc * kBN);
+        if (!FINE) {
+          ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag,
+                                      tlimit);
+          if (!ok) break;
+          ptx::tc_fence_after();
+        }
+        uint32_t d_tmem = sh.tmem_base + static_cast<uint32_t>(acc * kBN);
         for (int kb = 0; kb < tl.nkb; ++kb) {
+          // FINE: an accumulator for every kFineBlocks K blocks
+          const int kb_acc = FINE ? kb % kFineBlocks : kb;
+          if (FINE && kb_acc == 0) {
+            ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tempty[acc]), acc_phase ^ 1, abort_flag, tlimit);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            d_tmem = sh.tmem_base + static_cast<uint32_t>(acc * kBN);
+          }
           int kk0 = 0;  // first 16-deep K step issued for this block
           bool edge = false;
           if (OP == kOpDw) {
@@ -535,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every block but a dw group's straddling last one: four MMAs back to
             // back (with a skip test in front of each, dw's issue took ~1.3x as long)
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) mma(ad[kk], bd[kk], (kb > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kBK / 16; ++kk) mma(ad[kk], bd[kk], (kb_acc > 0 || kk > 0) ? 1u : 0u);
           } else {
 #pragma unroll 1
             for (int kk = kk0; kk < kBK / 16; ++kk)
@@ -544,8 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.empty[stage]), 0x3);
           else ptx::tc_commit(ptx::smem_addr(&sh.empty[stage]));
           if (++stage == S) stage = 0;
+          if (FINE && (kb_acc == kFineBlocks - 1 || kb == tl.nkb - 1)) {
+            if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.tfull[acc]), 0x3);
+            else ptx::tc_commit(ptx::smem_addr(&sh.tfull[acc]));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+          }
         }
         if (!ok) break;
+        if (FINE) continue;
         if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.tfull[acc]), 0x3);
         else ptx::tc_commit(ptx::smem_addr(&sh.tfull[acc]));
         acc ^= 1;
@@ -560,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp < 2 + kEpiWarpsN) {
     // ------------------------------------------------------------ epilogue
     // Eight warps, two per 32-lane quarter of the accumulator (32 tile rows);
     // the two split the tile's 32-column chunks.  A chunk is read from TMEM
@@ -569,10 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stored 8 rows x 64 contiguous bytes per instruction.
     const int e = warp - 2;
     const int q = warp & 3;      // TMEM lane quarter this warp may access
-    const int half = e >> 2;     // which half of the chunks
+    const int half = e >> 2;     // which half (of FINE, quarter) of the chunks
     constexpr int tile_w = GLU ? kBN / 2 : kBN;
     constexpr int kChunks = tile_w / 32;
-    const int c_begin = half * (kChunks / 2), c_end = c_begin + kChunks / 2;
+    constexpr int kShares = kEpiWarpsN / 4;  // of the chunks, one for each warp of a lane quarter
+    const int c_begin = half * (kChunks / kShares), c_end = c_begin + kChunks / kShares;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(args.out);
     uint4* stg = sh.epi[e];
     const uint32_t tempty_leader =
@@ -660,32 +692,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (LINEAR) {
         // bias, activation and residual on the f32 sums, of which nothing has been rounded yet; a thread
         // holds a row, so a bias value is one broadcast load and a row's residual 64 or 128 bytes
-        bool ok = true;
-        if (tl.nkb > 0) {
-          ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          ptx::tc_fence_after();
-        }
-        const uint32_t tb =
-            sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kBN);
         const float* bias = args.bias == nullptr
                                 ? nullptr
                                 : args.bias + static_cast<size_t>(tl.j) * args.n_out;
         const int row = wrow0 + lane;
         const bool row_ok = row >= lo && row < hi;
         const size_t row_at = static_cast<size_t>(row_ok ? row : 0) * args.ldo;
-#pragma unroll 1
-        for (int c = c_begin; c < c_end; ++c) {
-          const int col = col0 + c * 32;
-          if (col >= args.n_out) break;
-          uint32_t v[32];
-          if (tl.nkb > 0) {
-            ptx::tmem_load_32cols(tb + c * 32, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-          }
+        auto finish = [&](uint32_t (&v)[32], int col) {
           if (bias != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -706,12 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           with_act(args.act, [&](auto tag) {
             constexpr int kAct = decltype(tag)::value;
-            if (kAct == RD_ACT_NONE) return;
+            if constexpr (kAct != RD_ACT_NONE) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 r = act_value<kAct>(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-              v[i] = __float_as_uint(r.x);
-              v[i + 1] = __float_as_uint(r.y);
+              for (int i = 0; i < 32; i += 2) {
+                const float2 r = act_value<kAct>(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                v[i] = __float_as_uint(r.x);
+                v[i + 1] = __float_as_uint(r.y);
+              }
             }
           });
           if (args.residual != nullptr && row_ok) {
@@ -750,18 +764,80 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
             emit(p, col, 0);
           }
+        };
+        if constexpr (FINE) {
+          // two chunks of 32 columns a thread; the sums of every kFineBlocks K blocks are added with rounding
+          uint32_t v[2][32];
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i / 32][i % 32] = 0u;
+          const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
+          bool ok = true;
+          for (int kb = 0; kb < tl.nkb && ok; kb += kFineBlocks) {
+            ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t from = sh.tmem_base + quarter + static_cast<uint32_t>(acc * kBN + c_begin * 32);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t r[16];
+              ptx::tmem_load_16cols(from + c * 16, r);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                uint32_t& d = v[c / 2][(c % 2) * 16 + i];
+                d = __float_as_uint(__uint_as_float(d) + __uint_as_float(r[i]));
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (PAIR && rank != 0)
+                ptx::mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+              else
+                ptx::mbar_arrive(ptx::smem_addr(&sh.tempty[acc]));
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (col0 + (c_begin + c) * 32 < args.n_out) finish(v[c], col0 + (c_begin + c) * 32);
+        } else {
+          if (tl.nkb > 0) {
+            bool ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[acc]), acc_phase, abort_flag, tlimit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
+          const uint32_t tb =
+              sh.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kBN);
+#pragma unroll 1
+          for (int c = c_begin; c < c_end; ++c) {
+            const int col = col0 + c * 32;
+            if (col >= args.n_out) break;
+            uint32_t v[32];
+            if (tl.nkb > 0) {
+              ptx::tmem_load_32cols(tb + c * 32, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            finish(v, col);
+          }
+          if (tl.nkb > 0) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (PAIR && rank != 0)
+                ptx::mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+              else
+                ptx::mbar_arrive(ptx::smem_addr(&sh.tempty[acc]));
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+          }
         }
-        if (tl.nkb == 0) continue;
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR && rank != 0)
-            ptx::mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * sizeof(uint64_t)));
-          else
-            ptx::mbar_arrive(ptx::smem_addr(&sh.tempty[acc]));
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
         continue;
       }
       if (tl.nkb == 0) {
@@ -883,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-  } else if (OP == kOpDw && warp == 2 + kEpiWarps) {
+  } else if (OP == kOpDw && warp == 2 + kEpiWarpsN) {
     // ------------------------------------------------------------ dw edge rows
     // For each edge block (the last K block of a group, whose first rows precede
     // the group), wait for this CTA's own copy, zero the rows of the straddling
@@ -918,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == S) stage = 0;
       }
     }
-  } else if (OP != kOpDw && warp == 2 + kEpiWarps) {
+  } else if (OP != kOpDw && warp == 2 + kEpiWarpsN) {
     // ------------------------------------------------------------ zero fill
     // Rows [0, zero_lo) and [zero_hi, L) are two contiguous byte ranges of the
     // output (its rows are contiguous).  Each CTA takes a contiguous 16-byte
@@ -1018,7 +1094,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int OP, int EPI, bool PAIR>
 cudaError_t launch_gemm_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b,
                              const GemmArgs& args, int grid, cudaStream_t stream) {
-  constexpr size_t smem = gemm_smem_bytes_t<PAIR>();
+  constexpr size_t smem = gemm_smem_bytes_t<PAIR, EPI == kEpiLinearF32>();
+  constexpr int threads = TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN;
   // the shared-memory size attribute is set once per device (it is per-device
   // state); two threads racing here both set it, which is harmless
   static std::atomic<bool> attr_set[64];
@@ -1032,11 +1109,11 @@ cudaError_t launch_gemm_impl(const CUtensorMap& tmap_a, const CUtensorMap& tmap_
     attr_set[dev].store(true, std::memory_order_release);
   }
   if (!PAIR) {
-    grouped_gemm_kernel<OP, EPI, PAIR><<<grid, kThreads, smem, stream>>>(tmap_a, tmap_b, args);
+    grouped_gemm_kernel<OP, EPI, PAIR><<<grid, threads, smem, stream>>>(tmap_a, tmap_b, args);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

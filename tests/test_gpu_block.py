@@ -270,13 +270,17 @@ def test_linear_few_rows(rd_lib, m, k, n):
 
 def test_linear_f32_output_is_as_exact_as_f32(rd_lib):
     """Router logits: the tensor core cuts its sums off (by less than an ulp, 2^-23) at each of 32 steps, then a
-    rounded sum takes over, whatever k is: at most 32 ulp of the result's norm."""
-    for m, k, n in ((300, 8192, 136), (2500, 4096, 128), (9, 16384, 72), (130, 4096, 14336)):
+    rounded sum takes over, whatever k is: at most 32 ulp of the result's norm.  On few tiles and on many."""
+    for m, k, n in ((300, 8192, 136), (2500, 4096, 128), (9, 16384, 72), (130, 4096, 14336), (3000, 8192, 2056)):
         rng = np.random.default_rng(m)
         x, w = _rows(rng, (m, k), "bf16"), _rows(rng, (k, n), "bf16", 1 / math.sqrt(k))
         got = rd_lib.linear(x.to(DEV), w.to(DEV), out_dtype=torch.float32)
         ref = x.to(DEV).double() @ w.to(DEV).double()
         assert float((got.double() - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23, (m, k, n)
+        for v in (rd_lib.VARIANT_SINGLE, rd_lib.VARIANT_PAIR):
+            with rd_lib.tuning(variant=v):
+                one = rd_lib.linear(x.to(DEV), w.to(DEV).unsqueeze(0), group_sizes=_i32([m]), out_dtype=torch.float32)
+            assert float((one.double() - ref).norm() / ref.norm()) <= 32 * 2.0 ** -23, (m, k, n, v)
 
 
 @pytest.mark.parametrize("m,k,n", [(16381, 72, 128), (2047, 136, 1000), (19000, 64, 64), (700, 200, 2000)])
@@ -629,8 +633,9 @@ def test_binding_refusals(rd_lib):
 
 
 # ---------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("ot", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("which", ["split", "single", "pair"])
-def test_timeout_unwinds_and_reports(rd_lib, which):
+def test_timeout_unwinds_and_reports(rd_lib, which, ot):
     """With a bound of 1 ns every wait that its first tries (of a microsecond each) do not end gives up: the
     call reports it and the next one is right.  The waits of the kernel for few tiles are shorter than the
     tries when nothing else runs, so there a call that reports nothing has to be right itself."""
@@ -638,7 +643,7 @@ def test_timeout_unwinds_and_reports(rd_lib, which):
     m, k, n = (40, 16384, 512) if which == "split" else (1024, 8192, 512)
     x, w = _rows(rng, (m, k), "bf16").to(DEV), _rows(rng, (k, n), "bf16", 1 / math.sqrt(k)).to(DEV)
     status = _i32([0])
-    args = dict(act=block.SILU, status=status)
+    args = dict(act=block.SILU, status=status, out_dtype=ot)
     if which != "split":
         w, args["group_sizes"] = w.unsqueeze(0), _i32([m])
     v = rd_lib.VARIANT_PAIR if which == "pair" else rd_lib.VARIANT_SINGLE
