@@ -78,7 +78,8 @@ rd_status rd_layer_norm_bwd_workspace_size(int64_t rows, int64_t hidden, size_t*
  *   x [m, k], w, pre [m, n] bf16; bias f32 or NULL; out and residual (or NULL) [m, n] of `out_dtype`.
  * Accuracy: the products are exact and summed in f32 by the tensor cores, which cut the sum off at every 16 of k;
  * an f32 output adds up stretches of 512 of k with rounding (some 5e-7 of the output's norm, whatever k is).
- * Activations are within 4e-6 of their value, relatively, for arguments down to -13 (gelu) or -87.
+ * Activations are within 4e-6 + 5e-7 |u| of their value, relatively, u the argument of their exponential (z^2 / 2,
+ * 2 sqrt(2 / pi) (z + 0.044715 z^3) or z); values below 1e-37 may be 0.
  * Its gradients: rd_linear_act_bwd gives d_pre and d_bias; dx is rd_ragged_dot_trans_rhs(d_pre, w),
  * dw is rd_trans_ragged_dot(x, d_pre) (one weight: with group_sizes a word that holds m), and the
  * residual's gradient is d_out.
