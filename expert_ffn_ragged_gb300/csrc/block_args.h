@@ -25,6 +25,7 @@ struct NormArgs {
   int32_t rows;
   int32_t hidden;
   int32_t split;         // backward: blocks that share a row too long for one (set by the launcher)
+  int32_t split_cols;    // and the columns of each but the last
   float eps;
 };
 

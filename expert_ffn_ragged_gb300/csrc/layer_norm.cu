@@ -233,7 +233,7 @@ __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
   return v;
 }
 
-// SPLIT: a cluster holds a row, each block kCols of its columns; the row's two sums cross the cluster
+// SPLIT: a cluster holds a row, each block split_cols (at most kCols) of its columns; the row's two sums cross the cluster
 template <class X, class O, int T, int V, int R, int S, int B, bool SPLIT>
 __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(const NormArgs a) {
   constexpr int kThreads = Shape<T>::kThreads, kGroups = Shape<T>::kGroups;
@@ -258,11 +258,12 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
   pdl_wait();
   const int split = SPLIT ? a.split : 1;
   const int rank = SPLIT ? static_cast<int>(ptx::cluster_ctarank()) : 0;
-  const int64_t col0 = SPLIT ? static_cast<int64_t>(rank) * kCols : 0;  // of this block
+  const int64_t col0 = SPLIT ? static_cast<int64_t>(rank) * a.split_cols : 0;  // of this block
   RawX* ring_x = reinterpret_cast<RawX*>(smem) + threadIdx.x;
   RawO* ring_d = reinterpret_cast<RawO*>(smem + S * R * V * kThreads * sizeof(RawX)) + threadIdx.x;
   const int t = threadIdx.x % T;
-  const int quads = static_cast<int>((a.hidden - col0) >> 2);  // from col0 on
+  const int64_t cols = SPLIT && a.hidden - col0 > a.split_cols ? a.split_cols : a.hidden - col0;
+  const int quads = static_cast<int>(cols >> 2);
   const int64_t hidden = a.hidden;
   const int32_t L = rows_within(a.limit, a.rows);
   const int blocks = SPLIT ? gridDim.x / split : gridDim.x;  // (clusters)
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
   };
   stats(row);
   uint32_t joined_phase = 0;  // a bit a slot
+  bool there = true;  // SPLIT: no wait has run out
   int stage = 0, slot = 0;
   for (; row < L; row += step) {
     fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
@@ -352,13 +354,13 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
       // Every block's sums to every block.  A slot's words are written again two turns on, by blocks that have this
       // block's sums of the turn in between, which it sends after it has read the slot.
       const uint32_t bar = ptx::smem_addr(&joined_full[slot]);
-      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, split * R * 8);
+      if (threadIdx.x == 0 && there) ptx::mbar_arrive_expect_tx(bar, split * R * 8);
       if (threadIdx.x < split) {
 #pragma unroll
         for (int j = 0; j < R; ++j)
           put_peer(&joined[slot][rank][j], &joined_full[slot], static_cast<int>(threadIdx.x), pq[2 * j], pq[2 * j + 1]);
       }
-      const bool there = ptx::mbar_wait_bounded(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWaitNs);
+      there = ptx::mbar_wait_bounded_cluster(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWaitNs) && there;
       joined_phase ^= 1u << slot;
 #pragma unroll
       for (int j = 0; j < 2 * R; ++j) pq[j] = 0.0f;
@@ -368,7 +370,11 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
           pq[2 * j] += joined[slot][i][j].x;
           pq[2 * j + 1] += joined[slot][i][j].y;
         }
-      if (!there) pq[0] = __int_as_float(0x7FC00000);  // a block of the cluster never came: the row shows it
+      if (!there) {
+        // a block of the cluster never came: this row and the ones after it show it
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j) pq[j] = __int_as_float(0x7FC00000);
+      }
     }
     slot ^= 1;
 #pragma unroll
@@ -386,7 +392,8 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     }
   }
   if (SPLIT) {
-    // (a block leaves when it has all blocks' sums of the last turn: nothing more is written to it)
+    // a block has all blocks' sums of the last turn by now; after a wait that ran out some may still be on their way to it
+    ptx::cluster_sync();
     if (a.parts == nullptr) return;
     float* part = a.parts + static_cast<int64_t>(block) * 2 * hidden + col0 + 4 * t;
 #pragma unroll
@@ -607,8 +614,9 @@ BwdShape bwd_shape(int64_t hidden) {
   if (hidden <= 2048) return {2, 2, 1};
   if (hidden <= 4096) return {1, 2, 1};
   if (hidden <= 8192) return {1, 1, 1};
-  if (hidden <= 4096 * kNormMaxSplit) return {2, 1, static_cast<int>(ceil_of(hidden, 4096))};
-  if (hidden <= 8192 * kNormMaxSplit) return {1, 1, static_cast<int>(ceil_of(hidden, 8192))};
+  // clusters of 2, 4 or 8, which leave few SMs without work (clusters of three took 190 or 277 us for 9385 x 12288, as 46 of
+  // them, the most by the runtime's count, sometimes did not run at once)
+  if (hidden <= 8192 * kNormMaxSplit) return {1, 1, hidden <= 16384 ? 2 : (hidden <= 32768 ? 4 : 8)};
   return {0, 0, 1};
 }
 
@@ -651,8 +659,8 @@ cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
 // GB/s with f32 rows and bf16 d_out / bf16 both, other forms in brackets:
 //   256: - / 5110 (two rows at a time 3360);  1024: - / 5820 (64 threads x 4 quads 4650);  2048: - / 5670
 //   4096: 6580 / 5710 (512 threads x 2 quads, two rows at a time: 6410 / 5070; one row: 5420 / 4350);  8192: 6530 / -
-//   12288: - / 3630, 16384: 5570 / -, 32768: - / 3050 (a row read twice by one block instead of shared by a cluster:
-//   1970, 2970, 2200)
+//   12288: - / 3860, 16384: 6070 / -, 32768: - / 4360 (two rows at a time over twice as many blocks 3630, 5570, 3050; a row
+//   read twice by one block instead of shared by a cluster 1970, 2970, 2200)
 template <class X, class O>
 cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t stream) {
   // (rows at a time and blocks as bwd_shape has them)
@@ -665,8 +673,8 @@ cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t st
   if (split > 1) {
     NormArgs shared = a;
     shared.split = split;
-    return a.hidden <= 4096 * kNormMaxSplit ? bwd<X, O, 512, 2, 2, 1, true>(shared, parts, stream)
-                                            : bwd<X, O, 512, 4, 1, 1, true>(shared, parts, stream);
+    shared.split_cols = static_cast<int32_t>(ceil_of(a.hidden, 64 * split) * 64);  // whole lines
+    return bwd<X, O, 512, 4, 1, 1, true>(shared, parts, stream);
   }
   const int64_t most = 2 * static_cast<int64_t>(sms);
   if (a.rows > 0) {

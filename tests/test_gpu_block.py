@@ -286,7 +286,7 @@ def test_linear_f32_output_is_as_exact_as_f32(rd_lib):
 @pytest.mark.parametrize("m,k,n", [(16381, 72, 128), (2047, 136, 1000), (19000, 64, 64), (700, 200, 2000)])
 @pytest.mark.parametrize("ot", ["bf16", "f32"])
 def test_linear_low_tiles(rd_lib, m, k, n, ot):
-    """Tiles cut lower than the MMA so that every SM has one."""
+    """One weight, tiles for most SMs and for a little more than all."""
     _check_linear(rd_lib, m, k, n, block.GELU, residual=True, pre=True, ot=ot, limit=m - 5)
 
 
@@ -325,6 +325,23 @@ def test_linear_by_expert(rd_lib, variant, ot, sizes, off, gl, limit):
         for i, (kind, residual, pre) in enumerate(((block.GELU, False, True), (block.GELU_TANH, True, False),
                                                    (block.NONE, True, True), (block.RELU, False, False))):
             _check_linear(rd_lib, 643 + 20 * (i % 2), 200, 264 + 32 * i, kind, True, residual, pre, ot, limit, sizes, off, gl)
+
+
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+def test_most_groups(rd_lib, ot):
+    """1024 groups, most of them short and some empty."""
+    sizes = [(7 * i) % 11 for i in range(1024)]
+    sizes[500] = 700
+    _check_linear(rd_lib, 5900, 584, 40, block.GELU, True, True, True, ot, 5800, sizes, 3, 1000)
+    _check_act_bwd(rd_lib, 5900, 72, block.GELU, ot, sizes, 3, 1000, 5800)
+    _check_act_bwd(rd_lib, 2000, 72, block.SILU, ot, [s % 3 for s in sizes], 0, 1024, None)
+
+
+@pytest.mark.parametrize("variant", ["single", "pair"])
+def test_linear_f32_by_expert_of_long_rows(rd_lib, variant):
+    """k of three stretches of f32 sums and a part of one, so that the accumulators' turns go on from tile to tile."""
+    with rd_lib.tuning(variant=rd_lib.VARIANT_PAIR if variant == "pair" else rd_lib.VARIANT_SINGLE):
+        _check_linear(rd_lib, 26000, 1608, 520, block.SILU, True, True, True, "f32", None, [9000, 0, 300, 1, 16600], 0, 4)
 
 
 def test_linear_one_weight_equals_one_group(rd_lib):
@@ -528,10 +545,12 @@ def _calls(rd, g):
     gain, words, limit = n(520, dtype=torch.float32), torch.tensor([5, 6], device=DEV), _i32([250])
     big, wg, bg, sizes = n(2600, 520), n(3, 520, 264), n(3, 264, dtype=torch.float32), _i32([700, 0, 1900])
     d, pre = n(2600, 264), n(2600, 264)
-    f = rd.layer_norm_fwd(x, gain)
+    f, wide = rd.layer_norm_fwd(x, gain), n(90, 20000)
+    fw = rd.layer_norm_fwd(wide)
     return {
         "norm": lambda **kw: rd.layer_norm_fwd(x, gain, gain, out_dtype=torch.float32, **kw),
         "norm_bwd": lambda **kw: rd.layer_norm_bwd(x, x, gain, f.mean, f.rstd, **kw),
+        "norm_bwd_wide": lambda **kw: rd.layer_norm_bwd(wide, wide, None, fw.mean, fw.rstd, **kw),
         "split": lambda **kw: (rd.linear(x, w, b, act=2, **kw),),
         "linear": lambda **kw: rd.linear(big, wg, bg, act=4, group_sizes=sizes, save_pre=True, **kw),
         "act_bwd": lambda **kw: rd.linear_act_bwd(d, pre, 3, group_sizes=sizes, **kw),
