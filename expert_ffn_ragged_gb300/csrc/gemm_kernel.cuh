@@ -44,7 +44,7 @@
 //     apply it and add the residual, all in f32 on the accumulator.  An f32 output is kept as exact as a rounded f32 sum:
 //     the tensor core cuts its sums off after every step of 16 along k (4.3e-6 of the result's norm at k = 4096), so
 //     the two accumulators take turns every 512 of k and 16 epilogue warps add the complete one to sums in
-//     registers (4.7e-7; 16384 x 4096 x 4096: 362 us against 289 for bf16, which rounds far coarser anyway);
+//     registers (4.7e-7; 16384 x 4096 x 4096: 365 us against 287 for bf16, which rounds far coarser anyway);
 //   * every wait is bounded; on expiry the CTA unwinds, drains its TMA and
 //     MMA work, frees TMEM and reports RD_STATUS_TIMEOUT.
 #pragma once
@@ -69,10 +69,11 @@ constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr uint64_t kGraceNs = 200000ull;
 
 // FINE: f32 outputs whose sums the epilogue takes over every kFineBlocks K blocks (kEpiLinearF32): 16 epilogue warps
-// with 64 sums a thread, and one stage less for their staging.
+// with 64 sums a thread, which they store from there, whole sectors at a time: their staging would cost a stage (12000 x 4096
+// x 4096 in 64 groups: 518 us with one, 454 without).
 template <bool PAIR, bool FINE = false>
 struct TileCfg {
-  static constexpr int kStagesN = (PAIR ? 6 : 4) - (FINE ? 1 : 0);
+  static constexpr int kStagesN = PAIR ? 6 : 4;
   static constexpr int kEpiWarpsN = FINE ? 16 : kEpiWarps;
   static constexpr int kThreadsN = FINE ? 32 * (2 + 16 + 1) : kThreads;
   static constexpr int kTileM = PAIR ? 2 * kBM : kBM;   // rows of one (pair) tile
@@ -103,7 +104,7 @@ struct alignas(128) GemmShared {
   int32_t fills;      // stages the producer has filled so far (paces the zero fill)
   int32_t bound[kMaxGroups + 1];       // group boundaries, clamped to L
   int32_t tile_start[kMaxGroups + 1];  // fwd/dx: first tile of each local group; dw: group order
-  uint4 epi[TileCfg<PAIR, FINE>::kEpiWarpsN][32 * 4];  // epilogue staging per warp: 32 rows x 64 bytes
+  uint4 epi[FINE ? 1 : kEpiWarps][32 * 4];  // epilogue staging per warp: 32 rows x 64 bytes
   uint4 zeros[256];                    // 4 KB zero block, the source of the zero-fill copies
 };
 
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
     constexpr int kShares = kEpiWarpsN / 4;  // of the chunks, one for each warp of a lane quarter
     const int c_begin = half * (kChunks / kShares), c_end = c_begin + kChunks / kShares;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(args.out);
-    uint4* stg = sh.epi[e];
+    uint4* stg = sh.epi[FINE ? 0 : e];
     const uint32_t tempty_leader =
         PAIR ? ptx::map_to_rank(ptx::smem_addr(&sh.tempty[0]), 0) : 0u;
     const int sr = lane >> 2;      // row (within 8) this lane stores
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
         }
         __syncwarp();
       };
-      // f32 output (of dw or of a linear product), 16 columns (64 bytes a row) at a time through the same
+      // f32 output of dw, 16 columns (64 bytes a row) at a time through the same
       // staging layout; the accumulating form adds them to what the output holds
       auto emit_f32 = [&](const uint32_t* v16, int col) {
 #pragma unroll
@@ -653,8 +654,8 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
           stg[lane * 4 + (v ^ ((lane >> 1) & 3))] =
               make_uint4(v16[4 * v], v16[4 * v + 1], v16[4 * v + 2], v16[4 * v + 3]);
         __syncwarp();
-        float* outf = reinterpret_cast<float*>(args.out);
-        if (OP == kOpDw) outf += static_cast<size_t>(tl.j) * args.m_out * args.ldo;
+        float* outf = reinterpret_cast<float*>(args.out) +
+                      static_cast<size_t>(tl.j) * args.m_out * args.ldo;
         // the accumulating form reads the prior values of all four rows before it
         // writes any (one read-modify-write after another serialised four HBM
         // round trips)
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
           uint4 val = stg[rl * 4 + (piece ^ ((rl >> 1) & 3))];
           const int row = wrow0 + rl;
           const int c = col + piece * 4;
-          if ((OP == kOpDw || row >= lo) && row < hi && c + 4 <= args.n_out) {
+          if (row < hi && c + 4 <= args.n_out) {
             uint4* dst = reinterpret_cast<uint4*>(outf + static_cast<size_t>(row) * args.ldo + c);
             if (EPI == kEpiF32Acc) {
               const uint4 o = prior[it];
@@ -715,7 +716,15 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               p[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            emit(p, col, 0, reinterpret_cast<__nv_bfloat16*>(args.pre));
+            if constexpr (FINE) {
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(args.pre) + row_at + col;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (row_ok && col + 8 * i + 8 <= args.n_out)
+                  *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+            } else {
+              emit(p, col, 0, reinterpret_cast<__nv_bfloat16*>(args.pre));
+            }
           }
           with_act(args.act, [&](auto tag) {
             constexpr int kAct = decltype(tag)::value;
@@ -756,8 +765,15 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
             }
           }
           if (EPI == kEpiLinearF32) {
-            emit_f32(v, col);
-            emit_f32(v + 16, col + 16);
+            float* dst = reinterpret_cast<float*>(args.out) + row_at + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (row_ok && col + 8 * i + 8 <= args.n_out)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 8 * i), "r"(v[8 * i]),
+                             "r"(v[8 * i + 1]), "r"(v[8 * i + 2]), "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]),
+                             "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
+                             : "memory");
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
