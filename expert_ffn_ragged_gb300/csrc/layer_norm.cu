@@ -12,7 +12,7 @@
 //
 // Bound: HBM.  28157 x 4096, f32 stream, bf16 in the products: forward 692 MB in 106 us (6.5 TB/s), gradients 1.15 GB in
 // 175 us (6.6 TB/s, the second kernel's 3 us among them).  bf16 throughout the gradients take 121 us (5.7 TB/s): issue
-// slots, 22 packed operations for four elements.  One row takes 2.0 us, 509 rows' gradients 10.8 us (two launches, each some 4 us
+// slots, 22 packed operations for four elements.  One row takes 2.0 us, 509 rows' gradients 10.4 us (two launches, each some 4 us
 // from its start to its first result).
 #include <cuda_runtime.h>
 #include <stdint.h>
