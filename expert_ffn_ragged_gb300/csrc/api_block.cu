@@ -221,7 +221,7 @@ int split_cols(int sms, int64_t m, int64_t n, bool f32) {
 bool split_alone(int sms, int cols, int64_t tiles) { return cols == 128 && tiles <= sms; }
 
 int split_cluster(int sms, int cols, int64_t tiles, int64_t k) {
-  if (split_alone(sms, cols, tiles)) return 1;
+  if (cols == 128) return 1;  // tiles for two thirds of the SMs or more
   const int64_t blocks = (k + kBK - 1) / kBK;
   int c = 1;
   while (c < 8 && tiles * c <= sms && blocks >= 8 * c) c *= 2;
