@@ -185,6 +185,11 @@ bool use_pair(int sms, int64_t m, int32_t g_total) {
   return m >= 512 * static_cast<int64_t>(g_total);
 }
 
+bool variant_forced() {
+  const int32_t v = g_variant.load(std::memory_order_relaxed);
+  return v == RD_VARIANT_SINGLE || v == RD_VARIANT_PAIR;
+}
+
 // m-tiles per band of the forward / dx tile order: the band's lhs rows stay in
 // L2 while the band sweeps every output column block.
 int32_t band_tiles(bool pair, int32_t default_rows) {

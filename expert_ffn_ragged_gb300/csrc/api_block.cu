@@ -193,27 +193,52 @@ rd_status check_linear(int64_t m, int64_t k, int64_t n, const int32_t* group_siz
   return n > kMaxWidth ? RD_ERR_UNSUPPORTED : RD_OK;
 }
 
-// Tiles of 128 x 128, by which the two rules below go.
-int64_t square_tiles(int64_t m, int64_t n) { return (m + 127) / 128 * ((n + 127) / 128); }
+// Rows of an output tile of the kernel that splits k.  By group a tile is two to four times as high as the average group.
+int32_t split_rows(int64_t m, bool groups, int32_t g_total) {
+  int64_t rows = kSplitRows;
+  if (groups)
+    while (rows > 8 && rows / 2 * g_total >= 2 * m) rows /= 2;
+  return static_cast<int32_t>(m < rows ? (m + 7) / 8 * 8 : rows);
+}
 
-// One weight: the kernel that splits k over clusters, or the persistent one, whose tiles are twice as wide (and on
+// The most row tiles that there can be: by group, a last tile that is not full for every group with rows.
+int64_t most_row_tiles(int64_t m, int32_t rows, bool groups, int32_t g_local) {
+  return groups ? (m < g_local ? m : g_local) + m / rows : (m + rows - 1) / rows;
+}
+// As many as the rules below reckon with: by group, one each or, of long groups, half a tile that is not full.
+int64_t usual_row_tiles(int64_t m, int32_t rows, bool groups, int32_t g_local) {
+  const int64_t most = most_row_tiles(m, rows, groups, g_local), some = m < g_local ? m : g_local;
+  return groups ? (most - g_local / 2 > some ? most - g_local / 2 : some) : most;
+}
+
+// Few tiles: the kernel that splits k over clusters, or the persistent one, whose tiles are twice as wide (and on
 // CTA pairs twice as high).  At k = 4096, us split / persistent:
 //   m x n     16 x 14336  256 x 14336  512 x 4096  2048 x 1024  16381 x 128  1024 x 4096  16384 x 256
 //   tiles     112         224          128         128          128          256          256
 //             23 / 37     39 / 39      23 / 30     23 / 29      32 / 35      33 / 30      39 / 36
-bool use_split(int sms, int64_t m, int64_t n) { return 2 * square_tiles(m, n) <= 3 * static_cast<int64_t>(sms); }
+// and by group (rows x k x n, groups): 4 x 2960 x 392, 16: 7.4 / 31; 310 x 2912 x 64, 4: 7.1 / 19; 128 x 4096 x 1024, 8: 18 / 35;
+// 8 x 7168 x 2048, 32: 39 / 62; 4096 x 1024 x 256, 16: 12 / 19.
+bool use_split(int sms, int64_t wide) { return 2 * wide <= 3 * static_cast<int64_t>(sms); }
 
-// Its tiles have 128 columns where these are tiles enough for two thirds of the SMs, else 64.  At k = 4096, us 64 / 128:
-//   m x n     256 x 4096  4096 x 256  64 x 4096 (k = 14336)  1 x 14336  128 x 14336  512 x 4096  2048 x 1024  256 x 14336
-//   tiles     64          64          32                     112        112          128         128          224
-//             17 / 20     17 / 20     25 / 29                24 / 23    31 / 29      24 / 23     25 / 23      53 / 39
-// An f32 output of 128 columns holds a row's sums in so many registers that its CTA has the SM for itself.
-int split_cols(int sms, int64_t m, int64_t n, bool f32) {
-  const int64_t tiles = square_tiles(m, n);
-  return 3 * tiles >= 2 * static_cast<int64_t>(sms) && (!f32 || tiles <= sms) ? 128 : 64;
+// By group also where there are many tiles but few rows a group: the weights are the time, and its tiles are half as wide, so that they
+// spread better over the SMs (bf16, us split / persistent: 16 x 4096 x 4096 in 8 groups 36 / 44, 512 x 4096 x 4096 in 8 48 / 52, 256 x
+// 2048 x 1024 in 64 45 / 51, 4096 x 2048 x 1024 in 64 55 / 56, but 1024 x 4096 x 4096 in 8 73 / 70, 8192 x 2048 x 1024 in 64 73 / 65).  Its f32
+// tiles of 64 columns that run in turns are slower (512 x 4096 x 4096 in 8: 59 / 53).
+bool short_groups(int64_t m, int32_t g_total, int32_t out_dtype) {
+  return out_dtype == RD_BF16 && m <= 64 * static_cast<int64_t>(g_total);
 }
 
-// Where tiles of 128 columns are two thirds of the SMs and no more than all, each has an SM and a deep ring for
+// Its tiles have 128 columns where these are tiles enough for more than half of the SMs, else 64 (tiles of 64 then have an SM each or
+// share their k).  At k = 4096, us 64 / 128:
+//   m x n     256 x 4096  4096 x 256  64 x 4096 (k = 14336)  1 x 11264  384 x 4096  11000 x 128  1 x 14336  512 x 4096  256 x 14336
+//   tiles     64          64          32                     88         96          86           112        128         224
+//             17 / 20     17 / 20     25 / 29                21 / 20    24 / 21     27 / 24      24 / 23    24 / 23     53 / 39
+// An f32 output of 128 columns holds a row's sums in so many registers that its CTA has the SM for itself.
+int split_cols(int sms, int64_t wide, bool f32) {
+  return 2 * wide > static_cast<int64_t>(sms) && (!f32 || wide <= sms) ? 128 : 64;
+}
+
+// Where tiles of 128 columns are more than half of the SMs and no more than all, each has an SM and a deep ring for
 // itself (us against two CTAs a tile on half the ring, k = 4096: 1 x 14336 21.6 / 22.2, 96 x 14336 25.8 / 27.4, 16381 x 128
 // 30.6 / 31.9).  Otherwise as many CTAs a tile as still all run at once, two on an SM, with at least four K blocks each
 // (tiles of 64 columns, 256 x 4096: 16.3 on two CTAs a tile, 19.8 alone; 64 x 4096, k = 14336: 23.9 on four, 33 on two
@@ -221,7 +246,7 @@ int split_cols(int sms, int64_t m, int64_t n, bool f32) {
 bool split_alone(int sms, int cols, int64_t tiles) { return cols == 128 && tiles <= sms; }
 
 int split_cluster(int sms, int cols, int64_t tiles, int64_t k) {
-  if (cols == 128) return 1;  // tiles for two thirds of the SMs or more
+  if (cols == 128) return 1;  // tiles for more than half of the SMs
   const int64_t blocks = (k + kBK - 1) / kBK;
   int c = 1;
   while (c < 8 && tiles * c <= sms && blocks >= 8 * c) c *= 2;
@@ -257,21 +282,29 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
   if ((st = current_device(&sms)) != RD_OK) return st;
   if (m == 0 || n == 0) return RD_OK;
 
-  if (group_sizes == nullptr && use_split(sms, m, n)) {
-    const int cols = split_cols(sms, m, n, out_dtype == RD_F32);
-    const int64_t col_tiles = (n + cols - 1) / cols, tiles = (m + kSplitRows - 1) / kSplitRows * col_tiles;
+  const bool groups = group_sizes != nullptr;
+  const int32_t box_rows = split_rows(m, groups, g_total);
+  const int64_t usual = usual_row_tiles(m, box_rows, groups, g_local), wide = usual * ((n + 127) / 128);
+  if (groups ? !variant_forced() && (use_split(sms, wide) || short_groups(m, g_total, out_dtype)) : use_split(sms, wide)) {
+    const int cols = split_cols(sms, wide, out_dtype == RD_F32);
+    const int64_t tiles = usual * ((n + cols - 1) / cols);
     SplitArgs s = {};
     s.bias = bias;
     s.residual = residual;
     s.out = out;
     s.pre = pre;
+    s.group_sizes = group_sizes;
     s.limit = limit;
     s.status = status;
     s.m = static_cast<int32_t>(m);
     s.k = static_cast<int32_t>(k);
     s.n = static_cast<int32_t>(n);
     s.act = act;
-    s.box_rows = static_cast<int32_t>(m < kSplitRows ? (m + 7) / 8 * 8 : kSplitRows);
+    s.g_total = g_total;
+    s.group_offset = group_offset;
+    s.g_local = g_local;
+    s.box_rows = box_rows;
+    s.row_tiles = static_cast<int32_t>(most_row_tiles(m, box_rows, groups, g_local));
     const int stage = s.box_rows * 128 + cols * kBK * 2;
     s.ring_bytes = split_alone(sms, cols, tiles) ? kSplitRingAlone : kSplitRing;
     s.stages = s.ring_bytes / stage < kSplitMaxStages ? s.ring_bytes / stage : kSplitMaxStages;
@@ -282,9 +315,9 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
       const uint64_t dx[2] = {static_cast<uint64_t>(k), um}, sx[1] = {static_cast<uint64_t>(k) * 2};
       const uint32_t bx[2] = {64, static_cast<uint32_t>(s.box_rows)};
       if ((st = encode(&tx, x, 2, dx, sx, bx)) != RD_OK) return st;
-      const uint64_t dw[2] = {un, static_cast<uint64_t>(k)}, sw[1] = {un * 2};
-      const uint32_t bw[2] = {64, kBK};
-      if ((st = encode(&tw, w, 2, dw, sw, bw)) != RD_OK) return st;
+      const uint64_t dw[3] = {un, static_cast<uint64_t>(k), ug}, sw[2] = {un * 2, static_cast<uint64_t>(k) * un * 2};
+      const uint32_t bw[3] = {64, kBK, 1};
+      if ((st = encode(&tw, w, groups ? 3 : 2, dw, sw, bw)) != RD_OK) return st;
     }
     return done(launch_gemm_split(out_dtype == RD_F32, cols, tx, tw, s, cu(stream)));
   }

@@ -1,4 +1,4 @@
-// gemm_split.cu -- rd_linear with one weight and few output tiles: a decoding batch, whose time is the
+// gemm_split.cu -- rd_linear with few output tiles: a decoding batch, of one weight or by expert, whose time is the
 // weights' bytes, or a router's few columns, whose time is the tokens'.
 //
 // The persistent kernel (gemm_kernel.cuh) gives an output tile to one CTA (pair), so with few tiles most SMs
@@ -18,6 +18,9 @@
 // 23.5, 16381 x 4096 x 128, f32: 144 MB in 29.8 (4.8 TB/s).  Without any MMA they take 20.9, 22.6 and 28.1: what is left is the start of
 // the copies, the last tile and, for the last of the three, 128 tiles for 152 SMs; the weights, which every SM reads from L2 there,
 // cost nothing.
+//
+// By group the grid has as many row tiles as the rows can fill; each CTA adds the group sizes up, finds its tile, or none and leaves,
+// and sets its share of the rows outside the local groups to zero.
 //
 // The MMA always has 128 rows; x brings only box_rows of them, and the rest of the operand's rows are whatever
 // lies behind in shared memory: their products land in accumulator rows that nothing reads.
@@ -49,6 +52,8 @@ struct SplitShared {
   uint64_t tempty[2];
   uint32_t tmem_base;
   int32_t abort_flag;
+  // by group: this CTA's tile (group, first row, end of the group's rows) and the rows outside the local groups
+  int32_t group, row0, group_end, zero_lo, zero_hi;
 };
 
 constexpr size_t split_smem(int ring_bytes) { return 1024 + ring_bytes + sizeof(SplitShared); }
@@ -71,7 +76,76 @@ struct IsF32<float> {
   static constexpr bool value = true;
 };
 
-template <class O, int BN, int C>
+// Run by one warp: row tile t of the local groups' tiles in order, box_rows high.
+__device__ __forceinline__ void find_tile(SplitShared& sh, const SplitArgs& a, int32_t L, int t, int lane) {
+  const int G = a.g_total, per = (G + 31) / 32, lo = min(lane * per, G), hi = min(lo + per, G);
+  long long sum = 0;
+  bool neg = false;
+  for (int i = lo; i < hi; ++i) {
+    const int32_t s = a.group_sizes[i];
+    neg |= s < 0;
+    sum += s > 0 ? s : 0;
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  neg = __any_sync(0xFFFFFFFFu, neg);
+  if (lane == 0) sh.group = sh.row0 = sh.group_end = 0;
+  __syncwarp();
+  // once to count this lane's tiles, once to find the one that is wanted
+  int before = 0, tiles = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = incl - sum;
+    int at = before;
+    for (int i = lo; i < hi; ++i) {
+      const int32_t s = a.group_sizes[i], b0 = clamp_boundary(run, L);
+      run += s > 0 ? s : 0;
+      const int32_t b1 = clamp_boundary(run, L), j = i - a.group_offset;
+      if (j < 0 || j >= a.g_local) continue;
+      const int n = ceil_div(b1 - b0, a.box_rows);
+      if (pass == 0) {
+        if (j == 0) sh.zero_lo = b0;
+        if (j == a.g_local - 1) sh.zero_hi = b1;
+      } else if (t >= at && t < at + n) {
+        sh.group = j;
+        sh.row0 = b0 + (t - at) * a.box_rows;
+        sh.group_end = b1;
+      }
+      at += n;
+    }
+    if (pass == 0) {
+      tiles = at;
+      int upto = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      before = upto - tiles;
+    }
+  }
+  if (lane == 0 && a.status != nullptr && blockIdx.x == 0 && blockIdx.y == 0) {
+    const int bits = (neg ? RD_STATUS_NEG_SIZE : 0) | (total > a.m ? RD_STATUS_OVERFLOW : 0);
+    if (bits) atomicOr(a.status, bits);
+  }
+}
+
+// +0 in the rows outside the local groups: 64 threads of every CTA
+__device__ __forceinline__ void zero_rows(const SplitShared& sh, int32_t L, void* out, int64_t row_bytes, int thread) {
+  const int64_t vecs = row_bytes / 16, low = sh.zero_lo * vecs, all = low + (L - sh.zero_hi) * vecs;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * gridDim.y * 64;
+  uint4* p = static_cast<uint4*>(out);
+  for (int64_t v = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 64 + thread; v < all; v += step)
+    p[v < low ? v : v - low + sh.zero_hi * vecs] = make_uint4(0, 0, 0, 0);
+}
+
+// C: CTAs that share a tile's k; G: by group (else one weight for all rows)
+template <class O, int BN, int C, bool G>
 __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 1 : 2)
     gemm_split_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const SplitArgs a) {
@@ -118,10 +192,19 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
   const int rank = static_cast<int>(blockIdx.x) % C;
   const int32_t col0 = static_cast<int32_t>(blockIdx.x) / C * BN;
   const int32_t L = rows_within(a.limit, a.m);
-  const int32_t row0 = static_cast<int32_t>(blockIdx.y) * a.box_rows;
-  const int32_t row_end = L - row0 > a.box_rows ? row0 + a.box_rows : L;  // rows [row0, row_end) are stored
+  int32_t row0 = static_cast<int32_t>(blockIdx.y) * a.box_rows, group_end = L, group = 0;
+  if constexpr (G) {
+    if (warp == 2) find_tile(sh, a, L, static_cast<int>(blockIdx.y), lane);
+    __syncthreads();
+    row0 = sh.row0;
+    group_end = sh.group_end;
+    group = sh.group;
+  }
+  const float* const bias_row = a.bias == nullptr ? nullptr : a.bias + static_cast<int64_t>(group) * a.n;
+  const int32_t row_end = group_end - row0 > a.box_rows ? row0 + a.box_rows : group_end;  // rows [row0, row_end) are stored
   const bool live = row_end > row0;                                       // the same in the whole cluster
-  // the box ends at row_end, so that no row at or past L is read (rows before 0 arrive as zeros)
+  // the box ends at row_end, so that no row at or past L is read (rows before 0 arrive as zeros, rows of the group in front are
+  // not stored)
   const int32_t row_load = row_end - a.box_rows;
   const int nkb = ceil_div(a.k, kBK);
   const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / C);
@@ -138,9 +221,11 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
         if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, a.timeout_ns)) break;
         ptx::mbar_arrive_expect_tx(bar, a_bytes + b_bytes);
 #pragma unroll
-        for (int c = 0; c < BN / 64; ++c)
-          ptx::tma_load_2d(ptx::smem_addr(s_b + stage * b_bytes + c * (kBK * 128)), &tmap_w, bar, col0 + c * 64,
-                           kb * kBK);
+        for (int c = 0; c < BN / 64; ++c) {
+          const uint32_t to = ptx::smem_addr(s_b + stage * b_bytes + c * (kBK * 128));
+          if constexpr (G) ptx::tma_load_3d(to, &tmap_w, bar, col0 + c * 64, kb * kBK, group);
+          else ptx::tma_load_2d(to, &tmap_w, bar, col0 + c * 64, kb * kBK);
+        }
         ptx::tma_load_2d(ptx::smem_addr(s_a + stage * a_bytes), &tmap_x, bar, kb * kBK, row_load);
         ++fills;
         if (++stage == a.stages) {
@@ -199,7 +284,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
     constexpr int kLine = 128 / static_cast<int>(sizeof(O)), kLines = BN / kLine;
     constexpr int kIdle = kFine ? 64 : kSplitThreads - 64;
     const int i0 = static_cast<int>(threadIdx.x) - 64;
-    if (a.bias != nullptr && i0 < BN / 32 && col0 + i0 * 32 < a.n) ptx::prefetch_l2(a.bias + col0 + i0 * 32);
+    if (bias_row != nullptr && i0 < BN / 32 && col0 + i0 * 32 < a.n) ptx::prefetch_l2(bias_row + col0 + i0 * 32);
     if (a.residual != nullptr && i0 < kIdle) {
       for (int i = i0 + rank * kIdle; i < (row_end - row0) * kLines; i += C * kIdle) {
         const int32_t col = col0 + (i % kLines) * kLine;
@@ -207,6 +292,12 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
           ptx::prefetch_l2(static_cast<const O*>(a.residual) + static_cast<int64_t>(row0 + i / kLines) * a.n + col);
       }
     }
+    __syncwarp();
+  }
+  if (G && (warp == 2 || warp == 3)) {
+    const int thread = static_cast<int>(threadIdx.x) - 64;
+    zero_rows(sh, L, a.out, static_cast<int64_t>(a.n) * static_cast<int64_t>(sizeof(O)), thread);
+    if (a.pre != nullptr) zero_rows(sh, L, a.pre, static_cast<int64_t>(a.n) * 2, thread);
     __syncwarp();
   }
   if (kFine && warp >= 4) {
@@ -300,7 +391,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
         const uint32_t at = base + static_cast<uint32_t>(((r + shift) * kPitch + c) * 4);
 #pragma unroll
         for (int s = 1; s < C; ++s) part[i][s - 1] = ld_cluster(ptx::map_to_rank(at, (rank + s) % C));
-        if (a.bias != nullptr) bias[i] = *reinterpret_cast<const float4*>(a.bias + col0 + c);
+        if (bias_row != nullptr) bias[i] = *reinterpret_cast<const float4*>(bias_row + col0 + c);
         if (residual != nullptr)
           res[i] = *reinterpret_cast<const typename Quad<O>::Raw*>(
               residual + static_cast<int64_t>(row0 + r) * a.n + col0 + c);
@@ -324,7 +415,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
           z[0] = add2(z[0], make_float2(part[i][s - 1].x, part[i][s - 1].y));
           z[1] = add2(z[1], make_float2(part[i][s - 1].z, part[i][s - 1].w));
         }
-        if (a.bias != nullptr) {
+        if (bias_row != nullptr) {
           z[0] = add2(z[0], make_float2(bias[i].x, bias[i].y));
           z[1] = add2(z[1], make_float2(bias[i].z, bias[i].w));
         }
@@ -351,40 +442,45 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
   if (threadIdx.x == 0 && !ok && a.status != nullptr) atomicOr(a.status, RD_STATUS_TIMEOUT);
 }
 
-template <class O, int BN, int C>
+template <class O, int BN, int C, bool G>
 cudaError_t go(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_split_kernel<O, BN, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(gemm_split_kernel<O, BN, C, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(split_smem(kSplitRingAlone)));
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
   const dim3 grid(static_cast<unsigned>(ceil_div(a.n, BN)) * static_cast<unsigned>(C),
-                  static_cast<unsigned>(ceil_div(a.m, a.box_rows)));
-  return launch_pdl(gemm_split_kernel<O, BN, C>, grid, kSplitThreads, split_smem(a.ring_bytes), C, stream, tx, tw, a);
+                  static_cast<unsigned>(a.row_tiles));
+  return launch_pdl(gemm_split_kernel<O, BN, C, G>, grid, kSplitThreads, split_smem(a.ring_bytes), C, stream, tx, tw, a);
 }
 
-template <class O, int BN>
+template <class O, int BN, bool G>
 cudaError_t by_cluster(const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
-  if constexpr (BN == 128) return go<O, BN, 1>(tx, tw, a, stream);  // (tiles of 128 columns are enough for the SMs)
+  if constexpr (BN == 128) return go<O, BN, 1, G>(tx, tw, a, stream);  // (tiles of 128 columns are enough for the SMs)
   else switch (a.cluster) {
-    case 8: return go<O, BN, 8>(tx, tw, a, stream);
-    case 4: return go<O, BN, 4>(tx, tw, a, stream);
-    case 2: return go<O, BN, 2>(tx, tw, a, stream);
-    default: return go<O, BN, 1>(tx, tw, a, stream);
+    case 8: return go<O, BN, 8, G>(tx, tw, a, stream);
+    case 4: return go<O, BN, 4, G>(tx, tw, a, stream);
+    case 2: return go<O, BN, 2, G>(tx, tw, a, stream);
+    default: return go<O, BN, 1, G>(tx, tw, a, stream);
   }
+}
+
+template <class O, bool G>
+cudaError_t by_cols(int cols, const CUtensorMap& tx, const CUtensorMap& tw, const SplitArgs& a, cudaStream_t stream) {
+  return cols == 64 ? by_cluster<O, 64, G>(tx, tw, a, stream) : by_cluster<O, 128, G>(tx, tw, a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_split(bool f32_out, int cols, const CUtensorMap& tx, const CUtensorMap& tw,
                               const SplitArgs& a, cudaStream_t stream) {
-  if (f32_out)
-    return cols == 64 ? by_cluster<float, 64>(tx, tw, a, stream) : by_cluster<float, 128>(tx, tw, a, stream);
-  return cols == 64 ? by_cluster<bf16, 64>(tx, tw, a, stream) : by_cluster<bf16, 128>(tx, tw, a, stream);
+  if (a.group_sizes == nullptr)
+    return f32_out ? by_cols<float, false>(cols, tx, tw, a, stream) : by_cols<bf16, false>(cols, tx, tw, a, stream);
+  return f32_out ? by_cols<float, true>(cols, tx, tw, a, stream) : by_cols<bf16, true>(cols, tx, tw, a, stream);
 }
 
 }  // namespace rd

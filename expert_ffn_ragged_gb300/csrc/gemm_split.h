@@ -12,12 +12,17 @@ struct SplitArgs {
   const void* residual;   // [m, n] of the output's type or null
   void* out;              // [m, n] bf16 or f32
   void* pre;              // [m, n] bf16 or null
+  const int32_t* group_sizes;  // or null: one weight
   const int32_t* limit;
   int32_t* status;
   int32_t m;
   int32_t k;
   int32_t n;
   int32_t act;
+  int32_t g_total;        // (with group_sizes)
+  int32_t group_offset;
+  int32_t g_local;
+  int32_t row_tiles;      // of the grid: the most that the rows can fill
   int32_t box_rows;       // rows of an output tile and of x's boxes (multiple of 8, at most kSplitRows)
   int32_t stages;
   int32_t ring_bytes;     // of shared memory for the stages: kSplitRing or kSplitRingAlone

@@ -337,6 +337,39 @@ def test_most_groups(rd_lib, ot):
     _check_act_bwd(rd_lib, 2000, 72, block.SILU, ot, [s % 3 for s in sizes], 0, 1024, None)
 
 
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+@pytest.mark.parametrize("m,sizes,off,gl,limit", [
+    (1, [0, 0, 1, 0], 0, None, None),
+    (1, [0, 0, 1, 0], 1, 1, None),                        # no row of the local groups: zeros alone
+    (4, [1, 0, 2, 1], 0, None, None),
+    (17, [3, 0, 0, 9, 5, 0], 1, 4, None),
+    (17, [3, 0, 0, 9, 5, 0], 1, 4, 10),
+    (60, [1] * 40 + [0] * 60, 3, 90, None),               # rows behind the groups
+    (130, [129, 0, 1], 0, None, 130),
+    (130, [130], 0, None, -1),
+    (257, [127, 1, 128, 1], 0, 3, None),
+    (300, [0, 300, 0, 0, 0, 0, 0, 0], 0, None, 299),      # all rows in one group of eight
+    (40, [0] * 1000 + [7] + [0] * 20 + [30] + [0] * 2, 500, 523, None),
+])
+def test_linear_by_expert_few_rows(rd_lib, m, sizes, off, gl, limit, ot):
+    """Few tiles: k shared out over clusters, tiles as high as the groups ask for."""
+    cases = ((200, 72), (1032, 40)) if len(sizes) > 100 else ((0, 64), (200, 72), (1032, 136), (2056, 520))
+    for i, (k, n) in enumerate(cases):
+        _check_linear(rd_lib, m, k, n, (i + m) % 5, i != 2, i % 2 == 0, i < 2, ot, limit, sizes, off, gl)
+
+
+def test_linear_by_expert_bad_sizes_are_reported(rd_lib):
+    """Negative sizes count as none, sizes past m are cut, and the status word says so."""
+    x = torch.randn(30, 200, device=DEV).bfloat16()
+    w = torch.randn(3, 200, 72, device=DEV).bfloat16()
+    for sizes, same in (([10, -5, 9], [10, 0, 9]), ([10, 15, 9], [10, 15, 5]), ([40, -1, 3], [30, 0, 0])):
+        status, clean = _i32([0]), _i32([0])
+        got = rd_lib.linear(x, w, group_sizes=_i32(sizes), status=status)
+        want = rd_lib.linear(x, w, group_sizes=_i32(same), status=clean)
+        bits = (rd_lib.STATUS_NEG_SIZE if min(sizes) < 0 else 0) | (rd_lib.STATUS_OVERFLOW if sum(v for v in sizes if v > 0) > 30 else 0)
+        assert int(status.item()) == bits and int(clean.item()) == 0 and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("variant", ["single", "pair"])
 def test_linear_f32_by_expert_of_long_rows(rd_lib, variant):
     """k of three stretches of f32 sums and a part of one, so that the accumulators' turns go on from tile to tile."""
@@ -545,7 +578,7 @@ def _calls(rd, g):
     gain, words, limit = n(520, dtype=torch.float32), torch.tensor([5, 6], device=DEV), _i32([250])
     big, wg, bg, sizes = n(2600, 520), n(3, 520, 264), n(3, 264, dtype=torch.float32), _i32([700, 0, 1900])
     d, pre = n(2600, 264), n(2600, 264)
-    f, wide = rd.layer_norm_fwd(x, gain), n(90, 20000)
+    f, wide, few = rd.layer_norm_fwd(x, gain), n(90, 20000), _i32([7, 0, 20])
     fw = rd.layer_norm_fwd(wide)
     return {
         "norm": lambda **kw: rd.layer_norm_fwd(x, gain, gain, out_dtype=torch.float32, **kw),
@@ -553,6 +586,7 @@ def _calls(rd, g):
         "norm_bwd_wide": lambda **kw: rd.layer_norm_bwd(wide, wide, None, fw.mean, fw.rstd, **kw),
         "split": lambda **kw: (rd.linear(x, w, b, act=2, **kw),),
         "linear": lambda **kw: rd.linear(big, wg, bg, act=4, group_sizes=sizes, save_pre=True, **kw),
+        "experts": lambda **kw: rd.linear(big[:30], wg, bg, act=2, group_sizes=few, save_pre=True, **kw),
         "act_bwd": lambda **kw: rd.linear_act_bwd(d, pre, 3, group_sizes=sizes, **kw),
         "act_bwd_few": lambda **kw: rd.linear_act_bwd(d[:100], pre[:100], 3, **kw),
         "dropout": lambda **kw: (rd.dropout_rows(x, words, 0.2, residual=x, **kw),),
