@@ -213,19 +213,25 @@ int64_t usual_row_tiles(int64_t m, int32_t rows, bool groups, int32_t g_local) {
 
 // Few tiles: the kernel that splits k over clusters, or the persistent one, whose tiles are twice as wide (and on
 // CTA pairs twice as high).  At k = 4096, us split / persistent:
-//   m x n     16 x 14336  256 x 14336  512 x 4096  2048 x 1024  16381 x 128  1024 x 4096  16384 x 256
-//   tiles     112         224          128         128          128          256          256
-//             23 / 37     39 / 39      23 / 30     23 / 29      32 / 35      33 / 30      39 / 36
+//   m x n     16 x 14336  512 x 4096  2048 x 1024  16381 x 128  2500 x 1024  256 x 14336  1024 x 4096  16384 x 256
+//   tiles     112         128         128          128          160          224          256          256
+//             22 / 37     20 / 29     21 / 29      30 / 35      32 / 28      38 / 37      32 / 29      37 / 34
 // and by group (rows x k x n, groups): 4 x 2960 x 392, 16: 7.4 / 31; 310 x 2912 x 64, 4: 7.1 / 19; 128 x 4096 x 1024, 8: 18 / 35;
-// 8 x 7168 x 2048, 32: 39 / 62; 4096 x 1024 x 256, 16: 12 / 19.
-bool use_split(int sms, int64_t wide) { return 2 * wide <= 3 * static_cast<int64_t>(sms); }
+// 8 x 7168 x 2048, 32: 39 / 62; 4096 x 1024 x 256, 16: 12 / 19.  A short k leaves the persistent kernel's few epilogue warps too much of the
+// time (200 to 256 tiles, n = 1024, k = 512 / 1024 / 2048: 10 / 13, 14 / 15, 20 / 19; f32 14.4 / 15.0, 19.6 / 17.4; 30000 x 512 x 128 12 / 17),
+// except by group in f32 (100 x 512 x 512 in 128 groups 20 / 15).
+bool use_split(int sms, int64_t wide, int64_t k, bool groups, bool f32) {
+  const bool brief = k <= (f32 ? 512 : 1024) && !(groups && f32);
+  return wide <= (brief ? 3 : 1) * static_cast<int64_t>(sms);
+}
 
-// By group also where there are many tiles but few rows a group: the weights are the time, and its tiles are half as wide, so that they
-// spread better over the SMs (bf16, us split / persistent: 16 x 4096 x 4096 in 8 groups 36 / 44, 512 x 4096 x 4096 in 8 48 / 52, 256 x
-// 2048 x 1024 in 64 45 / 51, 4096 x 2048 x 1024 in 64 55 / 56, but 1024 x 4096 x 4096 in 8 73 / 70, 8192 x 2048 x 1024 in 64 73 / 65).  Its f32
-// tiles of 64 columns that run in turns are slower (512 x 4096 x 4096 in 8: 59 / 53).
-bool short_groups(int64_t m, int32_t g_total, int32_t out_dtype) {
-  return out_dtype == RD_BF16 && m <= 64 * static_cast<int64_t>(g_total);
+// By group also where there are more tiles but few rows a group: the weights are the time, and its tiles are half as wide, so that they
+// spread better over the SMs, if they do not take many turns (bf16, us split / persistent: 16 x 4096 x 4096 in 8 groups 36 / 39, 607 x 1280 x 2176
+// in 16 21 / 23, 256 x 2048 x 1024 in 64 45 / 47, 32 x 7168 x 2048 in 32 106 / 122, 8 x 2048 x 7168 in 32 40 / 50, but 512 x 4096 x 4096 in 8 48 /
+// 49, 4096 x 2048 x 1024 in 64 56 / 52, and with 896 tiles 64 x 4096 x 14336 in 8 147 / 142).  Its f32 tiles of 64 columns that run in
+// turns are slower (512 x 4096 x 4096 in 8: 59 / 52).
+bool short_groups(int sms, int64_t m, int64_t wide, int32_t g_total, bool f32) {
+  return !f32 && m <= 48 * static_cast<int64_t>(g_total) && wide <= 4 * static_cast<int64_t>(sms);
 }
 
 // Its tiles have 128 columns where these are tiles enough for more than half of the SMs, else 64 (tiles of 64 then have an SM each or
@@ -285,8 +291,10 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
   const bool groups = group_sizes != nullptr;
   const int32_t box_rows = split_rows(m, groups, g_total);
   const int64_t usual = usual_row_tiles(m, box_rows, groups, g_local), wide = usual * ((n + 127) / 128);
-  if (groups ? !variant_forced() && (use_split(sms, wide) || short_groups(m, g_total, out_dtype)) : use_split(sms, wide)) {
-    const int cols = split_cols(sms, wide, out_dtype == RD_F32);
+  const bool f32 = out_dtype == RD_F32;
+  if (!(groups && variant_forced()) &&
+      (use_split(sms, wide, k, groups, f32) || (groups && short_groups(sms, m, wide, g_total, f32)))) {
+    const int cols = split_cols(sms, wide, f32);
     const int64_t tiles = usual * ((n + cols - 1) / cols);
     SplitArgs s = {};
     s.bias = bias;
