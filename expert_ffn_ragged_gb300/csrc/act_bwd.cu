@@ -6,7 +6,7 @@
 // run at once.  It keeps its sums in registers until its rows' group ends, then adds its threads' in a fixed order
 // and writes one sum a column to the workspace.  Along the rows p and j only rise, so no two meetings of a
 // share p and a group j have the same p + j, and that numbers the sums; a second kernel adds a group's in their
-// order (no atomics).  A few rows over many groups are taken a group a block instead: its sums are the
+// order (no atomics).  A few rows, or some over many groups, are taken a group a block instead: its sums are the
 // result, and there is neither a workspace nor a second launch (2048 x 1024, 64 groups: 8.0 us against 10.1).
 //
 // Bound: HBM.  16384 x 14336, exact gelu, bf16: 1.41 GB in 227 us (6.2 TB/s), the tanh form 220; issue slots come next (58 % of
@@ -320,8 +320,12 @@ __global__ void __launch_bounds__(256) linear_bias_parts_kernel(const ActBwdArgs
 
 constexpr int kFewUnits = 64;  // of 128 columns and a group
 
-// whether a block takes a whole group: groups enough for all SMs, and no group that could be long
-bool whole_groups(int64_t m, int64_t n, int32_t g_local) { return m <= 2048 && (n + 63) / 64 * g_local >= 304; }
+// Whether a block takes a whole group: groups enough for all SMs and none that could be long, or few rows a group and altogether (us
+// whole / shares, gelu: 8 x 136 2.5 / 4.0, 64 x 4096 4.3 / 4.7, 32 x 136 in 64 groups 2.9 / 12, 256 x 1024 in 16 3.7 / 6.6, 256 x 4096 in 4
+// 5.7 / 6.9, but 128 x 4096 6.0 / 4.8).
+bool whole_groups(int64_t m, int64_t n, int32_t g_local) {
+  return m <= 2048 && ((n + 63) / 64 * g_local >= 304 || (m <= 256 && m <= 64 * static_cast<int64_t>(g_local)));
+}
 
 template <class D, int ACT, int W>
 cudaError_t go(ActBwdArgs a, cudaStream_t stream) {
@@ -350,10 +354,12 @@ template <class D, int ACT>
 cudaError_t by_width(const ActBwdArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e;
   const bool whole = whole_groups(a.m, a.n, a.g_local);
-  // whole groups: 128 columns, whose units are two turns of the blocks (2048 x 1024, 64 groups: 8.0 us; 64 columns and four
-  // turns 9.7, 256 and one 8.1)
+  // Whole groups: 128 columns a block, whose units are two turns of the blocks (2048 x 1024, 64 groups: 8.0 us; 64 columns and four turns
+  // 9.7), and 256 where units are many and groups short (us 128 / 256: 64 x 4096 in 64 groups 8.2 / 5.6, 256 x 14336 in 64 35 / 20, 1000 x
+  // 2048 in 64 9.7 / 8.3, but 2048 x 2048 in 16 12 / 17).
+  const bool wide = a.m <= 32 * static_cast<int64_t>(a.g_local) && static_cast<int64_t>(a.n) * a.g_local >= 128 * 608;
   if (a.n <= 64) e = go<D, ACT, 8>(a, stream);
-  else if (whole || a.n <= 128) e = go<D, ACT, 16>(a, stream);
+  else if ((whole && !wide) || a.n <= 128) e = go<D, ACT, 16>(a, stream);
   else e = go<D, ACT, 32>(a, stream);
   if (e != cudaSuccess || whole || a.d_bias == nullptr) return e;
   const int64_t quads = a.n / 4, most = static_cast<int64_t>(sms) * 8;

@@ -109,7 +109,7 @@ rd_status rd_linear_act_bwd(const void* d_out, int32_t out_dtype, const void* pr
                             int32_t g_local, const int32_t* limit, void* workspace,
                             size_t workspace_bytes, int32_t* status, rd_stream_t stream);
 
-/* The workspace of rd_linear_act_bwd; 0 where it needs none (few rows over many groups). */
+/* The workspace of rd_linear_act_bwd; 0 where it needs none (few rows). */
 rd_status rd_linear_act_bwd_workspace_size(int64_t m, int64_t n, int32_t g_local, size_t* bytes);
 
 /*
