@@ -652,7 +652,7 @@ def test_graphs_that_run_at_once_keep_their_own_workspaces(rd_lib):
 
 def test_binding_refusals(rd_lib):
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(64, 72, dtype=torch.bfloat16, device=DEV)
-    v = torch.zeros(64, device=DEV)
+    v, many = torch.zeros(64, device=DEV), torch.zeros(1000, 64, dtype=torch.bfloat16, device=DEV)
     words = torch.zeros(2, dtype=torch.int64, device=DEV)
     st = torch.zeros(4, device=DEV)
     gs = _i32([4])
@@ -678,7 +678,7 @@ def test_binding_refusals(rd_lib):
     for call in (lambda: rd_lib.layer_norm_fwd(x, eps=-1.0), lambda: rd_lib.linear(x, w, act=9),
                  lambda: rd_lib.linear_act_bwd(x, x, 0), lambda: rd_lib.linear_act_bwd(x, None, 2),
                  lambda: rd_lib.dropout_rows(x, words, 1.5), lambda: rd_lib.dropout_rows(x, words, 0.1, out=x),
-                 lambda: rd_lib.linear_act_bwd(x, x, 1, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)),
+                 lambda: rd_lib.linear_act_bwd(many, many, 1, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)),
                  lambda: rd_lib.layer_norm_fwd(torch.zeros(4, 12, device=DEV)),
                  lambda: rd_lib.layer_norm_fwd(torch.zeros(4 * 64 + 4, device=DEV)[4:].view(4, 64))):
         with pytest.raises(rd_lib.RdError):
