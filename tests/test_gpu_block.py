@@ -690,8 +690,9 @@ def test_binding_refusals(rd_lib):
 @pytest.mark.parametrize("which", ["split", "single", "pair"])
 def test_timeout_unwinds_and_reports(rd_lib, which, ot):
     """With a bound of 1 ns every wait that its first tries (of a microsecond each) do not end gives up: the
-    call reports it and the next one is right.  The waits of the kernel for few tiles are shorter than the
-    tries when nothing else runs, so there a call that reports nothing has to be right itself."""
+    call reports it and the next one is right.  The waits of the kernel for few tiles, and those of f32 outputs
+    for each 512 of k, can be shorter than the tries when nothing else runs, so there a call that reports nothing has to be
+    right itself."""
     rng = np.random.default_rng(2)
     m, k, n = (40, 16384, 512) if which == "split" else (1024, 8192, 512)
     x, w = _rows(rng, (m, k), "bf16").to(DEV), _rows(rng, (k, n), "bf16", 1 / math.sqrt(k)).to(DEV)
@@ -704,7 +705,7 @@ def test_timeout_unwinds_and_reports(rd_lib, which, ot):
         bounded = rd_lib.linear(x, w, **args)
     torch.cuda.synchronize()
     reported = int(status.item()) & rd_lib.STATUS_TIMEOUT
-    assert reported or which == "split"
+    assert reported or which == "split" or ot is torch.float32
     status.zero_()
     with rd_lib.tuning(variant=v):
         out = rd_lib.linear(x, w, **args)
