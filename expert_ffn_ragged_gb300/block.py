@@ -187,7 +187,9 @@ def layer_norm_bwd(d_out, x, weight, mean, rstd, limit=None, need_weight: bool =
             if len(_norm_bytes) >= 1024:
                 _norm_bytes.clear()
             need = _norm_bytes[key] = layer_norm_bwd_workspace_bytes(rows, hidden, dev)
-        scratch = _scratch(workspace, need, dev, idx)
+        scratch = workspace
+        if workspace is not None or need:
+            scratch = _scratch(workspace, need, dev, idx)
     _launch(lib.rd_layer_norm_bwd, "rd_layer_norm_bwd", idx, dev, stream, d_out.data_ptr(), out_type, x.data_ptr(),
             dtype, w_at, mean.data_ptr(), rstd.data_ptr(), d_x.data_ptr(), dw_at, db_at, rows, hidden,
             _word(limit, "limit", idx), _at(scratch), 0 if scratch is None else scratch.numel())

@@ -112,7 +112,7 @@ extern "C" rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, con
   if (rows > 0 && hidden > 0 &&
       (x == nullptr || d_out == nullptr || d_x == nullptr || mean == nullptr || rstd == nullptr))
     return RD_ERR_INVALID_ARG;
-  if (sums && hidden > 0 && workspace == nullptr) return RD_ERR_INVALID_ARG;
+  if (sums && hidden > 0 && workspace == nullptr && !layer_norm_bwd_few(rows, hidden)) return RD_ERR_INVALID_ARG;
   if (st != RD_OK) return st;
   if (!matrix_aligned(x, dtype) || !matrix_aligned(d_x, dtype) || !matrix_aligned(d_out, out_dtype) ||
       !aligned16(weight) || !aligned16(d_weight) || !aligned16(d_bias) || !matrix_aligned(workspace, RD_F32) ||
@@ -126,7 +126,8 @@ extern "C" rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, con
     return RD_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = current_device(&sms)) != RD_OK) return st;
-  if (sums && workspace_bytes < norm_bwd_bytes(rows, hidden, sms)) return RD_ERR_INVALID_ARG;
+  const uint64_t need = sums && hidden > 0 ? norm_bwd_bytes(rows, hidden, sms) : 0;
+  if (workspace_bytes < need) return RD_ERR_INVALID_ARG;
   if (hidden == 0) return RD_OK;
   if (rows == 0 && !sums) return RD_OK;
   NormArgs a = {};
@@ -138,7 +139,7 @@ extern "C" rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, con
   a.rstd = const_cast<float*>(rstd);
   a.d_weight = d_weight;
   a.d_bias = d_bias;
-  a.parts = sums ? static_cast<float*>(workspace) : nullptr;
+  a.parts = need > 0 ? static_cast<float*>(workspace) : nullptr;
   a.limit = limit;
   a.rows = static_cast<int32_t>(rows);
   a.hidden = static_cast<int32_t>(hidden);

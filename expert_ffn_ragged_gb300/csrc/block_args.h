@@ -35,6 +35,8 @@ cudaError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, int out_dtype, i
                                   cudaStream_t stream);
 // rows of partial sums that the backward pass keeps in its workspace
 int layer_norm_bwd_parts(int64_t rows, int64_t hidden, int sms);
+// whether it is the kernel for few rows, which needs no workspace
+bool layer_norm_bwd_few(int64_t rows, int64_t hidden);
 
 struct DropoutArgs {
   const void* x;

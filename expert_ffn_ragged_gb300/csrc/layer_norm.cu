@@ -6,14 +6,14 @@
 // so no barrier is needed for them) while this row is summed.  A thread keeps the same columns throughout:
 // weight and bias stay in registers, and the backward pass adds its columns' d_out * y and d_out there.
 // At the end the blocks of a cluster add their two sums a column through distributed shared memory, in their
-// order, and write one part a cluster to the workspace; a second kernel adds the parts in theirs (no atomics).
+// order, and write one part a cluster to the workspace; a second kernel adds the parts in theirs (no atomics).  (Up to 1024 rows: below.)
 // Rows of the backward pass too long for one block's registers (past 8192) are shared by a cluster, whose blocks send
 // each other the row's two sums; past 65536 the row is read twice and the columns are summed by a kernel of their own.
 //
 // Bound: HBM.  28157 x 4096, f32 stream, bf16 in the products: forward 692 MB in 106 us (6.5 TB/s), gradients 1.15 GB in
 // 175 us (6.6 TB/s, the second kernel's 3 us among them).  bf16 throughout the gradients take 121 us (5.7 TB/s): issue
-// slots, 22 packed operations for four elements.  One row takes 2.0 us, 509 rows' gradients 10.4 us (two launches, each some 4 us
-// from its start to its first result).
+// slots, 22 packed operations for four elements.  One row takes 2.0 us, 509 rows' gradients 6.3 us, in one launch (in the two
+// of the many rows, each some 4 us from its start to its first result, 10.4).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -560,7 +560,129 @@ __global__ void __launch_bounds__(32 * kPartLanes) layer_norm_parts_kernel(const
   if (out != nullptr) out[c < a.hidden ? c : c - a.hidden] = s;
 }
 
+// Few rows: everything in one launch and no workspace.  The first blocks take 32 columns each and read all rows for their sums
+// (64 rows at a time, in a fixed order), the others a row a block (T = 256) or a warp (T = 32) for d_x; what both read comes
+// from HBM once and from L2 once.
+template <class X, class O, int T, int V>
+__global__ void __launch_bounds__(256) layer_norm_bwd_few_kernel(const NormArgs a, int32_t col_blocks) {
+  __shared__ __align__(16) float pairs[8 * 2];
+  __shared__ float across[8][2][32];
+  pdl_trigger();
+  pdl_wait();
+  const int64_t hidden = a.hidden;
+  const int32_t L = rows_within(a.limit, a.rows);
+  const X* x = static_cast<const X*>(a.x);
+  const O* d_out = static_cast<const O*>(a.d_out);
+  if (static_cast<int32_t>(blockIdx.x) < col_blocks) {
+    const int piece = threadIdx.x & 3, row_lane = threadIdx.x >> 2, warp = threadIdx.x >> 5;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 32, col = col0 + piece * 8;
+    float2 dw[4], db[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[i] = db[i] = both(0.0f);
+    if (col < hidden) {
+#pragma unroll 4
+      for (int32_t row = row_lane; row < L; row += 64) {
+        float y[8], d[8];
+        load8(x + row * hidden + col, y);
+        load8(d_out + row * hidden + col, d);
+        const float2 m2 = both(-a.mean[row]), r2 = both(a.rstd[row]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d2 = make_float2(d[2 * i], d[2 * i + 1]);
+          dw[i] = fma2(d2, mul2(add2(make_float2(y[2 * i], y[2 * i + 1]), m2), r2), dw[i]);
+          db[i] = add2(db[i], d2);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 4; s < 32; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dw[i].x += __shfl_xor_sync(0xFFFFFFFFu, dw[i].x, s);
+        dw[i].y += __shfl_xor_sync(0xFFFFFFFFu, dw[i].y, s);
+        db[i].x += __shfl_xor_sync(0xFFFFFFFFu, db[i].x, s);
+        db[i].y += __shfl_xor_sync(0xFFFFFFFFu, db[i].y, s);
+      }
+    if ((threadIdx.x & 31) < 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        across[warp][0][piece * 8 + 2 * i] = dw[i].x;
+        across[warp][0][piece * 8 + 2 * i + 1] = dw[i].y;
+        across[warp][1][piece * 8 + 2 * i] = db[i].x;
+        across[warp][1][piece * 8 + 2 * i + 1] = db[i].y;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int c = threadIdx.x & 31, which = threadIdx.x >> 5;
+    float* out = which == 0 ? a.d_weight : a.d_bias;
+    if (out == nullptr || col0 + c >= hidden) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += across[i][which][c];
+    out[col0 + c] = s;
+    return;
+  }
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) - col_blocks) * (256 / T) + threadIdx.x / T;
+  if (row >= L) return;
+  const int t = threadIdx.x % T, vecs = a.hidden >> 3;
+  const float inv = 1.0f / static_cast<float>(a.hidden), mean = a.mean[row], rstd = a.rstd[row];
+  float y[V][8], d[V][8], pq[2] = {0.0f, 0.0f};
+  Raw8<X> rx[V];
+  Raw8<O> rd[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (t + i * T < vecs) {
+      load_raw(rx[i], x + row * hidden + 8 * (t + i * T));
+      load_raw(rd[i], d_out + row * hidden + 8 * (t + i * T));
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (t + i * T < vecs) {
+      float w[8];
+      widen(rx[i], y[i]);
+      widen(rd[i], d[i]);
+      if (a.weight != nullptr) {
+        load8_param(a.weight + 8 * (t + i * T), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[i][e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[i][e] = (y[i][e] - mean) * rstd;
+        pq[0] += d[i][e];
+        pq[1] = fmaf(d[i][e], y[i][e], pq[1]);
+      }
+    }
+  row_sums<T>(pq, pairs);
+  const float p = pq[0] * inv, q = pq[1] * inv;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (t + i * T < vecs) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[i][e] = rstd * (d[i][e] - fmaf(y[i][e], q, p));
+      store8(static_cast<X*>(a.out) + row * hidden + 8 * (t + i * T), d[i]);
+    }
+}
+
 int64_t ceil_of(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+
+template <class X, class O, int T, int V>
+cudaError_t bwd_few(const NormArgs& a, cudaStream_t stream) {
+  const bool sums = a.d_weight != nullptr || a.d_bias != nullptr;
+  const int64_t cols = sums ? ceil_of(a.hidden, 32) : 0, blocks = cols + ceil_of(a.rows, 256 / T);
+  return launch_pdl(layer_norm_bwd_few_kernel<X, O, T, V>, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, stream, a,
+                    static_cast<int32_t>(cols));
+}
+
+template <class X, class O>
+cudaError_t bwd_few_by_width(const NormArgs& a, cudaStream_t stream) {
+  if (a.hidden <= 256) return bwd_few<X, O, 32, 1>(a, stream);
+  if (a.hidden <= 1024) return bwd_few<X, O, 32, 4>(a, stream);
+  if (a.hidden <= 4096) return bwd_few<X, O, 256, 2>(a, stream);
+  return bwd_few<X, O, 256, 4>(a, stream);
+}
 
 // R rows at a time, S of these in the ring, B blocks on an SM
 template <class X, class O, int T, int V, int R, int S, int B>
@@ -666,6 +788,7 @@ cudaError_t bwd(const NormArgs& a, int* parts, cudaStream_t stream) {
 //   read twice by one block instead of shared by a cluster 1970, 2970, 2200)
 template <class X, class O>
 cudaError_t bwd_by_width(const NormArgs& a, int* parts, int sms, cudaStream_t stream) {
+  if (layer_norm_bwd_few(a.rows, a.hidden)) return bwd_few_by_width<X, O>(a, stream);
   // (rows at a time and blocks as bwd_shape has them)
   if (a.hidden <= 256) return bwd<X, O, 32, 2, 1, 3>(a, parts, stream);
   if (a.hidden <= 1024) return bwd<X, O, 128, 2, 2, 4>(a, parts, stream);
@@ -702,8 +825,13 @@ cudaError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, int out_dtype, i
                              : fwd_by_width<bf16, bf16>(a, sms, stream);
 }
 
+// us in one launch / in two, bf16: 256 x 256 2.5 / 4.6, 512 x 1024 3.2 / 7.2, 512 x 4096 5.7 / 10.4, 1024 x 4096 12.1 / 12.6, 1024 x 8192
+// 15.6 / 16.4, but 2048 x 256 9.8 / 7.7, 2048 x 4096 22.8 / 16.7
+bool layer_norm_bwd_few(int64_t rows, int64_t hidden) { return rows <= 1024 && hidden <= 8192; }
+
 // the most that the kernels write: as many clusters as fit the SMs' threads, and no more than the rows fill
 int layer_norm_bwd_parts(int64_t rows, int64_t hidden, int sms) {
+  if (layer_norm_bwd_few(rows, hidden)) return 0;
   const BwdShape shape = bwd_shape(hidden);
   int64_t p, most;
   if (shape.rows == 0) {
@@ -727,7 +855,7 @@ cudaError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, int out_dtype, i
   else
     e = out_dtype == RD_F32 ? bwd_by_width<bf16, float>(a, &parts, sms, stream)
                             : bwd_by_width<bf16, bf16>(a, &parts, sms, stream);
-  if (e != cudaSuccess || a.parts == nullptr) return e;
+  if (e != cudaSuccess || a.parts == nullptr || parts == 0) return e;
   return launch_pdl(layer_norm_parts_kernel, dim3(static_cast<unsigned>(ceil_of(2 * static_cast<int64_t>(a.hidden), 32))),
                     32 * kPartLanes, 0, 1, stream, a, static_cast<int32_t>(parts));
 }

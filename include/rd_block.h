@@ -48,7 +48,8 @@ rd_status rd_layer_norm_fwd(const void* x, int32_t dtype, const float* weight, c
  *   d_out of `out_dtype`, x and d_x of `dtype`, weight [hidden] f32 or NULL, mean, rstd [rows] f32.
  *   d_weight, d_bias [hidden] f32, either NULL to leave it out.  No atomics: the same result on every run.
  *   workspace  device scratch of rd_layer_norm_bwd_workspace_size bytes, 32-byte aligned; may be
- *              NULL when both d_weight and d_bias are.  Its contents before and after do not matter.
+ *              NULL when both d_weight and d_bias are, or that size is 0.  Its contents before and
+ *              after do not matter.
  * Requires hidden % 8 == 0.
  */
 rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, const void* x, int32_t dtype,
@@ -57,7 +58,7 @@ rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, const void* x,
                             const int32_t* limit, void* workspace, size_t workspace_bytes,
                             rd_stream_t stream);
 
-/* The workspace of rd_layer_norm_bwd on the current device. */
+/* The workspace of rd_layer_norm_bwd on the current device; 0 where it needs none (few rows). */
 rd_status rd_layer_norm_bwd_workspace_size(int64_t rows, int64_t hidden, size_t* bytes);
 
 /* activations of rd_linear */

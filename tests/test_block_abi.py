@@ -71,7 +71,7 @@ def test_norm_refusals(lib):
               dict(w=addr(2) + 4), dict(b=addr(3) + 8), dict(mean=addr(5) + 2), dict(limit=addr(7) + 1)])
 
     def bwd(d=addr(1), out_dtype=1, x=addr(2), dtype=0, w=addr(3), mean=addr(4), rstd=addr(5), d_x=addr(6),
-            dw=addr(7), db=addr(8), rows=4, hidden=64, limit=None, ws=addr(9), nb=1 << 30):
+            dw=addr(7), db=addr(8), rows=1 << 20, hidden=64, limit=None, ws=addr(9), nb=1 << 30):
         return lib.rd_layer_norm_bwd(d, out_dtype, x, dtype, w, mean, rstd, d_x, dw, db, rows, hidden, limit, ws, nb, None)
 
     _refused(bwd,

@@ -180,8 +180,25 @@ def test_norm_bwd(rd_lib, hidden, dt, ot):
     _check_norm_bwd(rd_lib, 37, hidden, dt, ot)
 
 
-@pytest.mark.parametrize("rows", [0, 1, 3, 8, 9, 600, 3001])
-@pytest.mark.parametrize("hidden", [64, 1032, 4096, 12000])
+@pytest.mark.parametrize("hidden", [8, 248, 264, 1024, 1032, 2048, 2056, 4096, 4104, 8192])
+@pytest.mark.parametrize("dt,ot", [("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_norm_bwd_many_rows(rd_lib, hidden, dt, ot):
+    _check_norm_bwd(rd_lib, 1061, hidden, dt, ot)
+
+
+@pytest.mark.parametrize("limit", [-1, 0, 1, 700, 1299, 2000])
+@pytest.mark.parametrize("hidden", [248, 4096])
+def test_norm_bwd_many_rows_limit(rd_lib, limit, hidden):
+    _check_norm_bwd(rd_lib, 1300, hidden, "f32", "bf16", limit=limit)
+
+
+@pytest.mark.parametrize("need", [(True, False), (False, True), (False, False)])
+def test_norm_bwd_many_rows_parts_left_out(rd_lib, need):
+    _check_norm_bwd(rd_lib, 1030, 1032, "bf16", "f32", weight=False, need=need)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 3, 8, 9, 600, 1024, 1025, 3001])
+@pytest.mark.parametrize("hidden", [64, 1032, 4096, 8192, 12000])
 def test_norm_bwd_rows(rd_lib, rows, hidden):
     _check_norm_bwd(rd_lib, rows, hidden, "bf16", "bf16")
 
