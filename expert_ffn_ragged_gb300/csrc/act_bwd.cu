@@ -320,11 +320,11 @@ __global__ void __launch_bounds__(256) linear_bias_parts_kernel(const ActBwdArgs
 
 constexpr int kFewUnits = 64;  // of 128 columns and a group
 
-// Whether a block takes a whole group: groups enough for all SMs and none that could be long, or few rows a group and altogether (us
-// whole / shares, gelu: 8 x 136 2.5 / 4.0, 64 x 4096 4.3 / 4.7, 32 x 136 in 64 groups 2.9 / 12, 256 x 1024 in 16 3.7 / 6.6, 256 x 4096 in 4
-// 5.7 / 6.9, but 128 x 4096 6.0 / 4.8).
+// Whether a block takes a whole group: groups enough for all SMs and none that could be long, or few rows (us whole / shares, gelu: 8 x 136
+// 2.5 / 4.0, 200 x 4096 5.0 / 5.5, 32 x 136 in 64 groups 2.9 / 12, 509 x 1024 in 16 4.6 / 6.2, 1024 x 1024 in 4 6.1 / 6.8, but 509 x 1024 6.5 /
+// 4.8, 2000 x 4096 in 4 16 / 14).
 bool whole_groups(int64_t m, int64_t n, int32_t g_local) {
-  return m <= 2048 && ((n + 63) / 64 * g_local >= 304 || (m <= 256 && m <= 64 * static_cast<int64_t>(g_local)));
+  return m <= 2048 && ((n + 63) / 64 * g_local >= 304 || m <= 256 * static_cast<int64_t>(g_local < 4 ? g_local : 4));
 }
 
 template <class D, int ACT, int W>
@@ -355,10 +355,13 @@ cudaError_t by_width(const ActBwdArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e;
   const bool whole = whole_groups(a.m, a.n, a.g_local);
   // Whole groups: 128 columns a block, whose units are two turns of the blocks (2048 x 1024, 64 groups: 8.0 us; 64 columns and four turns
-  // 9.7), and 256 where units are many and groups short (us 128 / 256: 64 x 4096 in 64 groups 8.2 / 5.6, 256 x 14336 in 64 35 / 20, 1000 x
-  // 2048 in 64 9.7 / 8.3, but 2048 x 2048 in 16 12 / 17).
+  // 9.7).  256 where units are many and groups short (us 128 / 256: 64 x 4096 in 64 groups 8.2 / 5.6, 256 x 14336 in 64 35 / 20, 1000 x
+  // 2048 in 64 9.7 / 8.3, but 2048 x 2048 in 16 12 / 17).  32 or, of many, 64 columns where a group's rows are more than a few turns (us 32 / 64 /
+  // 128: 200 x 4096 5.0 / 5.8 / 8, 509 x 136 in 4 4.0 / 4.9, 100 x 14336 7.0 / 5.5 / 6.5).
   const bool wide = a.m <= 32 * static_cast<int64_t>(a.g_local) && static_cast<int64_t>(a.n) * a.g_local >= 128 * 608;
-  if (a.n <= 64) e = go<D, ACT, 8>(a, stream);
+  const bool tall = whole && a.m <= 1024 && a.m > 64 * static_cast<int64_t>(a.g_local);
+  if (tall && a.n <= 4096) e = go<D, ACT, 4>(a, stream);
+  else if (tall || a.n <= 64) e = go<D, ACT, 8>(a, stream);
   else if ((whole && !wide) || a.n <= 128) e = go<D, ACT, 16>(a, stream);
   else e = go<D, ACT, 32>(a, stream);
   if (e != cudaSuccess || whole || a.d_bias == nullptr) return e;

@@ -103,7 +103,7 @@ def test_linear_refusals(lib):
               dict(out_dtype=0, res=addr(4) + 16), dict(pre=addr(6) + 8), dict(b=addr(3) + 4),
               dict(gs=addr(9) + 2), dict(limit=addr(7) + 1)])
 
-    def bwd(d=addr(1), out_dtype=1, pre=addr(2), act=4, d_pre=addr(3), d_bias=addr(4), m=1000, n=64, gs=None, g=1, off=0,
+    def bwd(d=addr(1), out_dtype=1, pre=addr(2), act=4, d_pre=addr(3), d_bias=addr(4), m=1100, n=64, gs=None, g=1, off=0,
             gl=1, limit=None, ws=addr(5), nb=1 << 20, status=None):
         return lib.rd_linear_act_bwd(d, out_dtype, pre, act, d_pre, d_bias, m, n, gs, g, off, gl, limit, ws, nb, status, None)
 
@@ -117,8 +117,8 @@ def test_linear_refusals(lib):
     assert lib.rd_linear_act_bwd_workspace_size(4, 64, 1, None) == INVALID
     assert lib.rd_linear_act_bwd_workspace_size(4, 64, 0, ctypes.byref(size)) == INVALID
     assert lib.rd_linear_act_bwd_workspace_size(4, 64, 2000, ctypes.byref(size)) == UNSUPPORTED
-    assert lib.rd_linear_act_bwd_workspace_size(1000, 64, 3, ctypes.byref(size)) == OK
-    assert size.value >= 4 * 64 * (1000 // 64 + 3)
+    assert lib.rd_linear_act_bwd_workspace_size(3000, 64, 3, ctypes.byref(size)) == OK
+    assert size.value >= 4 * 64 * (3000 // 64 + 3)
     assert lib.rd_linear_act_bwd_workspace_size(4, 64, 1, ctypes.byref(size)) == OK and size.value == 0
 
 

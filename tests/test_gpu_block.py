@@ -491,6 +491,17 @@ def test_act_bwd_by_expert(rd_lib, m, sizes, off, gl, limit):
     _check_act_bwd(rd_lib, m, 40, block.NONE, "f32", sizes, off, gl, limit)
 
 
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+@pytest.mark.parametrize("m,sizes", [
+    (65, None), (200, None), (256, None), (257, None), (500, [0, 500]), (513, [500, 13]), (700, [100, 0, 599, 1]),
+    (1024, [1, 1000, 23, 0, 0]), (1025, [500, 0, 25, 500]),
+])
+def test_act_bwd_whole_groups(rd_lib, m, sizes, ot):
+    """Around the sizes where a block takes a whole group, and of both widths that it may have then."""
+    for n in (8, 72, 1000, 4104):
+        _check_act_bwd(rd_lib, m, n, block.GELU if n % 16 else block.NONE, ot, sizes)
+
+
 @pytest.mark.parametrize("limit", [-1, 0, 1, 63, 64, 65, 2999, 4000])
 def test_act_bwd_limit(rd_lib, limit):
     for m in (90, 3000):
