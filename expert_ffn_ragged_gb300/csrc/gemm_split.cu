@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
   const int nkb = ceil_div(a.k, kBK);
   const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / C);
   const int kb1 = live ? static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / C) : kb0;
-  bool ok = true;
+  int fills = 0;               // stages that this thread has filled: the first thread's
   float sums[kFine ? BN : 1];  // of a row, in warps 4 to 7
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, fills = 0;
+      int stage = 0;
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
@@ -231,15 +231,6 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
         if (++stage == a.stages) {
           stage = 0;
           phase ^= 1;
-        }
-      }
-      if (*abort_flag) {
-        // the copies in flight land before this CTA's memory is given up
-        volatile int no_abort = 0;
-        const int last = fills < a.stages ? fills : a.stages;
-        for (int i = 1; i <= last; ++i) {
-          const int f = fills - i;
-          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[f % a.stages]), (f / a.stages) & 1, &no_abort, kSplitDrainNs);
         }
       }
     }
@@ -327,12 +318,23 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
   }
   {
     volatile int no_abort = 0;
-    // (twice the bound of the other waits, which end first and leave the drain above)
-    ok = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.done), 0, &no_abort, 2 * a.timeout_ns + kSplitDrainNs);
-    ok = __all_sync(0xFFFFFFFFu, ok) && *abort_flag == 0;
-    ptx::tc_fence_after();
+    // (twice the bound of the other waits, which end first)
+    if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.done), 0, &no_abort, 2 * a.timeout_ns + kSplitDrainNs)) *abort_flag = 1;
+    // After a wait that ran out, whichever role's it was, the copies that no MMA has waited for land before the ring's place
+    // is taken.  (The role may give up after the last copy has been asked for, so it is here that the flag is looked at: the
+    // issuing thread raises it before the commit that ends this wait.)
+    if (fills > 0 && *abort_flag) {
+      const int last = fills < a.stages ? fills : a.stages;
+      for (int i = 1; i <= last; ++i) {
+        const int f = fills - i;
+        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[f % a.stages]), (f / a.stages) & 1, &no_abort, kSplitDrainNs);
+      }
+    }
+    __syncwarp();
   }
-  __syncthreads();  // every warp is past its waits: the ring is free
+  __syncthreads();  // every warp is past its waits: the ring is free, and all see the same flag
+  const bool ok = *abort_flag == 0;
+  ptx::tc_fence_after();
 
   // the accumulator's rows to shared memory: a thread a row, two warps a quarter of the rows
   float* stage_f = reinterpret_cast<float*>(smem);

@@ -1,0 +1,58 @@
+"""Waits inside the kernels of include/rd_block.h that run out: the call returns, what it reports and leaves behind, and the
+calls after it."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+# kernel for few tiles: rows, k, n, group sizes (None: one weight)
+FEW_TILES = {
+    "eight share k": (40, 16384, 512, None),
+    "four share k": (64, 14336, 4096, None),
+    "two share k": (256, 4096, 4096, None),
+    "alone": (3, 4096, 14336, None),
+    "alone, no wait for a free stage": (3, 256, 14336, None),
+    "by group": (30, 4096, 512, [7, 0, 20]),
+    "by group, alone": (40, 4096, 4096, [3, 30, 5, 2]),
+}
+
+
+def _linear(rd, which, ot, seed=0):
+    """A call of rd_linear on the kernel for few tiles: function of a status word that gives the output."""
+    m, k, n, sizes = FEW_TILES[which]
+    g = torch.Generator().manual_seed(seed + m)
+    lead = () if sizes is None else (len(sizes),)
+    x = torch.randn(m, k, generator=g).bfloat16().to(DEV)
+    w = (torch.randn(*lead, k, n, generator=g) / math.sqrt(k)).bfloat16().to(DEV)
+    b = torch.randn(*lead, n, generator=g).to(DEV)
+    gs = None if sizes is None else _i32(sizes)
+    return lambda status: rd.linear(x, w, b, act=rd.ACT_SILU, group_sizes=gs, out_dtype=ot, status=status)
+
+
+@pytest.mark.parametrize("ot", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("which", list(FEW_TILES))
+def test_few_tiles_right_or_reported(rd_lib, which, ot):
+    """Bounds from one that no wait keeps to one that nearly all do, so that each role is the one that gives up:
+    what is not reported is right, and so is the call after it, on the same memory."""
+    call = _linear(rd_lib, which, ot)
+    status = _i32([0])
+    want = call(status).clone()
+    for limit in (1, 1500, 3000, 6000, 12000, 25000) * 3:
+        with rd_lib.tuning(wait_timeout_ns=limit):
+            bounded = call(status)
+        again = call(None)
+        torch.cuda.synchronize()
+        bits = int(status.item())
+        assert bits in (0, rd_lib.STATUS_TIMEOUT)
+        assert bits or torch.equal(bounded, want), limit
+        assert torch.equal(again, want), limit
+        status.zero_()
