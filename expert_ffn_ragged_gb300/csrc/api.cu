@@ -46,9 +46,9 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-uint64_t wait_timeout_ns() {
+WaitBound wait_limit() {
   const uint64_t t = g_timeout_ns.load(std::memory_order_relaxed);
-  return t == 0 ? kTimeoutNs : t;
+  return wait_bound(t == 0 ? kTimeoutNs : t);
 }
 
 rd_status current_device(int* sms) {
@@ -263,7 +263,7 @@ extern "C" rd_status rd_ragged_dot(const void* lhs, const void* rhs, void* out, 
   const int tile_w = glu ? kBN / 2 : kBN;
   a.n_tiles = static_cast<int32_t>((n_out + tile_w - 1) / tile_w);
   a.dw_m_tiles = 0;
-  a.timeout_ns = wait_timeout_ns();
+  a.wait = wait_limit();
   const bool pair = use_pair(sms, m, g_total);
   a.band_tiles = band_tiles(pair);
   const int grid = pair ? pair_grid(sms, ((m + 2 * kBM - 1) / (2 * kBM) + g_local) * a.n_tiles)
@@ -332,7 +332,7 @@ rd_status trans_rhs_impl(const void* lhs, const void* rhs, const void* fused, vo
   a.g_local = g_local;
   a.n_tiles = static_cast<int32_t>((k + kBN - 1) / kBN);
   a.band_tiles = band_tiles(pair);
-  a.timeout_ns = wait_timeout_ns();
+  a.wait = wait_limit();
   const int grid = pair ? pair_grid(sms, ((m + 2 * kBM - 1) / (2 * kBM) + g_local) * a.n_tiles)
                         : grid_for(sms, ((m + kBM - 1) / kBM + g_local) * a.n_tiles);
   return launch_gemm_dx(pair, glu_bwd, ta, tb, a, grid, reinterpret_cast<cudaStream_t>(stream)) ==
@@ -452,7 +452,7 @@ rd_status trans_ragged_impl(const void* x, const void* y, void* out, int64_t m, 
   a.g_local = g_local;
   a.n_tiles = static_cast<int32_t>((n + kBN - 1) / kBN);
   a.dw_m_tiles = static_cast<int32_t>((k + tile_rows - 1) / tile_rows);
-  a.timeout_ns = wait_timeout_ns();
+  a.wait = wait_limit();
   const int64_t tiles = static_cast<int64_t>(g_local) * a.dw_m_tiles * a.n_tiles;
   if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
   const int grid = pair ? pair_grid(sms, tiles) : grid_for(sms, tiles);

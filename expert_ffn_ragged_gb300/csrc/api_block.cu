@@ -318,7 +318,7 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
     s.ring_bytes = split_alone(sms, cols, tiles) ? kSplitRingAlone : kSplitRing;
     s.stages = s.ring_bytes / stage < kSplitMaxStages ? s.ring_bytes / stage : kSplitMaxStages;
     s.cluster = split_cluster(sms, cols, tiles, k);
-    s.timeout_ns = wait_timeout_ns();
+    s.wait = wait_limit();
     CUtensorMap tx = {}, tw = {};
     if (k > 0) {
       const uint64_t dx[2] = {static_cast<uint64_t>(k), um}, sx[1] = {static_cast<uint64_t>(k) * 2};
@@ -356,7 +356,7 @@ extern "C" rd_status rd_linear(const void* x, const void* w, const float* bias, 
   a.ldo = n;
   a.zero_cols = static_cast<int32_t>(n);
   a.n_tiles = static_cast<int32_t>((n + kBN - 1) / kBN);
-  a.timeout_ns = wait_timeout_ns();
+  a.wait = wait_limit();
   a.band_tiles = band_tiles(pair);
   a.bias = bias;
   a.residual = residual;

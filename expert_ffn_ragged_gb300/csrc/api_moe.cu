@@ -449,7 +449,7 @@ extern "C" rd_status rd_ragged_dot_mxfp4(const void* a, const void* a_scales, co
   // a 4-bit row is a quarter of a bf16 row: bands of four times the rows keep as many bytes in L2
   // (32768 x 4096 x 14336: 623 -> 617 us, means of six)
   g.band_tiles = band_tiles(pair, 4 * kBandRows) * (few ? kBM / 32 : 1);
-  g.timeout_ns = wait_timeout_ns();
+  g.wait = wait_limit();
   const int64_t tiles = ((m + tm - 1) / tm + g_local) * g.n_tiles;
   if (tiles > kMaxDim) return RD_ERR_UNSUPPORTED;
   const int grid = pair ? pair_grid(sms, tiles) : grid_for(sms, tiles);

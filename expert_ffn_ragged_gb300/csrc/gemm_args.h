@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "schedule.h"
+#include "wait_bound.h"
 
 namespace rd {
 
@@ -54,7 +55,7 @@ struct GemmArgs {
   int32_t band_tiles;          // fwd/dx: m-tiles per band of the tile order (lhs rows kept in L2)
   int32_t a_chunked;           // dw: tmap_a is (64, rows, width / 64): one box per stage
   int32_t b_chunked;           // dw: tmap_b likewise (else 2-D maps, one box per 64 columns)
-  uint64_t timeout_ns;         // bound of every wait inside the kernel
+  WaitBound wait;              // bound of every wait inside the kernel
   // kEpiLinear, kEpiLinearF32 (group_sizes may be null: one group of all rows)
   const float* bias;           // [g_local, n_out] or null
   const void* residual;        // [m, n_out] of the output's type or null

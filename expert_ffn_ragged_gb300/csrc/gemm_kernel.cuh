@@ -66,7 +66,7 @@ namespace rd {
 
 // Bounds of the waits made while unwinding after a timeout: every copy or MMA
 // still in flight then completes within microseconds.
-constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr WaitBound kDrain = wait_bound(1000000000ull);
 constexpr uint64_t kGraceNs = 200000ull;
 
 // FINE: f32 outputs whose sums the epilogue takes over every kFineBlocks K blocks (kEpiLinearF32): 16 epilogue warps
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
   ptx::tc_fence_after();
 
   const int total = sh.total_tiles;
-  const uint64_t tlimit = args.timeout_ns;
+  const WaitBound tlimit = args.wait;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -466,11 +466,11 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
           const bool e = (pend_edge >> s) & 1u;
           const uint32_t cp = (pend_cpar >> s) & 1u;
           if (e)
-            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.efull[s]), cp, &no_abort, kDrainNs);
+            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.efull[s]), cp, &no_abort, kDrain);
           else if (!PAIR || rank == 0)
-            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[s]), cp, &no_abort, kDrainNs);
+            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[s]), cp, &no_abort, kDrain);
         } else {
-          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), par, &no_abort, kDrainNs);
+          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), par, &no_abort, kDrain);
         }
       }
       if (PAIR && rank != 0 && *abort_flag && (pend_mask & ~pend_edge) != 0) {
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
         volatile int no_abort = 0;
         if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.drain), 0x1);
         else ptx::tc_commit(ptx::smem_addr(&sh.drain));
-        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.drain), 0, &no_abort, kDrainNs);
+        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.drain), 0, &no_abort, kDrain);
       }
     }
     __syncwarp();
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
           if (target <= done) {
             // pacing only: give up (and unwind with the CTA) like any other wait
             if (*abort_flag) break;
-            if (ptx::global_timer_ns() - t_last > tlimit) {
+            if (ptx::global_timer_ns() - t_last > tlimit.ns) {
               *abort_flag = 1;
               break;
             }

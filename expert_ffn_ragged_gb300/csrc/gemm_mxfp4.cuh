@@ -83,7 +83,7 @@ struct Gemm4Args {
   int32_t n_tiles;
   int32_t dw_m_tiles;    // unused (schedule)
   int32_t band_tiles;
-  uint64_t timeout_ns;
+  WaitBound wait;
 };
 
 // operands and their scales; boxes: a 128 rows, b 96 rows (of 128 bytes; scales: of 32)
@@ -200,9 +200,9 @@ __device__ __forceinline__ int b_row_of(int n_idx, int c, int n_out) {
 
 // One lane waits for the warp (polls by all lanes end at different times and then wait for each other).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          uint64_t limit_ns, int lane) {
+                                          WaitBound limit, int lane) {
   int ok = 1;
-  if (lane == 0) ok = ptx::mbar_wait_bounded(bar, parity, abort_flag, limit_ns) ? 1 : 0;
+  if (lane == 0) ok = ptx::mbar_wait_bounded(bar, parity, abort_flag, limit) ? 1 : 0;
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
   ptx::tc_fence_after();
 
   const int total = sh.total_tiles;
-  const uint64_t tlimit = args.timeout_ns;
+  const WaitBound tlimit = args.wait;
   int group = 0;  // of this role's last tile
 
   if (warp == 0) {
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       if (!*abort_flag) {
         for (int s = 0; s < S; ++s)
           if (pend_mask & (1u << s))
-            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), (pend_par >> s) & 1u, abort_flag, kDrainNs);
+            ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[s]), (pend_par >> s) & 1u, abort_flag, kDrain);
       }
       if (*abort_flag) {
         const uint64_t t0 = ptx::global_timer_ns();
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
           if (PAIR) ptx::tc_commit_pair(ptx::smem_addr(&sh.drain), 0x1);
           else ptx::tc_commit(ptx::smem_addr(&sh.drain));
         }
-        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.drain), 0, &no_abort, kDrainNs);
+        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.drain), 0, &no_abort, kDrain);
       }
     }
     __syncwarp();
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(k4Threads, 1)
       volatile int no_abort = 0;
       for (int s = 0; s < k4RawSlots; ++s)
         if (pend_mask & (1u << s))
-          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rfull[s]), (pend_par >> s) & 1u, &no_abort, kDrainNs);
+          ptx::mbar_wait_bounded(ptx::smem_addr(&sh.rfull[s]), (pend_par >> s) & 1u, &no_abort, kDrain);
     }
   } else {
     // ------------------------------------------------------------ scales

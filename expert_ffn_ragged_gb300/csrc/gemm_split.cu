@@ -41,7 +41,7 @@ namespace rd {
 namespace {
 
 constexpr int kSplitThreads = 256;  // warp 0 copies, warp 1 issues the MMAs; all eight take the sums
-constexpr uint64_t kSplitDrainNs = 1000000000ull;
+constexpr WaitBound kSplitDrain = wait_bound(1000000000ull);
 constexpr int kStretch = 8;  // K blocks that the tensor core sums before an f32 output takes them over
 
 struct SplitShared {
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t bar = ptx::smem_addr(&sh.full[stage]);
-        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, a.timeout_ns)) break;
+        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.empty[stage]), phase ^ 1, abort_flag, a.wait)) break;
         ptx::mbar_arrive_expect_tx(bar, a_bytes + b_bytes);
 #pragma unroll
         for (int c = 0; c < BN / 64; ++c) {
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
         const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(s_b + stage * b_bytes), kBK * 128, 1024);
         if (kFine && first && stretch >= 2 &&
             !ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tempty[stretch & 1]), ((stretch >> 1) - 1) & 1, abort_flag,
-                                    a.timeout_ns))
+                                    a.wait))
           break;
-        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), phase, abort_flag, a.timeout_ns)) break;
+        if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[stage]), phase, abort_flag, a.wait)) break;
         ptx::tc_fence_after();
         // the descriptors' address field counts 16 bytes: a step of 16 along k is 32 bytes of x and 16 rows of w
 #pragma unroll
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
     const int stretches = (kb1 - kb0 + kStretch - 1) / kStretch;
 #pragma unroll 1
     for (int s = 0; s < stretches; ++s) {
-      bool there = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[s & 1]), (s >> 1) & 1, abort_flag, a.timeout_ns);
+      bool there = ptx::mbar_wait_bounded(ptx::smem_addr(&sh.tfull[s & 1]), (s >> 1) & 1, abort_flag, a.wait);
       there = __all_sync(0xFFFFFFFFu, there);
       if (!there) break;
       ptx::tc_fence_after();
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
   {
     volatile int no_abort = 0;
     // (twice the bound of the other waits, which end first)
-    if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.done), 0, &no_abort, 2 * a.timeout_ns + kSplitDrainNs)) *abort_flag = 1;
+    if (!ptx::mbar_wait_bounded(ptx::smem_addr(&sh.done), 0, &no_abort, WaitBound{2 * a.wait.ns + kSplitDrain.ns, kSuspendHintNs})) *abort_flag = 1;
     // After a wait that ran out, whichever role's it was, the copies that no MMA has waited for land before the ring's place
     // is taken.  (The role may give up after the last copy has been asked for, so it is here that the flag is looked at: the
     // issuing thread raises it before the commit that ends this wait.)
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
       const int last = fills < a.stages ? fills : a.stages;
       for (int i = 1; i <= last; ++i) {
         const int f = fills - i;
-        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[f % a.stages]), (f / a.stages) & 1, &no_abort, kSplitDrainNs);
+        ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[f % a.stages]), (f / a.stages) & 1, &no_abort, kSplitDrain);
       }
     }
     __syncwarp();

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "wait_bound.h"
+
 namespace rd {
 
 struct SplitArgs {
@@ -27,7 +29,7 @@ struct SplitArgs {
   int32_t stages;
   int32_t ring_bytes;     // of shared memory for the stages: kSplitRing or kSplitRingAlone
   int32_t cluster;        // CTAs that share one output tile's k
-  uint64_t timeout_ns;
+  WaitBound wait;         // bound of every wait inside the kernel
 };
 
 constexpr int kSplitMaxStages = 12;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/rd.h"
+#include "wait_bound.h"
 
 namespace rd {
 
@@ -14,7 +15,7 @@ constexpr int64_t kMaxDim = 0x7FFFFFFF;
 constexpr int64_t kMaxWidth = kMaxDim - 255;
 
 // bound of every wait inside the kernels (rd_set_tuning, or the default)
-uint64_t wait_timeout_ns();
+WaitBound wait_limit();
 
 // SM count of the current device, and whether it is an sm_103 part
 rd_status current_device(int* sms);

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
 constexpr int kNormCluster = 2;  // blocks that add their sums before they go to the workspace
 
 constexpr int kNormMaxSplit = 8;  // blocks that share a row too long for one
-constexpr uint64_t kNormWaitNs = 4000000000ull;  // bound of the wait for their sums
+constexpr WaitBound kNormWait = wait_bound(4000000000ull);  // bound of the wait for their sums
 
 // two sums to the same words of another block of the cluster, counted on its barrier there (no fence: a release at
 // cluster scope would wait for the row's global stores too)
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
         for (int j = 0; j < R; ++j)
           put_peer(&joined[slot][rank][j], &joined_full[slot], static_cast<int>(threadIdx.x), pq[2 * j], pq[2 * j + 1]);
       }
-      there = ptx::mbar_wait_bounded_cluster(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWaitNs) && there;
+      there = ptx::mbar_wait_bounded_cluster(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWait) && there;
       joined_phase ^= 1u << slot;
 #pragma unroll
       for (int j = 0; j < 2 * R; ++j) pq[j] = 0.0f;

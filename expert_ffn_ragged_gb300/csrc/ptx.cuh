@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "wait_bound.h"
+
 namespace rd {
 namespace ptx {
 
@@ -54,69 +56,63 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Longest a single try_wait may suspend the thread before returning false;
-// without an explicit hint the suspension window is system-defined and can be
-// long enough to hide the bound of the waits below.
-constexpr uint32_t kSuspendHintNs = 1000;
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
       : "memory");
   return done != 0;
 }
 
-// A wait on phase `parity` of an mbarrier that gives up after `limit_ns`
+// A wait on phase `parity` of an mbarrier that gives up after `limit.ns`
 // nanoseconds or as soon as *abort becomes non-zero (another role gave up).
 // On giving up it raises *abort so that every role of the CTA unwinds.
+// A bound shorter than the usual window of a try is its one try's window: however
+// short a wait is, some bound is shorter.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort_flag, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+                                                  volatile int* abort_flag, WaitBound limit) {
+  if (mbar_try_wait(bar, parity, limit.try_ns)) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+  while (limit.try_ns == kSuspendHintNs) {
+    if (mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
-      *abort_flag = 1;
-      return false;
-    }
+    if (global_timer_ns() - t0 > limit.ns) break;
   }
+  *abort_flag = 1;
+  return false;
 }
 
 // try_wait with acquire at cluster scope, for a barrier another CTA of the
 // cluster arrives on with release semantics
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
       : "memory");
   return done != 0;
 }
 
 __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t parity,
-                                                          volatile int* abort_flag,
-                                                          uint64_t limit_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+                                                          volatile int* abort_flag, WaitBound limit) {
+  if (mbar_try_wait_cluster(bar, parity, limit.try_ns)) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
-  while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+  while (limit.try_ns == kSuspendHintNs) {
+    if (mbar_try_wait_cluster(bar, parity, kSuspendHintNs)) return true;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
-      *abort_flag = 1;
-      return false;
-    }
+    if (global_timer_ns() - t0 > limit.ns) break;
   }
+  *abort_flag = 1;
+  return false;
 }
 
 // ---------------------------------------------------------------- clusters

@@ -56,3 +56,40 @@ def test_few_tiles_right_or_reported(rd_lib, which, ot):
         assert bits or torch.equal(bounded, want), limit
         assert torch.equal(again, want), limit
         status.zero_()
+
+
+@pytest.mark.parametrize("ot", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("which", list(FEW_TILES))
+def test_few_tiles_shortest_bound_runs_out(rd_lib, which, ot):
+    """No copy lands within a nanosecond, so a bound of one has to run out and be reported, however short the call."""
+    call = _linear(rd_lib, which, ot, seed=5)
+    status = _i32([0])
+    want = call(None).clone()
+    for _ in range(3):
+        with rd_lib.tuning(wait_timeout_ns=1):
+            call(status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == rd_lib.STATUS_TIMEOUT
+        status.zero_()
+        assert torch.equal(call(status), want) and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("ot", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("variant", ["single", "pair"])
+@pytest.mark.parametrize("m,k,n,sizes", [(1024, 8192, 512, [1024]), (900, 72, 520, [100, 0, 793, 7]), (3000, 1608, 264, [3000, 0])])
+def test_many_tiles_shortest_bound_runs_out(rd_lib, variant, ot, m, k, n, sizes):
+    """The persistent kernel, with stretches of k that wait for one another (f32) and with one short one."""
+    g = torch.Generator().manual_seed(k)
+    x = torch.randn(m, k, generator=g).bfloat16().to(DEV)
+    w = (torch.randn(len(sizes), k, n, generator=g) / math.sqrt(k)).bfloat16().to(DEV)
+    status, gs = _i32([0]), _i32(sizes)
+    with rd_lib.tuning(variant=rd_lib.VARIANT_PAIR if variant == "pair" else rd_lib.VARIANT_SINGLE):
+        want = rd_lib.linear(x, w, group_sizes=gs, out_dtype=ot).clone()
+        for _ in range(3):
+            with rd_lib.tuning(wait_timeout_ns=1):
+                rd_lib.linear(x, w, group_sizes=gs, out_dtype=ot, status=status)
+            torch.cuda.synchronize()
+            assert int(status.item()) == rd_lib.STATUS_TIMEOUT
+            status.zero_()
+            got = rd_lib.linear(x, w, group_sizes=gs, out_dtype=ot, status=status)
+            assert torch.equal(got, want) and int(status.item()) == 0
