@@ -140,6 +140,7 @@ extern "C" rd_status rd_layer_norm_bwd(const void* d_out, int32_t out_dtype, con
   a.d_weight = d_weight;
   a.d_bias = d_bias;
   a.parts = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  a.wait = wait_limit();
   a.limit = limit;
   a.rows = static_cast<int32_t>(rows);
   a.hidden = static_cast<int32_t>(hidden);

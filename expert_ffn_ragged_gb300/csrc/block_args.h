@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/rd_block.h"
+#include "wait_bound.h"
 
 namespace rd {
 
@@ -27,6 +28,7 @@ struct NormArgs {
   int32_t split;         // backward: blocks that share a row too long for one (set by the launcher)
   int32_t split_cols;    // and the columns of each but the last
   float eps;
+  WaitBound wait;        // backward: bound of the waits of blocks that share a row
 };
 
 cudaError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, int out_dtype, int sms,

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long_kernel(const NormArg
 constexpr int kNormCluster = 2;  // blocks that add their sums before they go to the workspace
 
 constexpr int kNormMaxSplit = 8;  // blocks that share a row too long for one
-constexpr WaitBound kNormWait = wait_bound(4000000000ull);  // bound of the wait for their sums
+constexpr uint64_t kNormGraceNs = 200000ull;  // for sums on their way to a block that no longer waits for them
 
 // two sums to the same words of another block of the cluster, counted on its barrier there (no fence: a release at
 // cluster scope would wait for the row's global stores too)
@@ -231,6 +231,22 @@ __device__ __forceinline__ float4 peer_float4(const float4* local, int rank) {
                : "r"(ptx::map_to_rank(ptx::smem_addr(local), static_cast<uint32_t>(rank)))
                : "memory");
   return v;
+}
+
+// A bounded wait for the other blocks' sums.  Its tries have their usual window whatever the bound: read from the
+// arguments, it costs 2 % of the kernel's time (1760 x 65536 in bf16 192 us instead of 188).
+__device__ __forceinline__ bool wait_for_sums(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t limit_ns) {
+  if (ptx::mbar_try_wait_cluster(bar, parity, kSuspendHintNs)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+#pragma unroll 1
+  while (true) {
+    if (ptx::mbar_try_wait_cluster(bar, parity, kSuspendHintNs)) return true;
+    if (*gave_up) return false;
+    if (ptx::global_timer_ns() - t0 > limit_ns) {
+      *gave_up = 1;
+      return false;
+    }
+  }
 }
 
 // SPLIT: a cluster holds a row, each block split_cols (at most kCols) of its columns; the row's two sums cross the cluster
@@ -311,7 +327,9 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
   };
   stats(row);
   uint32_t joined_phase = 0;  // a bit a slot
-  bool there = true;  // SPLIT: no wait has run out
+  // SPLIT: no wait of this thread has run out.  Sums cross a cluster within the window of a try, so with a bound below that
+  // the first block starts as one that has given up, and the others' waits for its sums run out.
+  bool there = rank != 0 || a.wait.try_ns == kSuspendHintNs;
   int stage = 0, slot = 0;
   for (; row < L; row += step) {
     fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
@@ -351,16 +369,18 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     if (++stage == S) stage = 0;
     row_sums<T>(pq, pairs[slot]);
     if (SPLIT) {
-      // Every block's sums to every block.  A slot's words are written again two turns on, by blocks that have this
-      // block's sums of the turn in between, which it sends after it has read the slot.
+      // Every block's sums to every block.  A slot's words are written again two turns on, by threads that have seen this
+      // block's sums of the turn in between, which it sends after it has read the slot.  A thread whose wait has run
+      // out sends no more (it does not know that the others have read theirs): their waits then run out too, and no
+      // element gets another row's sums.
       const uint32_t bar = ptx::smem_addr(&joined_full[slot]);
       if (threadIdx.x == 0 && there) ptx::mbar_arrive_expect_tx(bar, split * R * 8);
-      if (threadIdx.x < split) {
+      if (threadIdx.x < split && there) {
 #pragma unroll
         for (int j = 0; j < R; ++j)
           put_peer(&joined[slot][rank][j], &joined_full[slot], static_cast<int>(threadIdx.x), pq[2 * j], pq[2 * j + 1]);
       }
-      there = ptx::mbar_wait_bounded_cluster(bar, (joined_phase >> slot) & 1u, &gave_up, kNormWait) && there;
+      there = wait_for_sums(bar, (joined_phase >> slot) & 1u, &gave_up, a.wait.ns) && there;
       joined_phase ^= 1u << slot;
 #pragma unroll
       for (int j = 0; j < 2 * R; ++j) pq[j] = 0.0f;
@@ -371,7 +391,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
           pq[2 * j + 1] += joined[slot][i][j].y;
         }
       if (!there) {
-        // a block of the cluster never came: this row and the ones after it show it
+        // a block of the cluster did not come in time: this row and the ones after it show it
 #pragma unroll
         for (int j = 0; j < 2 * R; ++j) pq[j] = __int_as_float(0x7FC00000);
       }
@@ -392,8 +412,13 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, B) layer_norm_bwd_kernel(c
     }
   }
   if (SPLIT) {
-    // a block has all blocks' sums of the last turn by now; after a wait that ran out some may still be on their way to it
+    // Every block has sent its last sums, and has those sent to it, unless one of its waits ran out: then some may still be
+    // on their way to its shared memory.
     ptx::cluster_sync();
+    if (*static_cast<volatile int*>(&gave_up)) {
+      const uint64_t t0 = ptx::global_timer_ns();
+      while (ptx::global_timer_ns() - t0 < kNormGraceNs) __nanosleep(1000);
+    }
     if (a.parts == nullptr) return;
     float* part = a.parts + static_cast<int64_t>(block) * 2 * hidden + col0 + 4 * t;
 #pragma unroll

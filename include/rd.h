@@ -303,8 +303,9 @@ rd_status rd_unsort_bwd_rows(const void* g, const void* y, const float* w, void*
  *                    next band starts, so the band's lhs rows stay in L2);
  *                    0 = the default, 6144.  Rounded down to whole tiles
  *                    (at least one).
- *   wait_timeout_ns  bound of every wait inside the grouped-GEMM kernels;
- *                    0 = the default, 4 s.
+ *   wait_timeout_ns  bound of every wait inside the kernels (the grouped
+ *                    products, rd_linear, and the gradients of long rows in
+ *                    rd_block.h); 0 = the default, 4 s.
  *   reserved         must be 0 (room for later fields).
  *
  * The values apply to calls made after rd_set_tuning returns, from any

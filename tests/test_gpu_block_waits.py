@@ -93,3 +93,27 @@ def test_many_tiles_shortest_bound_runs_out(rd_lib, variant, ot, m, k, n, sizes)
             status.zero_()
             got = rd_lib.linear(x, w, group_sizes=gs, out_dtype=ot, status=status)
             assert torch.equal(got, want) and int(status.item()) == 0
+
+
+# rows shared by two, four and eight blocks, several turns each
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,hidden", [(400, 9000), (250, 20000), (120, 40000), (100, 65536)])
+def test_norm_gradients_of_long_rows(rd_lib, rows, hidden, dt):
+    """Bounds as above: every element of d_x is its own or NaN, all of them NaN with bounds that a block never keeps, the
+    column sums need no other block's, and the call after it is right."""
+    g = torch.Generator().manual_seed(rows)
+    x, d = (torch.randn(rows, hidden, generator=g).to(dt).to(DEV) for _ in range(2))
+    w = torch.randn(hidden, generator=g).to(DEV)
+    f = rd_lib.layer_norm_fwd(x, w)
+    want = [t.clone() for t in rd_lib.layer_norm_bwd(d, x, w, f.mean, f.rstd)]
+    assert bool(torch.isfinite(want[0]).all())
+    for limit in (1, 500, 1500, 3000, 6000, 12000) * 3:
+        with rd_lib.tuning(wait_timeout_ns=limit):
+            got = rd_lib.layer_norm_bwd(d, x, w, f.mean, f.rstd)
+        again = rd_lib.layer_norm_bwd(d, x, w, f.mean, f.rstd)
+        torch.cuda.synchronize()
+        late = torch.isnan(got[0])
+        assert bool(late.all()) or limit >= 1000, limit
+        assert bool(((got[0] == want[0]) | late).all()), limit
+        assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:])), limit
+        assert all(torch.equal(a, b) for a, b in zip(again, want)), limit
