@@ -84,7 +84,7 @@ rd_status rd_layer_norm_bwd_workspace_size(int64_t rows, int64_t hidden, size_t*
  * Accuracy: the products are exact and summed in f32 by the tensor cores, which cut the sum off at every 16 of k;
  * an f32 output adds up stretches of 512 of k with rounding (some 5e-7 of the output's norm, whatever k is).
  * Activations are within 4e-6 + 5e-7 |u| of their value, relatively, u the argument of their exponential (z^2 / 2,
- * 2 sqrt(2 / pi) (z + 0.044715 z^3) or z); values below 1e-37 may be 0.
+ * 2 sqrt(2 / pi) (z + 0.044715 z^3) or z); silu's values below 1.1e-36 and gelu's, in both forms, below 1.2e-37 may be 0.
  * Its gradients: rd_linear_act_bwd gives d_pre and d_bias; dx is rd_ragged_dot_trans_rhs(d_pre, w),
  * dw is rd_trans_ragged_dot(x, d_pre) (one weight: with group_sizes a word that holds m), and the
  * residual's gradient is d_out.
@@ -103,6 +103,8 @@ rd_status rd_linear(const void* x, const void* w, const float* bias, const void*
  *                  where d_bias is not NULL; a group without rows gives 0
  *   Groups as rd_linear: rows of d_pre in [0, L) outside the local groups are +0.
  *   d_out [m, n] of `out_dtype`, pre [m, n] bf16 (NULL with RD_ACT_NONE), d_pre [m, n] bf16, d_bias [g_local, n].
+ *   act'(z) = P + z P' for the activation z P(z); it is within 4e-6 + 5e-7 |u| (as for rd_linear) of |P| + |z P'|, relatively,
+ *   and 0 may stand for what is below 3e-36.
  *   No atomics: the same result on every run.
  *   workspace  device scratch of rd_linear_act_bwd_workspace_size bytes, 32-byte aligned; may be NULL
  *              when d_bias is or that size is 0.  Its contents before and after do not matter.
