@@ -176,8 +176,10 @@ __global__ void __launch_bounds__(kSplitThreads, IsF32<O>::value && BN == 128 ? 
     }
     sh.abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&tmap_x);
-    ptx::prefetch_tmap(&tmap_w);
+    if (a.k > 0) {  // (else there are no maps)
+      ptx::prefetch_tmap(&tmap_x);
+      ptx::prefetch_tmap(&tmap_w);
+    }
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(&sh.tmem_base), kTmem);
