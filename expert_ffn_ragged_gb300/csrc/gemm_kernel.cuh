@@ -107,7 +107,7 @@ struct alignas(128) GemmShared {
   int32_t tile_start[kMaxGroups + 1];  // fwd/dx: first tile of each local group; dw: group order
   uint4 epi[FINE ? 1 : kEpiWarps][32 * 4];  // epilogue staging per warp: 32 rows x 64 bytes
   uint4 zeros[256];                    // 4 KB zero block, the source of the zero-fill copies
-  float4 bias[8 * 32];                 // linear products: 128 (FINE: 64) columns' bias for every epilogue warp
+  float4 bias[FINE ? 1 : 8 * 32];      // linear products: 128 columns' bias for every epilogue warp
 };
 
 template <bool PAIR, bool FINE>
@@ -694,9 +694,11 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
       };
       if (LINEAR) {
         // bias, activation and residual on the f32 sums, of which nothing has been rounded yet; a thread holds a
-        // row.  What they read is asked for before the wait for the sums, or where short rows of x leave the epilogue no rest each
-        // chunk of columns waits for L2 (8192 x 512 x 2048, bias / residual: 33 / 36 us against 21 for neither; now 24 / 32):
-        // the bias to shared memory, the residual's lines to L2 and, in bf16, the first chunk's, then always the next one's, to registers.
+        // row.  With a bf16 output what they read is asked for before the wait for the sums, or where short rows of x leave the
+        // epilogue no rest each chunk of columns waits for L2 (8192 x 512 x 2048, bias / residual: 33 / 36 us against 21 for neither;
+        // now 24 / 32): the bias to shared memory, the residual's lines to L2, the first chunk's, then always the next one's, to registers.
+        // FINE's sixteen warps cover for one another, and hold sums in those registers all the while: there the same costs more
+        // than it gives (16384 x 4096 x 4096, us plain / with both: 363 / 428 with it, 357 / 421 without; 8192 x 512 x 2048 the same).
         const float* bias = args.bias == nullptr
                                 ? nullptr
                                 : args.bias + static_cast<size_t>(tl.j) * args.n_out;
@@ -704,10 +706,10 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
         const bool row_ok = row >= lo && row < hi;
         const size_t row_at = static_cast<size_t>(row_ok ? row : 0) * args.ldo;
         constexpr int kWarpCols = kChunks / kShares * 32;
-        float4* const bias_at = sh.bias + e * (kWarpCols / 4);
+        float4* const bias_at = sh.bias + (FINE ? 0 : e) * (kWarpCols / 4);
         const int wcol0 = col0 + c_begin * 32;  // this warp's first column
         float4 own_bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (bias != nullptr && lane * 4 < kWarpCols && wcol0 + lane * 4 < args.n_out)
+        if (!FINE && bias != nullptr && lane * 4 < kWarpCols && wcol0 + lane * 4 < args.n_out)
           own_bias = __ldg(reinterpret_cast<const float4*>(bias + wcol0) + lane);
         // a chunk of the bf16 residual, 8 rows x 64 contiguous bytes an instruction like the stores (a thread's own row would
         // take 32 lines an instruction)
@@ -721,15 +723,14 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
               next[it] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(row) * args.ldo + c));
           }
         };
-        if (args.residual != nullptr && row_ok) {
-          constexpr int kSize = FINE ? 4 : 2, kLine = 128 / kSize;
-          const char* src = reinterpret_cast<const char*>(args.residual) + (row_at + wcol0) * kSize;
+        if (!FINE && args.residual != nullptr && row_ok) {
+          const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(args.residual) + row_at + wcol0;
 #pragma unroll
-          for (int i = 0; i < kWarpCols; i += kLine)
-            if (wcol0 + i < args.n_out) ptx::prefetch_l2(src + i * kSize);
+          for (int i = 0; i < kWarpCols; i += 64)
+            if (wcol0 + i < args.n_out) ptx::prefetch_l2(src + i);
         }
         if (!FINE && args.residual != nullptr && wcol0 < args.n_out) fetch(wcol0);
-        if (bias != nullptr) {
+        if (!FINE && bias != nullptr) {
           __syncwarp();  // the tile before has been read
           if (lane * 4 < kWarpCols) bias_at[lane] = own_bias;
           __syncwarp();
@@ -738,7 +739,8 @@ __global__ void __launch_bounds__(TileCfg<PAIR, EPI == kEpiLinearF32>::kThreadsN
           if (bias != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 b4 = bias_at[(col - wcol0) / 4 + i];
+              if (FINE && col + 4 * i + 4 > args.n_out) continue;
+              const float4 b4 = FINE ? __ldg(reinterpret_cast<const float4*>(bias + col) + i) : bias_at[(col - wcol0) / 4 + i];
               v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + b4.x);
               v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + b4.y);
               v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + b4.z);
