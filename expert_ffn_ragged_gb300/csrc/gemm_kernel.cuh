@@ -44,7 +44,7 @@
 //     apply it and add the residual, all in f32 on the accumulator.  An f32 output is kept as exact as a rounded f32 sum:
 //     the tensor core cuts its sums off after every step of 16 along k (4.3e-6 of the result's norm at k = 4096), so
 //     the two accumulators take turns every 512 of k and 16 epilogue warps add the complete one to sums in
-//     registers (4.7e-7; 16384 x 4096 x 4096: 365 us against 287 for bf16, which rounds far coarser anyway);
+//     registers (4.7e-7; 16384 x 4096 x 4096: 359 us against 287 for bf16, which rounds far coarser anyway);
 //   * every wait is bounded; on expiry the CTA unwinds, drains its TMA and
 //     MMA work, frees TMEM and reports RD_STATUS_TIMEOUT.
 #pragma once

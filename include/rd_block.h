@@ -50,7 +50,7 @@ rd_status rd_layer_norm_fwd(const void* x, int32_t dtype, const float* weight, c
  *   workspace  device scratch of rd_layer_norm_bwd_workspace_size bytes, 32-byte aligned; may be
  *              NULL when both d_weight and d_bias are, or that size is 0.  Its contents before and
  *              after do not matter.
- * Rows longer than 8192 are shared by blocks that wait for one another's sums, each wait bounded as those of rd.h are
+ * Rows of 8200 to 65536 elements are shared by blocks that wait for one another's sums, each wait bounded as those of rd.h are
  * (rd_set_tuning's wait_timeout_ns).  There is no status word: where a wait runs out, d_x is NaN from the row it was for
  * on, in that block's columns of the rows that it takes, and soon in those of the blocks that share them; every other
  * element of d_x, d_weight and d_bias is what it would be otherwise.
