@@ -19,6 +19,7 @@ namespace {
 
 constexpr size_t kWorkspaceBytesPerSm = 2048;   // size of a dw workspace
 constexpr uint64_t kTimeoutNs = 4000000000ull;  // default bound of any single wait in a kernel
+constexpr uint64_t kLongestWaitNs = 1ull << 62;
 
 // Process-wide tuning overrides (rd_set_tuning); 0 = the default.
 std::atomic<int32_t> g_variant{RD_VARIANT_AUTO};
@@ -48,7 +49,8 @@ EncodeTiledFn encode_fn() {
 
 WaitBound wait_limit() {
   const uint64_t t = g_timeout_ns.load(std::memory_order_relaxed);
-  return wait_bound(t == 0 ? kTimeoutNs : t);
+  // (cut off where twice a bound, which some waits take, would leave 64 bits)
+  return wait_bound(t == 0 ? kTimeoutNs : (t < kLongestWaitNs ? t : kLongestWaitNs));
 }
 
 rd_status current_device(int* sms) {

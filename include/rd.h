@@ -305,7 +305,9 @@ rd_status rd_unsort_bwd_rows(const void* g, const void* y, const float* w, void*
  *                    (at least one).
  *   wait_timeout_ns  bound of every wait inside the kernels (the grouped
  *                    products, rd_linear, and the gradients of long rows in
- *                    rd_block.h); 0 = the default, 4 s.
+ *                    rd_block.h); 0 = the default, 4 s.  Bounds below a
+ *                    microsecond are for tests of a wait that runs out: no
+ *                    copy from memory keeps them.
  *   reserved         must be 0 (room for later fields).
  *
  * The values apply to calls made after rd_set_tuning returns, from any

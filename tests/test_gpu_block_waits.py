@@ -117,3 +117,20 @@ def test_norm_gradients_of_long_rows(rd_lib, rows, hidden, dt):
         assert bool(((got[0] == want[0]) | late).all()), limit
         assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:])), limit
         assert all(torch.equal(a, b) for a, b in zip(again, want)), limit
+
+
+@pytest.mark.parametrize("limit", [2 ** 63 - 500_000_000, 2 ** 63, 2 ** 64 - 1])
+def test_longest_bounds(rd_lib, limit):
+    """A wait that takes twice the bound and a second more does not run out early where that leaves 64 bits."""
+    status = _i32([0])
+    for which in FEW_TILES:
+        call = _linear(rd_lib, which, torch.float32, seed=9)
+        want = call(None).clone()
+        with rd_lib.tuning(wait_timeout_ns=limit):
+            assert rd_lib.get_tuning()["wait_timeout_ns"] == limit
+            assert torch.equal(call(status), want)
+    x = torch.randn(100, 20000, device=DEV)
+    f = rd_lib.layer_norm_fwd(x)
+    with rd_lib.tuning(wait_timeout_ns=limit):
+        assert bool(torch.isfinite(rd_lib.layer_norm_bwd(x, x, None, f.mean, f.rstd)[0]).all())
+    assert int(status.item()) == 0
