@@ -322,7 +322,7 @@ constexpr int kFewUnits = 64;  // of 128 columns and a group
 
 // Whether a block takes a whole group: groups enough for all SMs, at most 2048 rows of all of them, or few rows (us whole / shares, gelu: 8 x 136
 // 2.5 / 4.0, 200 x 4096 5.0 / 5.5, 32 x 136 in 64 groups 2.9 / 12, 509 x 1024 in 16 4.6 / 6.2, 1024 x 1024 in 4 6.1 / 6.8, but 509 x 1024 6.5 /
-// 4.8, 2000 x 4096 in 4 16 / 14).  These are even groups, of which alone the host knows.  With all rows in one of them, that group's blocks have
+// 4.8, 2000 x 4096 in 4 16 / 14).  The host does not know the groups' rows: these are even groups.  With all rows in one of them, its blocks have
 // all of the work (us even / all in one / as one weight, by shares; inputs in L2: 2048 x 1024 in 64 5.5 / 50 / 6.8, 2048 x 4096 in 16 12 / 66 / 12,
 // 1000 x 1024 in 4 5.2 / 11 / 5.7, 1024 x 14336 in 8 20 / 21 / 18): 2048 rows are the bound of that.
 bool whole_groups(int64_t m, int64_t n, int32_t g_local) {

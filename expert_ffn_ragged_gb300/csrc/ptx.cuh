@@ -71,8 +71,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity, uin
 // A wait on phase `parity` of an mbarrier that gives up after `limit.ns`
 // nanoseconds or as soon as *abort becomes non-zero (another role gave up).
 // On giving up it raises *abort so that every role of the CTA unwinds.
-// A bound shorter than the usual window of a try is its one try's window: however
-// short a wait is, some bound is shorter.
+// A bound shorter than the usual window of a try is its one try's window (which the
+// hardware keeps to within some hundred nanoseconds: copies from memory take longer).
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   volatile int* abort_flag, WaitBound limit) {
   if (mbar_try_wait(bar, parity, limit.try_ns)) return true;
